@@ -55,6 +55,7 @@ extern "C" {
 #define PKV_DEV_BAD_BLOCK 2        /* block_table entry outside [0, num_blocks)      */
 #define PKV_DEV_BAD_LENGTH 4       /* length > max_blocks_per_seq * block_size, < 0  */
 #define PKV_DEV_TIMEOUT 8          /* a bounded wait inside a kernel gave up         */
+#define PKV_DEV_BAD_POSITION 16    /* rotary position outside [0, max_pos)           */
 
 #define PKV_BF16 0
 #define PKV_F32 1
@@ -267,6 +268,41 @@ int pkv_mla_rmsnorm_rope_write(void* cache_nope, void* cache_rope, void* k_nope_
                                int32_t kv_lora_rank, int32_t rope_dim, float epsilon,
                                int* dev_status, void* stream);
 
+/* Fused rotary embedding and cache write for GQA / MHA caches, with positions of one
+ * or several axes (the Llama forward's RoPE, "KV Cache 笔记", and its write through
+ * slot_mapping in one pass; several axes serve image and video tokens, whose time,
+ * height and width turn different pairs of a head). For token t, each q and k head x
+ * and pair i < rope_dim / 2, with p = positions[pair_axis[i]][t]:
+ *   c = rope_table[p][i], s = rope_table[p][rope_dim / 2 + i]
+ *   (x1, x2) -> (x1 c - x2 s, x2 c + x1 s)
+ * x1, x2 are elements i and i + rope_dim / 2 (interleaved = 0: rotate_half) or 2i and
+ * 2i + 1 (interleaved = 1); elements from rope_dim on are copied. fp32 arithmetic, one
+ * rounding to nearest even. The rotated q row goes to q_out[t], the rotated k row and
+ * the v row to cache row slot_mapping[t].
+ *   k_cache, v_cache [num_blocks, block_size, H_kv, head_dim] bf16
+ *   q, q_out [T, H, head_dim], k, v [T, H_kv, head_dim] bf16; *_stride: elements from
+ *     one token to the next (a multiple of 8; heads of a token are contiguous), so q, k
+ *     and v can be slices of one projection's output
+ *   rope_table [max_pos, rope_dim] fp32: rope_dim / 2 cosines, then the sines
+ *   positions [num_axes, T] int32; pair_axis: HOST array of rope_dim / 2 entries in
+ *     [0, num_axes), or NULL (every pair axis 0)
+ *   slot_mapping [T] int32: a negative slot skips the cache write of the row (q_out is
+ *     still written); a slot >= num_blocks * block_size also sets PKV_DEV_BAD_SLOT.
+ * A token with a position outside [0, max_pos) on any axis is skipped altogether and
+ * sets PKV_DEV_BAD_POSITION. q_out may be q itself (same pointer and stride); any other
+ * overlap of q_out's rows with those of q, k or v is refused (PKV_ERR_INVALID_ARG).
+ * Supported: head_dim a multiple of 16 up to 256, rope_dim a multiple of 16 up to
+ * head_dim, num_axes 1..4 (PKV_ERR_UNSUPPORTED otherwise). All pointers 16-byte aligned
+ * (positions and slot_mapping 4). Duplicate slots as for pkv_kv_cache_write. */
+int pkv_rope_kv_cache_write(void* k_cache, void* v_cache, void* q_out, int64_t q_out_stride,
+                            const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const float* rope_table,
+                            int64_t max_pos, int32_t rope_dim, const int32_t* positions,
+                            int32_t num_axes, const int32_t* pair_axis, int32_t interleaved,
+                            const int32_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,
+                            int32_t block_size, int32_t H, int32_t H_kv, int32_t head_dim,
+                            int* dev_status, void* stream);
+
 /* Decode attention, one query token per sequence (sparse_mode 0 / band 4).
  * For each b, h: o = softmax(scale * q[b,h] . K^T) V over positions
  * [max(0, len_b - window), len_b) (window <= 0: [0, len_b)) of sequence b, read
@@ -419,6 +455,28 @@ int pkv_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, float* 
                            const void* k, const void* v, const int32_t* slot_mapping,
                            int64_t num_tokens, int64_t num_blocks, int32_t block_size,
                            int32_t num_kv_heads, int32_t head_dim, int* dev_status, void* stream);
+/* pkv_rope_kv_cache_write into an FP8 cache: the rotated k row (fp32, not rounded to
+ * bf16 first) and the v row are quantised as above. head_dim must be 128
+ * (PKV_ERR_UNSUPPORTED); scales 4-byte aligned. */
+int pkv_rope_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                void* q_out, int64_t q_out_stride, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const float* rope_table, int64_t max_pos,
+                                int32_t rope_dim, const int32_t* positions, int32_t num_axes,
+                                const int32_t* pair_axis, int32_t interleaved,
+                                const int32_t* slot_mapping, int64_t num_tokens,
+                                int64_t num_blocks, int32_t block_size, int32_t H, int32_t H_kv,
+                                int32_t head_dim, int* dev_status, void* stream);
+/* Rows of an FP8 cache widened to bf16: k[t], v[t] = code * scale of cache row
+ * slot_mapping[t] (one fp32 product, rounded to nearest even), the way a quantised
+ * prefix reaches pkv_paged_attention_prefill, which reads bf16 caches. A negative slot
+ * gives a row of zeros, a slot >= num_blocks * block_size too and sets
+ * PKV_DEV_BAD_SLOT. k, v [num_tokens, H_kv, head_dim] bf16; head_dim must be 128
+ * (PKV_ERR_UNSUPPORTED). Rows and caches 16-byte aligned, scales 4. */
+int pkv_kv_cache_read_fp8(void* k, void* v, const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale, const int32_t* slot_mapping,
+                          int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                          int32_t num_kv_heads, int32_t head_dim, int* dev_status, void* stream);
 /* pkv_paged_attention_decode over an FP8 cache: same arguments, result, workspace
  * (pkv_decode_workspace_size) and error behaviour, plus the two scale arrays
  * (16-byte aligned). The attention is that of the dequantised cache; q stays bf16.

@@ -44,6 +44,14 @@ SIGNATURES = {
                                                  vp]),
     "pkv_mla_rmsnorm_rope_write": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32,
                                              i32, f32, vp, vp]),
+    "pkv_rope_kv_cache_write": (C.c_int, [vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32,
+                                          vp, i32, vp, i32, vp, i64, i64, i32, i32, i32, i32, vp,
+                                          vp]),
+    "pkv_rope_kv_cache_write_fp8": (C.c_int, [vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, i64,
+                                              vp, i64, i32, vp, i32, vp, i32, vp, i64, i64, i32,
+                                              i32, i32, i32, vp, vp]),
+    "pkv_kv_cache_read_fp8": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, vp,
+                                        vp]),
     "pkv_num_skipped_tokens": (i64, [i64, i64]),
     "pkv_build_block_table": (C.c_int, [vp, vp, i32, i32, i32, i32, vp]),
     "pkv_build_block_table_arange": (C.c_int, [i32, i32, vp]),

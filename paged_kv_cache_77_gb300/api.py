@@ -496,6 +496,143 @@ def kv_cache_write_fp8(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, d
           "pkv_kv_cache_write_fp8")
 
 
+def _rope_rows(t, T, d, name):
+    """Token stride of rows [T, heads, d]: bf16 on the GPU, the heads of a token contiguous,
+    tokens any multiple of 8 elements apart (a slice of a projection's output will do)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+        raise ValueError(f"{name} has shape {_shape_str(t.shape)}, expected [{T}, heads, {d}]")
+    heads = t.shape[1]
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st[0] if T > 1 else heads * d
+
+
+def _axis_array(pair_axis, rope_dim):
+    """pair_axis as the int32 host array the library reads (None: NULL, every pair axis 0)."""
+    if pair_axis is None:
+        return None
+    arr = np.ascontiguousarray(pair_axis, dtype=np.int32)
+    if arr.shape != (rope_dim // 2,):
+        raise ValueError(f"pair_axis must have rope_dim / 2 = {rope_dim // 2} entries")
+    return arr
+
+
+def _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions, slot_mapping, pair_axis, q_out,
+                 dev_status):
+    """Checks shared by the two rotary writes; returns q_out and the C arguments from q_out
+    to slot_mapping's sizes (the caches go in front, dev_status and the stream behind)."""
+    nb, bs, hkv, d = _cache_dims(k_cache, "k_cache")
+    check_shape(v_cache, (nb, bs, hkv, d), "v_cache")
+    _dev_i32(slot_mapping, "slot_mapping")
+    T = slot_mapping.numel()
+    qs, ks, vs = _rope_rows(q, T, d, "q"), _rope_rows(k, T, d, "k"), _rope_rows(v, T, d, "v")
+    H = q.shape[1]
+    if k.shape[1] != hkv or v.shape[1] != hkv:
+        raise ValueError(f"k and v must have the cache's {hkv} heads")
+    _f32_dev(rope_table, "rope_table")
+    if rope_table.dim() != 2:
+        raise ValueError("rope_table must be [max_pos, rope_dim]")
+    max_pos, rope_dim = rope_table.shape
+    _dev_i32(positions, "positions")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.shape != ((T,) if positions.dim() == 1 else (axes, T)):
+        raise ValueError(f"positions must be [T={T}] or [axes, T={T}], "
+                         f"got {_shape_str(positions.shape)}")
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+    else:
+        if not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    qos = _rope_rows(q_out, T, d, "q_out")
+    dev = k_cache.device
+    check_same_device(dev, v_cache=v_cache, q=q, k=k, v=v, rope_table=rope_table,
+                      positions=positions, slot_mapping=slot_mapping, q_out=q_out)
+    check_current_device(dev)
+    status_buffer(dev_status, dev)
+    arr = _axis_array(pair_axis, rope_dim)
+    args = (_ptr(q_out), qos, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(rope_table), max_pos,
+            rope_dim, _ptr(positions), axes, None if arr is None else _np_ptr(arr))
+    sizes = (_ptr(slot_mapping), T, nb, bs, H, hkv, d, _ptr(dev_status))
+    return q_out, args, sizes, arr
+
+
+def rope_kv_cache_write(k_cache, v_cache, q, k, v, rope_table, positions, slot_mapping,
+                        pair_axis=None, interleaved: bool = False, q_out=None, dev_status=None,
+                        stream=None):
+    """Rotary embedding of new q and k rows and the write of k and v into the paged caches.
+
+    q [T, H, d], k, v [T, H_kv, d] bf16 (slices of one projection's output will do);
+    rope_table [max_pos, rope_dim] fp32, rope_dim / 2 cosines then the sines per position;
+    positions [T] or [axes, T] int32, pair_axis the axis of each of the rope_dim / 2 pairs
+    (None: all axis 0); `interleaved` pairs elements 2i and 2i + 1 instead of i and
+    i + rope_dim / 2. Returns the rotated q (`q_out`, which may be q itself)."""
+    _dev_bf16(k_cache, "k_cache")
+    _dev_bf16(v_cache, "v_cache")
+    q_out, args, sizes, _keep = _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions,
+                                             slot_mapping, pair_axis, q_out, dev_status)
+    check(load().pkv_rope_kv_cache_write(_ptr(k_cache), _ptr(v_cache), *args, int(bool(interleaved)),
+                                         *sizes, _stream(stream)), "pkv_rope_kv_cache_write")
+    return q_out
+
+
+def rope_kv_cache_write_fp8(k_cache, v_cache, k_scale, v_scale, q, k, v, rope_table, positions,
+                            slot_mapping, pair_axis=None, interleaved: bool = False, q_out=None,
+                            dev_status=None, stream=None):
+    """rope_kv_cache_write into an FP8 cache (codes + per-row scales): the rotated k rows and
+    the v rows are quantised from their fp32 values. Returns the rotated q in bf16."""
+    _fp8_cache(k_cache, "k_cache")
+    _fp8_cache(v_cache, "v_cache")
+    _f32_dev(k_scale, "k_scale")
+    _f32_dev(v_scale, "v_scale")
+    q_out, args, sizes, _keep = _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions,
+                                             slot_mapping, pair_axis, q_out, dev_status)
+    nb, bs, hkv, _ = k_cache.shape
+    check_shape(k_scale, (nb, hkv, bs), "k_scale")
+    check_shape(v_scale, (nb, hkv, bs), "v_scale")
+    check_same_device(k_cache.device, k_scale=k_scale, v_scale=v_scale)
+    check(load().pkv_rope_kv_cache_write_fp8(
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), *args, int(bool(interleaved)),
+        *sizes, _stream(stream)), "pkv_rope_kv_cache_write_fp8")
+    return q_out
+
+
+def kv_cache_read_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=None, v_out=None,
+                      dev_status=None, stream=None):
+    """Rows of an FP8 cache widened to bf16: returns (k, v), [T, H_kv, d] each (`k_out` and
+    `v_out` if given). A negative slot gives a row of zeros."""
+    _fp8_cache(k_cache, "k_cache")
+    _fp8_cache(v_cache, "v_cache")
+    _f32_dev(k_scale, "k_scale")
+    _f32_dev(v_scale, "v_scale")
+    _dev_i32(slot_mapping, "slot_mapping")
+    nb, bs, hkv, d = _cache_dims(k_cache, "k_cache")
+    check_shape(v_cache, (nb, bs, hkv, d), "v_cache")
+    check_shape(k_scale, (nb, hkv, bs), "k_scale")
+    check_shape(v_scale, (nb, hkv, bs), "v_scale")
+    T = slot_mapping.numel()
+    dev = k_cache.device
+    outs = []
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=dev)
+        _dev_bf16(t, n)
+        check_shape(t, (T, hkv, d), n)
+        outs.append(t)
+    k_out, v_out = outs
+    check_same_device(dev, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                      slot_mapping=slot_mapping, k_out=k_out, v_out=v_out)
+    check_current_device(dev)
+    status_buffer(dev_status, dev)
+    check(load().pkv_kv_cache_read_fp8(_ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache),
+                                       _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping), T, nb, bs,
+                                       hkv, d, _ptr(dev_status), _stream(stream)),
+          "pkv_kv_cache_read_fp8")
+    return k_out, v_out
+
+
 def paged_attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
                                scale: float, window: int = 0, out=None, lse=None,
                                out_dtype=torch.float32, workspace=None, dev_status=None,
@@ -743,6 +880,7 @@ def paged_attention_decode_static(q, k_cache, v_cache, block_table, seq_lens, sc
 
 
 DEV_TIMEOUT = 8  # PKV_DEV_TIMEOUT: a bounded wait inside a kernel gave up
+DEV_BAD_POSITION = 16  # PKV_DEV_BAD_POSITION: a rotary position outside the table
 
 
 def selftest_bounded_wait(dev_status, stream=None) -> None:

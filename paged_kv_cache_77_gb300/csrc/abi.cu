@@ -267,6 +267,173 @@ int pkv_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, float* 
                        "pkv_kv_cache_write_fp8");
 }
 
+}  // extern "C"
+
+namespace {
+
+// Whether rows of `width` elements at a + t * a_stride and b + t * b_stride (t < tokens, 2-byte
+// elements) can share an element. Rows that run through one buffer at a common stride, as
+// slices of a projection's output do, are apart when their columns are.
+bool rows_overlap(const void* a, int64_t a_stride, int64_t a_width, const void* b, int64_t b_stride,
+                  int64_t b_width, int64_t tokens) {
+  const int64_t pa = (int64_t)((uintptr_t)a / 2), pb = (int64_t)((uintptr_t)b / 2);
+  const int64_t end_a = pa + (tokens - 1) * a_stride + a_width;
+  const int64_t end_b = pb + (tokens - 1) * b_stride + b_width;
+  if (end_a <= pb || end_b <= pa) return false;
+  if (a_stride != b_stride || a_stride <= 0) return true;
+  const int64_t off = (((pb - pa) % a_stride) + a_stride) % a_stride;  // b's first column after a's
+  return !(off >= a_width && off + b_width <= a_stride);
+}
+
+// Validation and argument set-up shared by the two rotary writes.
+int rope_setup(pkv::RopeArgs& a, const char* what, void* k_cache, void* v_cache, void* q_out,
+               int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+               int64_t k_stride, const void* v, int64_t v_stride, const float* rope_table,
+               int64_t max_pos, int32_t rope_dim, const int32_t* positions, int32_t num_axes,
+               const int32_t* pair_axis, const int32_t* slot_mapping, int64_t num_tokens,
+               int64_t num_blocks, int32_t block_size, int32_t H, int32_t H_kv, int32_t head_dim,
+               int* dev_status) {
+  using namespace pkv;
+  PKV_REQUIRE(num_tokens >= 0 && num_blocks > 0 && block_size > 0 && H > 0 && H_kv > 0 &&
+                  head_dim > 0 && rope_dim > 0 && max_pos > 0,
+              PKV_ERR_INVALID_ARG, "%s: non-positive size", what);
+  PKV_REQUIRE(head_dim % 16 == 0 && head_dim <= kRopeMaxDim, PKV_ERR_UNSUPPORTED,
+              "%s: head_dim must be a multiple of 16 up to %d", what, kRopeMaxDim);
+  PKV_REQUIRE(rope_dim % 16 == 0 && rope_dim <= head_dim, PKV_ERR_UNSUPPORTED,
+              "%s: rope_dim must be a multiple of 16 up to head_dim", what);
+  PKV_REQUIRE(num_axes >= 1 && num_axes <= kRopeMaxAxes, PKV_ERR_UNSUPPORTED,
+              "%s: 1 to %d position axes are implemented", what, kRopeMaxAxes);
+  // The kernel counts the heads of a token in 32 bits, and a row's elements from them.
+  PKV_REQUIRE((int64_t)H + 2 * (int64_t)H_kv <= (1 << 20), PKV_ERR_UNSUPPORTED,
+              "%s: too many heads", what);
+  PKV_REQUIRE(num_blocks * block_size <= INT32_MAX, PKV_ERR_UNSUPPORTED,
+              "%s: num_blocks * block_size must fit in int32", what);
+  PKV_REQUIRE(k_cache && v_cache && rope_table &&
+                  (num_tokens == 0 || (q && k && v && q_out && positions && slot_mapping)),
+              PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+  PKV_REQUIRE(aligned16(k_cache) && aligned16(v_cache) && aligned16(q) && aligned16(k) &&
+                  aligned16(v) && aligned16(q_out) && aligned16(rope_table),
+              PKV_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
+  const int64_t q_width = (int64_t)H * head_dim, kv_width = (int64_t)H_kv * head_dim;
+  PKV_REQUIRE(q_stride >= 0 && k_stride >= 0 && v_stride >= 0 && q_stride % 8 == 0 &&
+                  k_stride % 8 == 0 && v_stride % 8 == 0 && q_out_stride % 8 == 0 &&
+                  (num_tokens <= 1 || q_out_stride >= q_width),
+              PKV_ERR_INVALID_ARG, "%s: bad token stride", what);
+  if (num_tokens > 0) {
+    const bool in_place = q_out == q && (q_out_stride == q_stride || num_tokens == 1);
+    PKV_REQUIRE((in_place ||
+                 !rows_overlap(q_out, q_out_stride, q_width, q, q_stride, q_width, num_tokens)) &&
+                    !rows_overlap(q_out, q_out_stride, q_width, k, k_stride, kv_width, num_tokens) &&
+                    !rows_overlap(q_out, q_out_stride, q_width, v, v_stride, kv_width, num_tokens),
+                PKV_ERR_INVALID_ARG, "%s: q_out overlaps q, k or v", what);
+  }
+  a = RopeArgs{};
+  for (int i = 0; i < rope_dim / 2; ++i) {
+    const int32_t axis = pair_axis ? pair_axis[i] : 0;
+    PKV_REQUIRE(axis >= 0 && axis < num_axes, PKV_ERR_INVALID_ARG,
+                "%s: pair_axis[%d] = %d outside the %d axes", what, i, axis, num_axes);
+    a.pair_axis[i] = (uint8_t)axis;
+    a.chunk_axis[i / 8] = (i % 8 == 0 || a.chunk_axis[i / 8] == axis) ? (int8_t)axis : (int8_t)-1;
+  }
+  a.q = (const uint16_t*)q;
+  a.k = (const uint16_t*)k;
+  a.v = (const uint16_t*)v;
+  a.q_out = (uint16_t*)q_out;
+  a.k_cache = (uint8_t*)k_cache;
+  a.v_cache = (uint8_t*)v_cache;
+  a.table = rope_table;
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.dev_status = dev_status;
+  a.num_tokens = num_tokens;
+  a.num_slots = num_blocks * block_size;
+  a.max_pos = max_pos;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out_stride = q_out_stride;
+  a.H = H;
+  a.Hkv = H_kv;
+  a.head_dim = head_dim;
+  a.rope_dim = rope_dim;
+  a.num_axes = num_axes;
+  a.block_size = block_size;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_rope_kv_cache_write(void* k_cache, void* v_cache, void* q_out, int64_t q_out_stride,
+                            const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const float* rope_table,
+                            int64_t max_pos, int32_t rope_dim, const int32_t* positions,
+                            int32_t num_axes, const int32_t* pair_axis, int32_t interleaved,
+                            const int32_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,
+                            int32_t block_size, int32_t H, int32_t H_kv, int32_t head_dim,
+                            int* dev_status, void* stream) {
+  RopeArgs a;
+  const int rc = rope_setup(a, "pkv_rope_kv_cache_write", k_cache, v_cache, q_out, q_out_stride, q,
+                            q_stride, k, k_stride, v, v_stride, rope_table, max_pos, rope_dim,
+                            positions, num_axes, pair_axis, slot_mapping, num_tokens, num_blocks,
+                            block_size, H, H_kv, head_dim, dev_status);
+  if (rc != PKV_OK) return rc;
+  clear_error();
+  return launch_status(launch_rope_write(a, false, interleaved != 0, (cudaStream_t)stream,
+                                         current_num_sms()),
+                       "pkv_rope_kv_cache_write");
+}
+
+int pkv_rope_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                void* q_out, int64_t q_out_stride, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const float* rope_table, int64_t max_pos,
+                                int32_t rope_dim, const int32_t* positions, int32_t num_axes,
+                                const int32_t* pair_axis, int32_t interleaved,
+                                const int32_t* slot_mapping, int64_t num_tokens,
+                                int64_t num_blocks, int32_t block_size, int32_t H, int32_t H_kv,
+                                int32_t head_dim, int* dev_status, void* stream) {
+  PKV_REQUIRE(head_dim == 128, PKV_ERR_UNSUPPORTED,
+              "pkv_rope_kv_cache_write_fp8: only head_dim 128 is implemented");
+  RopeArgs a;
+  const int rc = rope_setup(a, "pkv_rope_kv_cache_write_fp8", k_cache, v_cache, q_out, q_out_stride,
+                            q, q_stride, k, k_stride, v, v_stride, rope_table, max_pos, rope_dim,
+                            positions, num_axes, pair_axis, slot_mapping, num_tokens, num_blocks,
+                            block_size, H, H_kv, head_dim, dev_status);
+  if (rc != PKV_OK) return rc;
+  PKV_REQUIRE(k_scale && v_scale && (((uintptr_t)k_scale) & 3) == 0 &&
+                  (((uintptr_t)v_scale) & 3) == 0,
+              PKV_ERR_INVALID_ARG,
+              "pkv_rope_kv_cache_write_fp8: scale arrays must be set and 4-byte aligned");
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  clear_error();
+  return launch_status(launch_rope_write(a, true, interleaved != 0, (cudaStream_t)stream,
+                                         current_num_sms()),
+                       "pkv_rope_kv_cache_write_fp8");
+}
+
+int pkv_kv_cache_read_fp8(void* k, void* v, const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale, const int32_t* slot_mapping,
+                          int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                          int32_t num_kv_heads, int32_t head_dim, int* dev_status, void* stream) {
+  PKV_REQUIRE(num_tokens >= 0 && num_blocks > 0 && block_size > 0 && num_kv_heads > 0,
+              PKV_ERR_INVALID_ARG, "pkv_kv_cache_read_fp8: bad sizes");
+  PKV_REQUIRE(head_dim == 128, PKV_ERR_UNSUPPORTED,
+              "pkv_kv_cache_read_fp8: only head_dim 128 is implemented");
+  PKV_REQUIRE(k_cache && v_cache && k_scale && v_scale && (num_tokens == 0 || (k && v && slot_mapping)),
+              PKV_ERR_INVALID_ARG, "pkv_kv_cache_read_fp8: null pointer");
+  PKV_REQUIRE(aligned16(k_cache) && aligned16(v_cache) && aligned16(k) && aligned16(v) &&
+                  (((uintptr_t)k_scale) & 3) == 0 && (((uintptr_t)v_scale) & 3) == 0,
+              PKV_ERR_INVALID_ARG, "pkv_kv_cache_read_fp8: misaligned pointer");
+  clear_error();
+  return launch_status(launch_kv_read_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping,
+                                          num_tokens, num_blocks, block_size, num_kv_heads,
+                                          dev_status, (cudaStream_t)stream, current_num_sms()),
+                       "pkv_kv_cache_read_fp8");
+}
+
 int pkv_paged_attention_decode_fp8(void* out, int32_t out_dtype, float* lse, const void* q,
                                    const void* k_cache, const void* v_cache, const float* k_scale,
                                    const float* v_scale, const int32_t* block_table,

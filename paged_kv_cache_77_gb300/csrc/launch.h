@@ -24,6 +24,33 @@ cudaError_t launch_mla_rmsnorm_rope_write(void* cache_nope, void* cache_rope, vo
                                           int64_t num_slots, float eps, int* dev_status,
                                           cudaStream_t stream, int num_sms);
 
+// Arguments of the fused rotary embedding + paged write (rope_write.cu). Strides are in
+// elements, between tokens; the heads of a token are contiguous.
+constexpr int kRopeMaxAxes = 4;
+constexpr int kRopeMaxDim = 256;
+struct RopeArgs {
+  const uint16_t *q, *k, *v;   // [T, H, d], [T, Hkv, d], [T, Hkv, d] bf16
+  uint16_t* q_out;             // [T, H, d] bf16
+  uint8_t *k_cache, *v_cache;  // [nb, bs, Hkv, d] bf16, or E4M3 codes
+  float *k_scale, *v_scale;    // FP8 cache only: [nb, Hkv, bs]
+  const float* table;          // [max_pos, rope_dim]: cosines, then sines
+  const int32_t* positions;    // [num_axes, T]
+  const int32_t* slots;        // [T]
+  int* dev_status;
+  int64_t num_tokens, num_slots, max_pos;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int H, Hkv, head_dim, rope_dim, num_axes, block_size;
+  uint8_t pair_axis[kRopeMaxDim / 2];   // position axis of each pair
+  int8_t chunk_axis[kRopeMaxDim / 16];  // axis of 8 pairs at a time, -1 where they differ
+};
+cudaError_t launch_rope_write(const RopeArgs& a, bool fp8, bool interleaved, cudaStream_t stream,
+                              int num_sms);
+// Rows of an FP8 cache widened to bf16 (kv_write.cu).
+cudaError_t launch_kv_read_fp8(void* k, void* v, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, const int32_t* slots,
+                               int64_t num_tokens, int64_t num_blocks, int block_size, int hkv,
+                               int* dev_status, cudaStream_t stream, int num_sms);
+
 // Arguments of the split-KV decode kernels and their LSE merge.
 struct DecodeArgs {
   const uint16_t* q;          // [B, q_len, H, D] bf16

@@ -1,0 +1,255 @@
+// Rotary embedding of new q and k rows fused with the paged write of k and v, for
+// positions with one or several axes (time, height, width), into a bf16 or an FP8 cache.
+//
+// Pair i of a head (i < rope_dim / 2) turns by the angle of position p = positions[axis(i)][t],
+// whose cosine and sine are c = table[p][i], s = table[p][rope_dim / 2 + i]:
+//
+//   (x1, x2) -> (x1 c - x2 s, x2 c + x1 s)
+//
+// with x1, x2 the elements i and i + rope_dim / 2 (the rotate_half form the pages print for
+// the Llama forward, "KV Cache 笔记") or 2i and 2i + 1. Elements from rope_dim on pass
+// through. fp32 arithmetic and one rounding: to bf16, or (FP8 cache) to E4M3 of the fp32
+// value over the row's scale, amax / 448. Angles come from the caller's table, so far
+// positions cost no accuracy here.
+//
+// Layout: a lane holds 16 elements of one head, either 8 whole pairs (two 16-byte vectors,
+// which are rope_dim / 2 apart or neighbours) or 16 elements that pass through, so a
+// head_dim of 128 takes 8 lanes and a warp 4 heads. The cosines and sines of a lane's 8
+// pairs are the same for every head of a token: they are loaded once and used for the q,
+// k and v heads of the warp's share (kUnroll passes of 4 heads; every load of the share is
+// issued before any arithmetic). Elements are read and written by the same thread, so q
+// may be rotated in place.
+//
+// Roofline: HBM. Algorithmic bytes per token = 2 (q) + 2 (k, v to bf16; 1.5 to FP8) times
+// the rows' bytes, the table row and 4 bytes of slot and of each position.
+#include <cuda_fp8.h>
+
+#include "device_common.cuh"
+#include "launch.h"
+
+namespace pkv {
+
+namespace {
+
+// Arithmetic that keeps subnormals whatever the build's flags: each result is the IEEE one.
+__device__ __forceinline__ float mul_ieee(float a, float b) {
+  float r;
+  asm("mul.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float fma_ieee(float a, float b, float c) {
+  float r;
+  asm("fma.rn.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float div_ieee(float a, float b) {
+  float r;
+  asm("div.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_ieee(float a, float b) {
+  float r;
+  asm("max.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* f) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16lo(u[i]);
+    f[2 * i + 1] = bf16hi(u[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// E4M3 codes of 8 values over the row's scale (0: an all-zero row, zero codes).
+__device__ __forceinline__ uint2 codes8(const float* f, float scale) {
+  uint32_t u[2] = {0, 0};
+  if (scale > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(
+          make_float2(div_ieee(f[2 * i], scale), div_ieee(f[2 * i + 1], scale)), __NV_SATFINITE,
+          __NV_E4M3);
+      u[i >> 1] |= (uint32_t)c << (16 * (i & 1));
+    }
+  }
+  return make_uint2(u[0], u[1]);
+}
+
+// Rotates the lane's 8 pairs in place (f: the 16 values of its two vectors).
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate(float* f, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float& a = f[INTERLEAVED ? 2 * i : i];
+    float& b = f[INTERLEAVED ? 2 * i + 1 : 8 + i];
+    const float x = fma_ieee(a, c[i], -mul_ieee(b, s[i]));
+    b = fma_ieee(b, c[i], mul_ieee(a, s[i]));
+    a = x;
+  }
+}
+
+}  // namespace
+
+template <bool FP8, bool INTERLEAVED, int kUnroll>
+__global__ void __launch_bounds__(256) rope_write_kernel(const __grid_constant__ RopeArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int lanes = a.head_dim / 16;       // lanes of one head
+  const int per_pass = 32 / lanes;         // heads a warp holds at a time
+  const int sub = lane / lanes, c = lane - sub * lanes;
+  const bool active = sub < per_pass;      // head_dim not a power of two leaves lanes over
+  const int nrot = a.rope_dim / 16;
+  const bool rot = c < nrot;
+  const int lo = rot && !INTERLEAVED ? 8 * c : 16 * c;
+  const int hi = rot && !INTERLEAVED ? a.rope_dim / 2 + 8 * c : 16 * c + 8;
+  const int heads = a.H + 2 * a.Hkv;       // q, then k, then v
+  const int share = per_pass * kUnroll;
+  const int parts = (heads + share - 1) / share;
+  const int64_t items = a.num_tokens * parts;
+  for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items;
+       item += (int64_t)gridDim.x * 8) {
+    const int64_t t = item / parts;
+    const int head0 = (int)(item - t * parts) * share + sub;
+    uint4 w0[kUnroll], w1[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = head0 + u * per_pass;
+      w0[u] = w1[u] = make_uint4(0, 0, 0, 0);
+      if (active && h < heads) {
+        const uint16_t* src = h < a.H ? a.q + t * a.q_stride + h * a.head_dim
+                              : h < a.H + a.Hkv
+                                  ? a.k + t * a.k_stride + (h - a.H) * a.head_dim
+                                  : a.v + t * a.v_stride + (h - a.H - a.Hkv) * a.head_dim;
+        w0[u] = *reinterpret_cast<const uint4*>(src + lo);
+        w1[u] = *reinterpret_cast<const uint4*>(src + hi);
+      }
+    }
+    const int32_t slot = __ldg(a.slots + t);
+    bool bad_pos = false;
+    int pos[kRopeMaxAxes];
+#pragma unroll
+    for (int x = 0; x < kRopeMaxAxes; ++x) {
+      pos[x] = x < a.num_axes ? __ldg(a.positions + x * a.num_tokens + t) : 0;
+      bad_pos |= pos[x] < 0 || pos[x] >= a.max_pos;
+    }
+    if (bad_pos) {  // the same for the whole warp
+      if (lane == 0) flag_status(a.dev_status, PKV_DEV_BAD_POSITION);
+      continue;
+    }
+    const bool bad_slot = (int64_t)slot >= a.num_slots;
+    if (bad_slot && lane == 0) flag_status(a.dev_status, PKV_DEV_BAD_SLOT);
+    const bool store = slot >= 0 && !bad_slot;
+    float cs[8], sn[8];
+    if (rot) {
+      const int axis = a.chunk_axis[c];
+      if (axis >= 0) {  // the 8 pairs share one axis: whole vectors of its table row
+        const int p = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
+        const float4* row = reinterpret_cast<const float4*>(a.table + (int64_t)p * a.rope_dim + 8 * c);
+        const float4* row_s = reinterpret_cast<const float4*>(
+            a.table + (int64_t)p * a.rope_dim + a.rope_dim / 2 + 8 * c);
+        const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row_s), s1 = __ldg(row_s + 1);
+        cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
+        cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+        sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
+        sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = a.pair_axis[8 * c + i];
+          const int p = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
+          const float* row = a.table + (int64_t)p * a.rope_dim + 8 * c + i;
+          cs[i] = __ldg(row);
+          sn[i] = __ldg(row + a.rope_dim / 2);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = head0 + u * per_pass;
+      const bool is_q = h < a.H, is_v = h >= a.H + a.Hkv;
+      if (!FP8) {
+        if (!active || h >= heads) continue;
+        if (rot && !is_v) {
+          float f[16];
+          unpack8(w0[u], f);
+          unpack8(w1[u], f + 8);
+          rotate<INTERLEAVED>(f, cs, sn);
+          w0[u] = pack8(f);
+          w1[u] = pack8(f + 8);
+        }
+        uint16_t* dst;
+        if (is_q) {
+          dst = a.q_out + t * a.q_out_stride + h * a.head_dim;
+        } else {
+          if (!store) continue;
+          const int g = is_v ? h - a.H - a.Hkv : h - a.H;
+          dst = reinterpret_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) +
+                ((int64_t)slot * a.Hkv + g) * a.head_dim;
+        }
+        *reinterpret_cast<uint4*>(dst + lo) = w0[u];
+        *reinterpret_cast<uint4*>(dst + hi) = w1[u];
+      } else {
+        float f[16];
+        unpack8(w0[u], f);
+        unpack8(w1[u], f + 8);
+        if (rot && !is_v) rotate<INTERLEAVED>(f, cs, sn);
+        // Largest magnitude of the row, over its 8 lanes (head_dim is 128).
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = max_ieee(amax, fabsf(f[i]));
+#pragma unroll
+        for (int o = 4; o; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (h >= heads) continue;
+        if (is_q) {
+          uint16_t* dst = a.q_out + t * a.q_out_stride + h * a.head_dim;
+          *reinterpret_cast<uint4*>(dst + lo) = pack8(f);
+          *reinterpret_cast<uint4*>(dst + hi) = pack8(f + 8);
+        } else if (store) {
+          const float scale = div_ieee(amax, 448.f);
+          const int g = is_v ? h - a.H - a.Hkv : h - a.H;
+          uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + ((int64_t)slot * a.Hkv + g) * 128;
+          *reinterpret_cast<uint2*>(dst + lo) = codes8(f, scale);
+          *reinterpret_cast<uint2*>(dst + hi) = codes8(f + 8, scale);
+          if (c == 0) {
+            const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
+            (is_v ? a.v_scale : a.k_scale)[(blk * a.Hkv + g) * a.block_size + off] = scale;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <bool FP8, bool INTERLEAVED, int kUnroll>
+static cudaError_t launch_rope_n(const RopeArgs& a, cudaStream_t stream, int num_sms) {
+  const int share = 32 / (a.head_dim / 16) * kUnroll;
+  const int64_t items = a.num_tokens * ((a.H + 2 * a.Hkv + share - 1) / share);
+  int64_t blocks = (items + 7) / 8;
+  const int64_t cap = (int64_t)num_sms * 8;
+  if (blocks > cap) blocks = cap;
+  rope_write_kernel<FP8, INTERLEAVED, kUnroll><<<(unsigned)blocks, 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rope_write(const RopeArgs& a, bool fp8, bool interleaved, cudaStream_t stream,
+                              int num_sms) {
+  if (a.num_tokens == 0) return cudaSuccess;
+  if (fp8)
+    return interleaved ? launch_rope_n<true, true, 4>(a, stream, num_sms)
+                       : launch_rope_n<true, false, 4>(a, stream, num_sms);
+  return interleaved ? launch_rope_n<false, true, 4>(a, stream, num_sms)
+                     : launch_rope_n<false, false, 4>(a, stream, num_sms);
+}
+
+}  // namespace pkv
