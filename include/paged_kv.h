@@ -365,6 +365,79 @@ int pkv_paged_attention_decode_spec(void* out, int32_t out_dtype, float* lse, co
                                     void* workspace, size_t workspace_bytes, int* dev_status,
                                     void* stream);
 
+/* Sparse decode: attention over a few blocks of each sequence, chosen per query row and
+ * kv head by a cheap score. The pages bound a decode step's reads by dropping positions
+ * (the sliding window, "KV Cache 管理设计文档" §2.3); here the whole cache stays and each
+ * step reads the part of it that matters most to its queries. Three calls, after the
+ * step's rows are written: update the summaries, select, attend.
+ *
+ * Summaries [num_blocks, H_kv, 2, head_dim] bf16: per kv head and channel the smallest
+ * (index 0) and the largest (index 1) key value of a block's rows. A cache tensor like
+ * any other, in the blocks' order: pkv_copy_blocks copies it for a fork.
+ *
+ * pkv_update_block_summaries: for each sequence b, the rows at positions
+ * [seq_lens[b] - num_new[b], seq_lens[b]), already in k_cache, enter the summaries of the
+ * blocks that hold them. A block whose first row is among them starts over; any other
+ * keeps what its summary says of its earlier rows. A NaN key makes its channel NaN.
+ *   max_new: at least every num_new[b] (host value; the launch is sized by it)
+ * num_new 0 leaves a sequence as it is. num_new outside [0, max_new] or above seq_lens[b],
+ * or seq_lens[b] > max_blocks_per_seq * block_size, skips the sequence and sets
+ * PKV_DEV_BAD_LENGTH; a table entry outside [0, num_blocks) skips the block
+ * (PKV_DEV_BAD_BLOCK). A block that two sequences of one call both update must not be.
+ * Supported: head_dim 128, block_size 128 (PKV_ERR_UNSUPPORTED otherwise). */
+int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32_t* block_table,
+                               int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                               const int32_t* num_new, int32_t max_new, int32_t B, int32_t H_kv,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               int* dev_status, void* stream);
+
+/* pkv_select_blocks: for each query row (b, i) and kv head g, the num_selected blocks of the
+ * sequence with the largest scores, ascending, -1 behind the last one. Row i of q_len sits
+ * at position len_b - q_len + i and sees n = ceil((len_b - q_len + 1 + i) / block_size)
+ * blocks (none if that is negative). Block j's score is
+ *   sum_d (P_d max_jd + N_d min_jd), P_d = sum_h max(q_hd, 0), N_d = sum_h min(q_hd, 0)
+ * over the H / H_kv heads h of g: no key of the block has a larger summed dot product with
+ * them. Scores decide as they would in 64 bits, whatever the order of the sums; equal ones
+ * in favour of the lower block; a NaN score ranks above all. Blocks [0, num_sink) and the
+ * last num_recent that the row sees are always among the selected. A row with
+ * n <= num_selected takes every block, and no summary is read for it. A summary also
+ * covers the rows of a sequence behind the query row's own position.
+ *   block_indices [B, q_len, H_kv, num_selected] int32 (written)
+ *   q [B, q_len, H, head_dim] bf16; block_table, seq_lens as for decode
+ * Table entries outside [0, num_blocks) rank below every block and set
+ * PKV_DEV_BAD_BLOCK; a length past the table is clamped (PKV_DEV_BAD_LENGTH).
+ * Supported: head_dim 128, block_size 128, H % H_kv == 0, H / H_kv <= 16,
+ * num_sink + num_recent <= num_selected, max_blocks_per_seq <= 8192 (1,048,576 tokens).
+ * No workspace. */
+int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summaries,
+                      const int32_t* block_table, int32_t max_blocks_per_seq,
+                      const int32_t* seq_lens, int32_t B, int32_t q_len, int32_t H, int32_t H_kv,
+                      int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                      int32_t num_selected, int32_t num_sink, int32_t num_recent, int* dev_status,
+                      void* stream);
+
+/* pkv_paged_attention_decode_sparse: decode attention of q_len query rows per sequence (any
+ * number; row i as in pkv_paged_attention_decode_spec, without a window) in which row (b, i)
+ * and kv head g attend only to the positions, up to the row's own, that lie in the blocks
+ * block_indices[b][i][g] (in any order). A negative entry is an empty place. Only the first
+ * min(num_selected, n) entries are read, n being the number of blocks that the row sees;
+ * an entry of n or more is skipped and sets PKV_DEV_BAD_BLOCK. A block listed twice counts
+ * twice. A row without a single position to attend to returns o = 0, lse = -inf.
+ *   out, q, lse, caches, block_table, seq_lens as for pkv_paged_attention_decode_spec
+ *   block_indices [B, q_len, H_kv, num_selected] int32 (device)
+ * Supported: head_dim 128, block_size 128, H / H_kv in {1, 2, 4, 8, 16}.
+ * Workspace: pkv_decode_sparse_workspace_size() bytes, 256-byte aligned. */
+size_t pkv_decode_sparse_workspace_size(int32_t B, int32_t q_len, int32_t H, int32_t H_kv,
+                                        int32_t head_dim);
+int pkv_paged_attention_decode_sparse(void* out, int32_t out_dtype, float* lse, const void* q,
+                                      const void* k_cache, const void* v_cache,
+                                      const int32_t* block_table, int32_t max_blocks_per_seq,
+                                      const int32_t* seq_lens, const int32_t* block_indices,
+                                      int32_t num_selected, int32_t B, int32_t q_len, int32_t H,
+                                      int32_t H_kv, int32_t head_dim, int32_t block_size,
+                                      int64_t num_blocks, float scale, void* workspace,
+                                      size_t workspace_bytes, int* dev_status, void* stream);
+
 /* Prefill attention over TND-packed queries (standalone guide: sparse_mode 3 for
  * TND paged prefill, q in cumulative form, kv in direct form; "KV Cache 笔记"
  * "手写40行": the causal mask is bottom-right aligned when a cache precedes the new

@@ -69,6 +69,14 @@ SIGNATURES = {
     "pkv_paged_attention_decode_spec": (C.c_int, [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32,
                                                   i32, i32, i32, i32, i64, f32, i32, vp, sz, vp,
                                                   vp]),
+    "pkv_update_block_summaries": (C.c_int, [vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64,
+                                             vp, vp]),
+    "pkv_select_blocks": (C.c_int, [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i64, i32,
+                                    i32, i32, vp, vp]),
+    "pkv_decode_sparse_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+    "pkv_paged_attention_decode_sparse": (C.c_int, [vp, i32, vp, vp, vp, vp, vp, i32, vp, vp, i32,
+                                                    i32, i32, i32, i32, i32, i32, i64, f32, vp, sz,
+                                                    vp, vp]),
     "pkv_prefill_workspace_size": (sz, []),
     "pkv_paged_attention_prefill": (C.c_int, [vp, i32, vp, vp, vp, i32, vp, vp, vp, i32, vp, i32,
                                               i32, i32, i32, i32, i64, f32, i32, vp, sz, vp, vp]),

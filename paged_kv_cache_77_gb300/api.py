@@ -745,6 +745,120 @@ def paged_attention_decode_spec(q, k_cache, v_cache, block_table, seq_lens, scal
     return out
 
 
+def update_block_summaries(summaries, k_cache, block_table, seq_lens, num_new, max_new: int,
+                           dev_status=None, stream=None) -> None:
+    """Enter the newest num_new[b] rows of each sequence into its blocks' key summaries.
+
+    summaries [nb, H_kv, 2, d] bf16 (per channel the smallest and the largest key of the
+    block), k_cache [nb, bs, H_kv, d] with the new rows already written, seq_lens [B] the
+    lengths including them, num_new [B] int32, max_new an upper bound of num_new."""
+    _dev_bf16(summaries, "summaries")
+    _dev_bf16(k_cache, "k_cache")
+    nb, bs, hkv, d = _cache_dims(k_cache, "k_cache")
+    check_shape(summaries, (nb, hkv, 2, d), "summaries")
+    _dev_i32(num_new, "num_new")
+    B = num_new.numel()
+    _table_and_lens(block_table, seq_lens, B)
+    check_shape(num_new, (B,), "num_new")
+    dev = k_cache.device
+    check_same_device(dev, summaries=summaries, block_table=block_table, seq_lens=seq_lens,
+                      num_new=num_new)
+    check_current_device(dev)
+    status_buffer(dev_status, dev)
+    check(load().pkv_update_block_summaries(
+        _ptr(summaries), _ptr(k_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+        _ptr(num_new), int(max_new), B, hkv, d, bs, nb, _ptr(dev_status), _stream(stream)),
+        "pkv_update_block_summaries")
+
+
+def _query_rows(q):
+    """(B, q_len, H, d) of queries [B, H, d] (one row per sequence) or [B, q_len, H, d]."""
+    _dev_bf16(q, "q")
+    if q.dim() == 3:
+        return q.shape[0], 1, q.shape[1], q.shape[2]
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, d] or [B, q_len, H, d]")
+    return tuple(q.shape)
+
+
+def select_blocks(q, summaries, block_table, seq_lens, num_selected: int, num_sink: int = 0,
+                  num_recent: int = 1, out=None, dev_status=None, stream=None):
+    """The num_selected blocks of each sequence with the largest key bounds for its queries.
+
+    q [B, H, d] or [B, q_len, H, d]; returns int32 [B, H_kv, num_selected] or
+    [B, q_len, H_kv, num_selected] (`out` if given): blocks of the sequence, ascending, -1
+    behind the last. The first num_sink and the last num_recent blocks are always among them."""
+    B, Q, H, d = _query_rows(q)
+    _dev_bf16(summaries, "summaries")
+    nb, hkv, _, sd = _cache_dims(summaries, "summaries")
+    check_shape(summaries, (nb, hkv, 2, sd), "summaries")
+    if sd != d:
+        raise ValueError(f"summaries head_dim {sd} differs from q's {d}")
+    _table_and_lens(block_table, seq_lens, B)
+    if num_selected < 1:
+        raise ValueError("num_selected must be positive")
+    dev = q.device
+    shape = (B, hkv, num_selected) if q.dim() == 3 else (B, Q, hkv, num_selected)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _dev_i32(out, "out")
+        check_shape(out, shape, "out")
+    check_same_device(dev, summaries=summaries, block_table=block_table, seq_lens=seq_lens, out=out)
+    check_current_device(dev)
+    status_buffer(dev_status, dev)
+    if Q == 0:
+        return out
+    check(load().pkv_select_blocks(
+        _ptr(out), _ptr(q), _ptr(summaries), _ptr(block_table), block_table.shape[1],
+        _ptr(seq_lens), B, Q, H, hkv, d, 128, nb, num_selected, num_sink, num_recent,
+        _ptr(dev_status), _stream(stream)), "pkv_select_blocks")
+    return out
+
+
+def decode_sparse_workspace_size(B: int, q_len: int, H: int, H_kv: int, head_dim: int) -> int:
+    return load().pkv_decode_sparse_workspace_size(B, q_len, H, H_kv, head_dim)
+
+
+def paged_attention_decode_sparse(q, k_cache, v_cache, block_table, seq_lens, block_indices,
+                                  scale: float, out=None, lse=None, out_dtype=torch.float32,
+                                  workspace=None, dev_status=None, stream=None):
+    """Decode attention over the blocks that select_blocks chose (or any other list).
+
+    q [B, H, d] with block_indices [B, H_kv, K], or q [B, q_len, H, d] with block_indices
+    [B, q_len, H_kv, K]; returns out in q's shape (and fills lse, the shape without d)."""
+    B, Q, H, d = _query_rows(q)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _dev_bf16(t, n)
+    nb, bs, hkv, dk = _cache_dims(k_cache, "k_cache")
+    if dk != d:
+        raise ValueError(f"k_cache head_dim {dk} differs from q's {d}")
+    check_shape(v_cache, (nb, bs, hkv, d), "v_cache")
+    _table_and_lens(block_table, seq_lens, B)
+    _dev_i32(block_indices, "block_indices")
+    K = block_indices.shape[-1] if block_indices.dim() else 0
+    lead = tuple(q.shape[:-2])
+    check_shape(block_indices, lead + (hkv, K), "block_indices")
+    dev = q.device
+    check_same_device(dev, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                      seq_lens=seq_lens, block_indices=block_indices)
+    check_current_device(dev)
+    out = out_buffer(out, q.shape, out_dtype, dev)
+    lse_buffer(lse, lead + (H,), dev)
+    status_buffer(dev_status, dev)
+    if Q == 0:
+        return out
+    code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
+    workspace, ws_bytes = workspace_buffer(workspace,
+                                           decode_sparse_workspace_size(B, Q, H, hkv, d), dev)
+    check(load().pkv_paged_attention_decode_sparse(
+        _ptr(out), code, _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+        block_table.shape[1], _ptr(seq_lens), _ptr(block_indices), K, B, Q, H, hkv, d, bs, nb,
+        float(scale), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream)),
+        "pkv_paged_attention_decode_sparse")
+    return out
+
+
 def prefill_workspace_size() -> int:
     return load().pkv_prefill_workspace_size()
 

@@ -460,6 +460,130 @@ int pkv_paged_attention_decode_fp8(void* out, int32_t out_dtype, float* lse, con
   return launch_status(launch_decode_merge(a, s), "pkv_paged_attention_decode_fp8 (merge)");
 }
 
+size_t pkv_decode_sparse_workspace_size(int32_t B, int32_t q_len, int32_t H, int32_t H_kv,
+                                        int32_t head_dim) {
+  if (B < 0 || q_len < 1 || H <= 0 || H_kv <= 0 || H % H_kv || head_dim <= 0 ||
+      (int64_t)B * q_len > INT32_MAX)
+    return 0;
+  return decode_workspace_bytes(B * q_len, H, H_kv, head_dim, current_num_sms());
+}
+
+int pkv_paged_attention_decode_sparse(void* out, int32_t out_dtype, float* lse, const void* q,
+                                      const void* k_cache, const void* v_cache,
+                                      const int32_t* block_table, int32_t max_blocks_per_seq,
+                                      const int32_t* seq_lens, const int32_t* block_indices,
+                                      int32_t num_selected, int32_t B, int32_t q_len, int32_t H,
+                                      int32_t H_kv, int32_t head_dim, int32_t block_size,
+                                      int64_t num_blocks, float scale, void* workspace,
+                                      size_t workspace_bytes, int* dev_status, void* stream) {
+  const char* what = "pkv_paged_attention_decode_sparse";
+  PKV_REQUIRE(q_len >= 1 && num_selected >= 1, PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  // Rows of all sequences are numbered together, and the merge has a block per row and kv head.
+  PKV_REQUIRE(B < 0 || H_kv < 0 || (int64_t)B * q_len <= INT32_MAX / (H_kv > 0 ? H_kv : 1),
+              PKV_ERR_UNSUPPORTED, "%s: B * q_len * H_kv must fit in int32", what);
+  PKV_REQUIRE(max_blocks_per_seq <= INT32_MAX / 128, PKV_ERR_UNSUPPORTED,
+              "%s: max_blocks_per_seq * 128 must fit in int32", what);
+  DecodeArgs a;
+  bool empty;
+  const int rc0 = decode_setup(a, &empty, what, out, out_dtype, lse, q, k_cache, v_cache,
+                               block_table, max_blocks_per_seq, seq_lens, B * q_len, H, H_kv,
+                               head_dim, block_size, num_blocks, scale, 0, workspace,
+                               workspace_bytes, dev_status);
+  if (rc0 != PKV_OK || empty) return rc0;
+  PKV_REQUIRE(block_indices, PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+  a.block_indices = block_indices;
+  a.num_selected = num_selected;
+  a.rows_per_seq = q_len;
+  clear_error();
+  cudaStream_t s = (cudaStream_t)stream;
+  int rc = launch_status(launch_decode_sparse(a, s), "pkv_paged_attention_decode_sparse (attention)");
+  if (rc != PKV_OK) return rc;
+  return launch_status(launch_decode_merge(a, s), "pkv_paged_attention_decode_sparse (merge)");
+}
+
+int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32_t* block_table,
+                               int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                               const int32_t* num_new, int32_t max_new, int32_t B, int32_t H_kv,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               int* dev_status, void* stream) {
+  const char* what = "pkv_update_block_summaries";
+  PKV_REQUIRE(B >= 0 && H_kv > 0 && max_blocks_per_seq > 0 && num_blocks > 0 && max_new >= 0,
+              PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  PKV_REQUIRE(head_dim == 128 && block_size == 128, PKV_ERR_UNSUPPORTED,
+              "%s: only head_dim 128 and block_size 128 are implemented", what);
+  PKV_REQUIRE(summaries && k_cache && (B == 0 || (block_table && seq_lens && num_new)),
+              PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+  PKV_REQUIRE(aligned16(summaries) && aligned16(k_cache), PKV_ERR_INVALID_ARG,
+              "%s: pointers must be 16-byte aligned", what);
+  if (B == 0 || max_new == 0) return PKV_OK;
+  SummaryArgs a = {};
+  a.span = (int)(((int64_t)max_new + block_size - 2) / block_size + 1);
+  if (a.span > max_blocks_per_seq) a.span = max_blocks_per_seq;
+  PKV_REQUIRE((int64_t)B * a.span <= INT32_MAX / H_kv, PKV_ERR_UNSUPPORTED,
+              "%s: B * blocks of max_new * H_kv must fit in int32", what);
+  a.summaries = (uint8_t*)summaries;
+  a.k_cache = (const uint8_t*)k_cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.num_new = num_new;
+  a.dev_status = dev_status;
+  a.num_blocks = num_blocks;
+  a.B = B;
+  a.Hkv = H_kv;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_new = max_new;
+  clear_error();
+  return launch_status(launch_block_summaries(a, (cudaStream_t)stream), what);
+}
+
+int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summaries,
+                      const int32_t* block_table, int32_t max_blocks_per_seq,
+                      const int32_t* seq_lens, int32_t B, int32_t q_len, int32_t H, int32_t H_kv,
+                      int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                      int32_t num_selected, int32_t num_sink, int32_t num_recent, int* dev_status,
+                      void* stream) {
+  const char* what = "pkv_select_blocks";
+  PKV_REQUIRE(B >= 0 && q_len >= 1 && H > 0 && H_kv > 0 && max_blocks_per_seq > 0 && num_blocks > 0,
+              PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  PKV_REQUIRE(H % H_kv == 0, PKV_ERR_INVALID_ARG, "%s: H (%d) not a multiple of H_kv (%d)", what, H,
+              H_kv);
+  PKV_REQUIRE(num_selected >= 1 && num_sink >= 0 && num_recent >= 0 &&
+                  (int64_t)num_sink + num_recent <= num_selected,
+              PKV_ERR_INVALID_ARG, "%s: num_sink + num_recent must be at most num_selected", what);
+  PKV_REQUIRE(head_dim == 128 && block_size == 128, PKV_ERR_UNSUPPORTED,
+              "%s: only head_dim 128 and block_size 128 are implemented", what);
+  PKV_REQUIRE(H / H_kv <= 16, PKV_ERR_UNSUPPORTED, "%s: H / H_kv = %d unsupported", what, H / H_kv);
+  PKV_REQUIRE(max_blocks_per_seq <= kSelectMaxBlocks, PKV_ERR_UNSUPPORTED,
+              "%s: at most %d blocks per sequence", what, kSelectMaxBlocks);
+  // A cluster of up to 8 CTAs per row and kv head.
+  PKV_REQUIRE((int64_t)B * q_len <= INT32_MAX / 8 / H_kv, PKV_ERR_UNSUPPORTED,
+              "%s: B * q_len * H_kv too large", what);
+  if (B == 0) return PKV_OK;
+  PKV_REQUIRE(block_indices && q && summaries && block_table && seq_lens, PKV_ERR_INVALID_ARG,
+              "%s: null pointer", what);
+  PKV_REQUIRE(aligned16(q) && aligned16(summaries), PKV_ERR_INVALID_ARG,
+              "%s: pointers must be 16-byte aligned", what);
+  SelectArgs a = {};
+  a.q = (const uint16_t*)q;
+  a.summaries = (const uint8_t*)summaries;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = block_indices;
+  a.dev_status = dev_status;
+  a.num_blocks = num_blocks;
+  a.B = B;
+  a.q_len = q_len;
+  a.H = H;
+  a.Hkv = H_kv;
+  a.n_rep = H / H_kv;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_selected = num_selected;
+  a.num_sink = num_sink;
+  a.num_recent = num_recent;
+  clear_error();
+  return launch_status(launch_select_blocks(a, (cudaStream_t)stream, current_num_sms()), what);
+}
+
 size_t pkv_prefill_workspace_size(void) { return prefill_workspace_bytes(current_num_sms()); }
 
 int pkv_paged_attention_prefill(void* out, int32_t out_dtype, float* lse, const void* q,

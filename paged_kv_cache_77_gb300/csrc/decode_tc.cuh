@@ -19,6 +19,10 @@
 // position - W). The rows are padded to N = 16 or 32; each block of 16 columns has
 // its own four softmax warps.
 //
+// Sparse decode is the same kernel over rows that each bring a list of blocks (SPARSE): the
+// producer looks a tile's block up in the row's list and leaves its place in the sequence
+// for the softmax.
+//
 // Work split: the balanced (b, kv head, block) tile list of device_common.cuh, one
 // persistent CTA per SM. Warp roles:
 //   warp 0      TMA producer: Q of each piece (box {64 d, n_rep heads, QL tokens}),
@@ -93,6 +97,7 @@ struct Shape {
   static constexpr int OFF_RED = (OFF_BAR + B_COUNT * 8 + 15) & ~15;  // float [2][4][N]
   static constexpr int OFF_LRED = OFF_RED + 2 * 4 * N * 4;  // float [4][N]
   static constexpr int OFF_MISC = OFF_LRED + 4 * N * 4;     // tmem addr, abort, total, snaps
+  static constexpr int OFF_META = OFF_MISC + 48;  // int [NST]: sparse tiles' logical blocks
   static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;   // + alignment slack
   // TMEM columns: S^T buffers at 0 and N, O^T buffers at 2N and 3N.
   static constexpr uint32_t TMEM_COLS = 4 * N;
@@ -134,7 +139,7 @@ __device__ __forceinline__ bool issue_value(const DecodeArgs& a, uint32_t sbase,
   return true;
 }
 
-template <int NREP, int QL>
+template <int NREP, int QL, bool SPARSE>
 __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
     decode_tc_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q) {
@@ -164,6 +169,13 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = a.max_blocks * BS;
+  const auto rows = [&] {
+    if constexpr (SPARSE)
+      return SparseRows{a.seq_lens, BS, a.rows_per_seq, a.num_selected, cap};
+    else
+      return DenseRows{a.seq_lens, BS, a.window, cap};
+  }();
+  volatile int* meta = reinterpret_cast<int*>(base + L::OFF_META);
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -185,7 +197,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
-    const int64_t tot = total_live_blocks(a.seq_lens, a.B, BS, a.window, cap, a.dev_status);
+    const int64_t tot = total_live_blocks(rows, a.B, a.dev_status);
     if (lane == 0) *total_s = tot * a.Hkv;
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
@@ -225,9 +237,44 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
   if (ntiles > 0 && warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
     TileCursor c;
-    cursor_seek(c, a.seq_lens, a.B, a.Hkv, BS, a.window, cap, t0, t1);
+    cursor_seek(c, rows, a.B, a.Hkv, t0, t1);
     int piece = 0;
     const int rows_oob = (int)(a.num_blocks * BS);  // first row past the cache: zero fill
+    // Sparse rows find a tile's block through the row's list and then the table. The list
+    // entry of tile j + 2 and the table entry of tile j + 1 are fetched while tile j waits
+    // for its stage, so neither latency is in the way of the tile's load.
+    struct Entry {
+      int lb, seen;              // list entry, blocks that the row sees
+      const int32_t* table_row;
+    };
+    [[maybe_unused]] TileCursor lead = c;
+    [[maybe_unused]] Entry e1 = {-1, 0, nullptr};
+    [[maybe_unused]] int lb0 = -1, blk0 = -1;
+    [[maybe_unused]] auto fetch_entry = [&]() {
+      Entry e = {-1, 0, nullptr};
+      if (lead.t < lead.t_end) {
+        e.lb = __ldg(a.block_indices + ((int64_t)lead.b * a.Hkv + lead.g) * a.num_selected + lead.j);
+        e.seen = (lead.len + BS - 1) / BS;
+        e.table_row = a.block_table + (int64_t)(lead.b / a.rows_per_seq) * a.max_blocks;
+        cursor_next(lead, rows, a.B, a.Hkv);
+      }
+      return e;
+    };
+    // The table entry of a list entry; -1 for an empty place (negative) and for a block
+    // that the row does not see (its list may have been made for a longer row).
+    [[maybe_unused]] auto look_up = [&](Entry& e) {
+      if (e.lb >= e.seen) {
+        if (e.table_row) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+        e.lb = -1;
+      }
+      return e.lb >= 0 ? __ldg(e.table_row + e.lb) : -1;
+    };
+    if constexpr (SPARSE) {
+      Entry e0 = fetch_entry();
+      blk0 = look_up(e0);
+      lb0 = e0.lb;
+      e1 = fetch_entry();
+    }
     for (int j = 0; j < ntiles && !*abort_flag; ++j) {
       if (j == 0 || c.j == 0) {
         const int qb = piece & 1;
@@ -239,10 +286,22 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
         ++piece;
       }
       const int st = j % NST;
+      [[maybe_unused]] int lb1 = -1, blk1 = -1;
+      if constexpr (SPARSE) {
+        blk1 = look_up(e1);
+        lb1 = e1.lb;
+        e1 = fetch_entry();
+      }
       if (!mbar_wait(bar(B_KVEMPTY + st), ((j / NST) & 1) ^ 1)) { fail(); break; }
-      const int blk = __ldg(a.block_table + (int64_t)c.b * a.max_blocks + c.jlo + c.j);
+      const int blk = SPARSE ? blk0 : __ldg(a.block_table + (int64_t)c.b * a.max_blocks + c.jlo + c.j);
       const bool ok = blk >= 0 && (int64_t)blk < a.num_blocks;
-      if (!ok) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+      // A negative list entry is an empty place; nothing is wrong with it.
+      if (!ok && (!SPARSE || lb0 >= 0)) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+      if constexpr (SPARSE) {
+        meta[st] = ok ? lb0 : -1;  // the arrivals below publish it
+        lb0 = lb1;
+        blk0 = blk1;
+      }
       const int row = ok ? blk * BS : rows_oob;
       const uint32_t ks = sbase + OFF_K + st * TILE, vs = sbase + OFF_V + st * TILE;
       mbar_expect_tx(bar(B_KFULL + st), TILE);
@@ -251,7 +310,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
       mbar_expect_tx(bar(B_VFULL + st), TILE);
       tma_load_3d(vs, &tm_v, bar(B_VFULL + st), 0, c.g, row);
       tma_load_3d(vs + HALF, &tm_v, bar(B_VFULL + st), 64, c.g, row);
-      cursor_next(c, a.seq_lens, a.B, a.Hkv, BS, a.window, cap);
+      cursor_next(c, rows, a.B, a.Hkv);
     }
   } else if (ntiles > 0 && warp == 1 && lane == 0) {
     // ------------------------------------------------------------ score-product issuer
@@ -261,7 +320,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
     // commits track only its own MMAs.
     constexpr uint32_t ID_S = idesc_bf16(128, N, 0, 0);  // K (K-major) x Q^T (K-major)
     TileCursor c;
-    cursor_seek(c, a.seq_lens, a.B, a.Hkv, BS, a.window, cap, t0, t1);
+    cursor_seek(c, rows, a.B, a.Hkv, t0, t1);
     int piece = -1;
     bool ok = true;
     for (int j = 0; j < ntiles && !*abort_flag; ++j) {
@@ -282,7 +341,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
                desc_add(qd, (kk >> 2) * (QBUF / 2) + (kk & 3) * 32), ID_S, kk > 0);
       mma_commit(bar(B_SFULL + sb));
       if (last) mma_commit(bar(B_QEMPTY + qb));
-      cursor_next(c, a.seq_lens, a.B, a.Hkv, BS, a.window, cap);
+      cursor_next(c, rows, a.B, a.Hkv);
     }
     if (!ok) fail();
   } else if (ntiles > 0 && warp == L::OWARP && lane == 0) {
@@ -306,7 +365,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
     // zero query row: their scores are 0 or masked, and nothing reads them.
     const int nreal = NR - qbase < CW ? NR - qbase : CW;
     TileCursor c;
-    cursor_seek(c, a.seq_lens, a.B, a.Hkv, BS, a.window, cap, t0, t1);
+    cursor_seek(c, rows, a.B, a.Hkv, t0, t1);
     // Online softmax with a lazily moved reference: m_run (log2 units) changes only
     // when a block's max exceeds it by more than kLazy, so most tiles skip the
     // rescale; weights stay below 2^kLazy, well inside bf16 and fp32. The result is
@@ -424,9 +483,20 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
       // Visible columns of this token: query tokens [qlo, qhi], i.e. columns
       // [qlo * NREP, (qhi + 1) * NREP) of the piece. dpos = position - (len - QL):
       // token i sees it iff dpos <= i, and with a window iff i <= dpos + W - 1.
-      const int blk = __ldg(a.block_table + (int64_t)c.b * a.max_blocks + c.jlo + c.j);
-      const bool blk_ok = blk >= 0 && (int64_t)blk < a.num_blocks;
-      const int dpos = (c.jlo + c.j) * BS + r - (c.len - QL);
+      int lblk = c.jlo + c.j;
+      bool blk_ok;
+      if constexpr (SPARSE) {
+        // The producer's note of the tile's block (written before it armed K full, whose
+        // phase cannot move on before this tile's P is published).
+        const int st = j % NST;
+        if (!mbar_wait(bar(B_KFULL + st), (j / NST) & 1)) fail();
+        lblk = meta[st];
+        blk_ok = lblk >= 0;
+      } else {
+        const int blk = __ldg(a.block_table + (int64_t)c.b * a.max_blocks + lblk);
+        blk_ok = blk >= 0 && (int64_t)blk < a.num_blocks;
+      }
+      const int dpos = lblk * BS + r - (c.len - QL);
       const int qlo = dpos > 0 ? dpos : 0;
       int qhi = QL - 1;
       if (a.row_window > 0 && dpos + a.row_window - 1 < qhi) qhi = dpos + a.row_window - 1;
@@ -567,7 +637,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
       mbar_arrive(bar(B_PFULL + sb));
       // ---- fold the previous tile's O^T into the registers, with this tile's rescale
       if (!first && !resc) acc_o(j - 1);
-      cursor_next(c, a.seq_lens, a.B, a.Hkv, BS, a.window, cap);
+      cursor_next(c, rows, a.B, a.Hkv);
     }
     if (!aborted) {
       acc_o(ntiles - 1);
@@ -587,7 +657,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
 bool make_tmap_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                     const uint64_t* strides, const uint32_t* box);
 
-template <int NREP, int QL>
+template <int NREP, int QL, bool SPARSE = false>
 static cudaError_t launch_tc_n(const DecodeArgs& a, cudaStream_t stream) {
   using namespace tcd;
   using L = Shape<NREP, QL>;
@@ -604,10 +674,10 @@ static cudaError_t launch_tc_n(const DecodeArgs& a, cudaStream_t stream) {
       !make_tmap_bf16(&tv, a.v_cache, 3, kdims, kstr, kbox) ||
       !make_tmap_bf16(&tq, a.q, 3, qdims, qstr, qbox))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NREP, QL>,
+  cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<NREP, QL, SPARSE>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_tc_kernel<NREP, QL>, dim3(a.num_ctas), dim3(L::NTHREADS), L::SMEM_BYTES, stream,
+  return launch_dependent(decode_tc_kernel<NREP, QL, SPARSE>, dim3(a.num_ctas), dim3(L::NTHREADS), L::SMEM_BYTES, stream,
                           a, tk, tv, tq);
 }
 

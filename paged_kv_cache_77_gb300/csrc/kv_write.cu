@@ -194,10 +194,7 @@ __global__ void __launch_bounds__(256) kv_read_fp8_kernel(
         const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(
             (__nv_fp8x2_storage_t)(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-        float lo, hi;  // without flushing subnormals, whatever the build's flags
-        asm("mul.rn.f32 %0, %1, %2;\n" : "=f"(lo) : "f"(f.x), "f"(scale));
-        asm("mul.rn.f32 %0, %1, %2;\n" : "=f"(hi) : "f"(f.y), "f"(scale));
-        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(mul_ieee(f.x, scale), mul_ieee(f.y, scale));
         r[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
       o0 = make_uint4(r[0], r[1], r[2], r[3]);

@@ -51,6 +51,32 @@ cudaError_t launch_kv_read_fp8(void* k, void* v, const void* k_cache, const void
                                int64_t num_tokens, int64_t num_blocks, int block_size, int hkv,
                                int* dev_status, cudaStream_t stream, int num_sms);
 
+// Block summaries and block selection (block_select.cu).
+constexpr int kSelectMaxBlocks = 8192;  // table width that a selection's shared memory holds
+struct SummaryArgs {
+  uint8_t* summaries;         // [nb, Hkv, 2, 128] bf16: minima, maxima
+  const uint8_t* k_cache;     // [nb, 128, Hkv, 128] bf16
+  const int32_t* block_table; // [B, max_blocks]
+  const int32_t* seq_lens;    // [B]
+  const int32_t* num_new;     // [B]
+  int* dev_status;
+  int64_t num_blocks;
+  int B, Hkv, max_blocks, max_new;
+  int span;                   // blocks that max_new new rows can touch
+};
+cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream);
+struct SelectArgs {
+  const uint16_t* q;          // [B, q_len, H, 128] bf16
+  const uint8_t* summaries;
+  const int32_t* block_table; // [B, max_blocks]
+  const int32_t* seq_lens;    // [B]
+  int32_t* out;               // [B, q_len, Hkv, num_selected]
+  int* dev_status;
+  int64_t num_blocks;
+  int B, q_len, H, Hkv, n_rep, max_blocks, num_selected, num_sink, num_recent;
+};
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int num_sms);
+
 // Arguments of the split-KV decode kernels and their LSE merge.
 struct DecodeArgs {
   const uint16_t* q;          // [B, q_len, H, D] bf16
@@ -72,6 +98,9 @@ struct DecodeArgs {
   float scale_log2;           // scale * log2(e)
   const float* k_scale;       // FP8 cache only: [nb, Hkv, bs] per-row scales
   const float* v_scale;
+  // Sparse decode only: B counts query rows, rows_per_seq of each sequence.
+  const int32_t* block_indices;  // [B, Hkv, num_selected] blocks of the sequence, or null
+  int num_selected, rows_per_seq;
 };
 
 size_t decode_workspace_bytes(int B, int H, int Hkv, int D, int G);
@@ -84,6 +113,8 @@ cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t stream);
 // The same kernel for q_len 1..4 query rows per sequence (q_len * n_rep <= 32).
 cudaError_t launch_decode_spec(const DecodeArgs& a, cudaStream_t stream);
+// The same kernel over the blocks that each query row lists (a.block_indices).
+cudaError_t launch_decode_sparse(const DecodeArgs& a, cudaStream_t stream);
 // tcgen05 split-KV decode over an FP8 (E4M3) cache with per-row scales; same
 // partials and merge as above.
 cudaError_t launch_decode_fp8(const DecodeArgs& a, cudaStream_t stream);

@@ -31,28 +31,6 @@ namespace pkv {
 
 namespace {
 
-// Arithmetic that keeps subnormals whatever the build's flags: each result is the IEEE one.
-__device__ __forceinline__ float mul_ieee(float a, float b) {
-  float r;
-  asm("mul.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float fma_ieee(float a, float b, float c) {
-  float r;
-  asm("fma.rn.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float div_ieee(float a, float b) {
-  float r;
-  asm("div.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_ieee(float a, float b) {
-  float r;
-  asm("max.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 __device__ __forceinline__ void unpack8(const uint4& w, float* f) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
