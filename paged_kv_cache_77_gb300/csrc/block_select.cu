@@ -141,115 +141,352 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------ selection
-// One cluster of C CTAs per (query row, kv head): all of them score blocks, the first keeps
-// the scores in its shared memory (the others store into it) and selects.
+// One cluster of C CTAs per (query row, kv head). Each CTA scores one run of the row's blocks
+// and keeps their keys (order-preserving whole numbers) in its shared memory. A row of at most
+// 256 competing blocks (C = 1) is then selected by one warp with the keys in registers; for
+// longer ones the CTAs select together, exchanging histograms and counts through distributed
+// shared memory.
 //
 // Scores are taken in fp32, 512 coalesced bytes per block (lanes 0-15 hold the minima and N,
 // lanes 16-31 the maxima and P, 8 channels each), 8 blocks per warp at a time whose sums are
 // reduced across the lanes together. Selection needs exact order only at the border, so the
 // kernel bounds the fp32 error,
 //
-//   |score32 - score| <= eps = 2^-18 (sum_d P_d + |N_d|) max |summary|,
+//   |score32 - score| <= eps = (n_rep + 14) 2^-24 (sum_d P_d + |N_d|) max |summary|
 //
-// (at most 15 roundings in P and N, one per product and sum, 5 in the reduction: 29 of 2^-24,
-// of terms whose magnitudes add up to no more than the product), takes every block above
-// tau + 2 eps and none below tau - 2 eps, tau being the K-th largest fp32 score, and scores
-// the blocks between again in fp64. Usually there is one, tau's own, and then nothing is left
-// to decide. The result is that of fp64 scores, ties to the lower block, whatever the order of
-// the fp32 sums.
+// (n_rep - 1 roundings in P and N, 8 in a lane's sum of products, 5 in the reduction, and
+// room for the bound's own), finds the K-th largest fp32 score tau to within a bin narrower
+// than eps, takes every block above the bin by more than 2 eps and none below it by more, and
+// scores the blocks between again in fp64 where they are more than the places left. The
+// result is that of fp64 scores, ties to the lower block, whatever the order of the fp32 sums.
 //
 // A block whose score is NaN (a NaN key, or infinite keys that cancel) ranks above all others.
 namespace {
 
 constexpr int kSelWarps = 8;
 constexpr int kSelThreads = 32 * kSelWarps;
+constexpr int kMaxCluster = 8;
+constexpr int kWarpKeys = 8;              // keys of a lane where one warp selects
 constexpr uint32_t kNanKey = 0xfffffffeu;
+constexpr uint32_t kTaken = 0xffffffffu;  // above every score's key
+constexpr uint32_t kEdge = kNanKey;       // candidates at the border, once no key is a NaN's
 
-// Order-preserving whole numbers for scores; -0 and +0 are equal, NaN is the largest.
+// Order-preserving whole numbers for scores; -0 and +0 are equal, NaN is the largest. Key 0
+// stands for a block whose table entry is bad.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return kNanKey;
   const uint32_t u = x == 0.f ? 0u : __float_as_uint(x);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_score(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 __device__ __forceinline__ unsigned long long order_key(double x) {
   if (x != x) return ~0ull;
   const unsigned long long u = x == 0.0 ? 0ull : (unsigned long long)__double_as_longlong(x);
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
+// Shared memory of one CTA. What other CTAs of the cluster read (hist, pub, the keys) is
+// written once per kernel and place, so one cluster barrier between the writes and the reads
+// is enough.
 struct SelShared {
-  int hist[256];
-  int count[kSelWarps];
-  int total, digit, above, above2;
-  unsigned long long prefix;
-  unsigned int amax[64];  // per warp of the cluster: largest |summary| seen, bf16 bits
+  float coef[2 * kDim], coef_low[2 * kDim];  // N, then P: their fp32 sums and what those left out
+  int hist[4 + 8][256];                  // digit counts: 4 passes over 32-bit keys, 8 over 64
+  unsigned long long pub[5][2];          // a pair of numbers per exchange
+  unsigned long long lo[kSelWarps], hi[kSelWarps];
+  float size[kSelWarps];
+  uint32_t any_q[kSelWarps], amax[kSelWarps];
+  int warp_sum[kSelWarps], warp_sum2[kSelWarps];
+  int digit, above, inside, candidates;
 };
 
-// The k-th largest of keys[0, n) (1 <= k <= n), by 8 bits at a time from the top; *greater is
-// the number of keys above it. Called by the whole CTA.
+struct Cluster {
+  int size, rank;
+  __device__ __forceinline__ void sync() const {
+    if (size > 1)
+      cg::this_cluster().sync();
+    else
+      __syncthreads();
+  }
+  template <typename T>
+  __device__ __forceinline__ T read(T* mine, int r) const {
+    return r == rank ? *mine : *cg::this_cluster().map_shared_rank(mine, r);
+  }
+};
+
+// Where a row's blocks lie and what bounds their scores.
+struct Row {
+  const int32_t* table;  // of the CTA's first block
+  const uint8_t* sum;    // the lane's 16 bytes of block 0's summary
+  int64_t sum_stride, num_blocks;
+  float eps;             // bound of a score's fp32 error
+  bool bounded;          // eps is one
+  bool exact;            // every good block's score is exactly zero
+};
+
+// Keys of up to 4 candidates in fp64, by a warp; key64[r] for the blocks cand[r].
+__device__ void score64(const Row& row, const SelShared& sh, const uint32_t* cand,
+                        unsigned long long* key64, int n) {
+  const int lane = threadIdx.x & 31;
+  uint4 x[4];
+  bool good[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int blk = r < n ? __ldg(row.table + cand[r]) : -1;
+    good[r] = blk >= 0 && (int64_t)blk < row.num_blocks;
+    x[r] = good[r] ? ld_nc_v4(row.sum + blk * row.sum_stride) : make_uint4(0, 0, 0, 0);
+  }
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double k = widen_ieee(sh.coef[8 * lane + i]) + widen_ieee(sh.coef_low[8 * lane + i]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (r >= n) break;
+      const uint32_t w = i < 2 ? x[r].x : i < 4 ? x[r].y : i < 6 ? x[r].z : x[r].w;
+      s[r] = fma(k, widen_ieee(i & 1 ? bf16hi(w) : bf16lo(w)), s[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (r >= n) break;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+    if (lane == 0) key64[r] = good[r] ? order_key(s[r]) : 0ull;
+  }
+}
+
+// [maybe, sure] from the bin [lo, hi] that holds the K-th largest key: keys above `sure` are
+// in, keys below `maybe` are out.
+__device__ __forceinline__ void border(const Row& row, uint32_t lo, uint32_t hi, uint32_t* maybe,
+                                       uint32_t* sure) {
+  *maybe = 0;
+  *sure = kNanKey;
+  if (row.exact) {
+    *maybe = *sure = lo;
+  } else if (row.bounded && lo != 0) {  // lo = 0: bad blocks are at the border
+    const float a = key_score(lo), b = key_score(hi);
+    // Rounded outward: a few units of 2^-24 of the operands.
+    *maybe = order_key(a - (2.f * row.eps + (fabsf(a) + row.eps) * 0x1p-22f));
+    *sure = order_key(b + (2.f * row.eps + (fabsf(b) + row.eps) * 0x1p-22f));
+  }
+}
+
+// Selection by one warp: the `want` best of the m <= 256 blocks with keys key32[0, m), in
+// ascending order, to out[i] = first + block. Lane l holds blocks l, l + 32, ...: a count of
+// the keys from a threshold on is 8 comparisons and one warp sum, so the K-th largest is found
+// bit by bit, from the highest bit in which the keys differ down to a bin narrower than eps.
+__device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* key32,
+                               unsigned long long* key64, uint32_t* cand, int m, int want, int first,
+                               int32_t* out) {
+  const int lane = threadIdx.x & 31;
+  uint32_t k[kWarpKeys];
+  uint32_t kmin = 0xffffffffu, kmax = 0;
+#pragma unroll
+  for (int u = 0; u < kWarpKeys; ++u) {
+    const int i = lane + 32 * u;
+    k[u] = i < m ? key32[i] : 0u;
+    kmin = min(kmin, i < m ? k[u] : 0xffffffffu);
+    kmax = max(kmax, k[u]);
+  }
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  auto count = [&](uint32_t from) {
+    int c = 0;
+#pragma unroll
+    for (int u = 0; u < kWarpKeys; ++u) c += k[u] >= from;
+    return (int)__reduce_add_sync(0xffffffffu, c);
+  };
+  uint32_t lo = kmin, hi = kmin, maybe, sure;
+  if (kmin != kmax && row.bounded) {
+    int bit = 31 - __clz((int)(kmin ^ kmax));
+    lo = kmin & ~((2u << bit) - 1);
+    for (;; --bit) {
+      const uint32_t from = lo | (1u << bit);
+      if (count(from) >= want) lo = from;
+      hi = lo | ((1u << bit) - 1);
+      if (bit == 0 || (lo != 0 && key_score(hi) - key_score(lo) <= row.eps)) break;
+    }
+  }
+  border(row, lo, hi, &maybe, &sure);
+  uint32_t pass = maybe;
+  // (Keys behind the row's end are 0: they count only where bad blocks do.)
+  int in = 0, surely = 0;
+#pragma unroll
+  for (int u = 0; u < kWarpKeys; ++u) {
+    in += lane + 32 * u < m && k[u] >= maybe;
+    surely += k[u] > sure;
+  }
+  in = __reduce_add_sync(0xffffffffu, in);
+  if (in > want) {
+    const int need = want - (int)__reduce_add_sync(0xffffffffu, surely);
+    int nc = 0;
+#pragma unroll
+    for (int u = 0; u < kWarpKeys; ++u) {
+      const bool c = lane + 32 * u < m && k[u] >= maybe && k[u] <= sure;
+      const unsigned mask = __ballot_sync(0xffffffffu, c);
+      if (c) cand[nc + __popc(mask & ((1u << lane) - 1))] = lane + 32 * u;
+      nc += __popc(mask);
+    }
+    __syncwarp();
+    for (int r = 0; r < nc; r += 4) {
+      if (row.exact) {
+        if (lane < 4 && r + lane < nc) key64[r + lane] = key32[cand[r + lane]];
+      } else {
+        score64(row, sh, cand + r, key64 + r, min(4, nc - r));
+      }
+    }
+    __syncwarp();
+    // A candidate's rank: those above it, and those equal to it in lower blocks.
+#pragma unroll 1
+    for (int u = 0; u < kWarpKeys; ++u) {
+      if (32 * u >= nc) break;
+      const int r = lane + 32 * u;
+      const unsigned long long mine = r < nc ? key64[r] : 0;
+      int rank = 0;
+      for (int s = 0; s < nc; ++s) {
+        const unsigned long long other = key64[s];
+        rank += other > mine || (other == mine && s < r);
+      }
+      if (r < nc) cand[r] |= rank < need ? 0x80000000u : 0u;
+    }
+    __syncwarp();
+    // Back to the lanes that hold the keys; the r-th candidate in ascending order is cand[r].
+    int at = 0;
+#pragma unroll
+    for (int u = 0; u < kWarpKeys; ++u) {
+      const bool c = lane + 32 * u < m && k[u] >= maybe && k[u] <= sure;
+      const unsigned mask = __ballot_sync(0xffffffffu, c);
+      if (c) k[u] = (cand[at + __popc(mask & ((1u << lane) - 1))] >> 31) ? kTaken : 0u;
+      at += __popc(mask);
+    }
+    pass = sure + 1;
+  }
+  int at = 0;
+#pragma unroll
+  for (int u = 0; u < kWarpKeys; ++u) {
+    const bool c = lane + 32 * u < m && k[u] >= pass;
+    const unsigned mask = __ballot_sync(0xffffffffu, c);
+    if (c) out[at + __popc(mask & ((1u << lane) - 1))] = first + lane + 32 * u;
+    at += __popc(mask);
+  }
+}
+
+// What a search for the k-th largest key found: it lies in [lo, hi], a bin of `inside` keys,
+// below `above` others.
 template <typename Key>
-__device__ Key kth_largest(const Key* keys, int n, int k, SelShared& sh, int* greater) {
-  constexpr int kBits = 8 * sizeof(Key);
-  Key prefix = 0;
-  int rest = k;
-  for (int shift = kBits - 8; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kSelThreads) sh.hist[i] = 0;
-    __syncthreads();
+struct Bin {
+  Key lo, hi;
+  int above, inside;
+};
+
+// The k-th largest of the cluster's keys (this CTA's are keys[0, n); all are in [kmin, kmax])
+// to within a bin that `done` accepts, by 8 bits at a time below the bits they share. Every
+// pass counts digits in its own histogram hist[pass], zero beforehand.
+template <typename Key, typename Done>
+__device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kmax, int (*hist)[256],
+                                SelShared& sh, const Cluster& cl, Done done) {
+  Bin<Key> b = {kmin, kmax, 0, 0};
+  if (kmin == kmax) return b;
+  const int top = 8 * (int)sizeof(Key) - 1 -
+                  (sizeof(Key) == 8 ? __clzll((long long)(kmin ^ kmax)) : __clz((int)(kmin ^ kmax)));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int pass = 0, high = top;; ++pass) {
+    const int shift = high > 7 ? high - 7 : 0;  // digit: bits [shift, high]
+    const Key mask = (Key)((1u << (high - shift + 1)) - 1);
     for (int i = threadIdx.x; i < n; i += kSelThreads) {
       const Key key = keys[i];
-      const bool in = shift == kBits - 8 || (key >> ((shift + 8) & (kBits - 1))) == prefix;
-      if (in) atomicAdd(&sh.hist[(int)(key >> shift) & 255], 1);
+      if (key >= b.lo && key <= b.hi) atomicAdd(&hist[pass][(int)((key >> shift) & mask)], 1);
+    }
+    cl.sync();
+    // Thread t holds digit 255 - t, so that a prefix sum counts the larger digits.
+    int own = 0;
+    for (int r = 0; r < cl.size; ++r) own += cl.read(&hist[pass][255 - threadIdx.x], r);
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    int before = b.above + incl - own;
+    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+    if (before < k && k <= before + own) {  // one thread
+      sh.digit = 255 - threadIdx.x;
+      sh.above = before;
+      sh.inside = own;
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-      // Lane l sums digits 8l..8l+7; the lanes above it hold the larger digits.
-      const int lane = threadIdx.x;
-      int own = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) own += sh.hist[8 * lane + i];
-      int incl = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_down_sync(0xffffffffu, incl, o);
-        if (lane + o < 32) incl += y;
-      }
-      int above = incl - own;
-      if (above < rest && rest <= incl) {
-        for (int d = 8 * lane + 7;; --d) {
-          if (above + sh.hist[d] >= rest) {
-            sh.digit = d;
-            sh.above = above;
-            break;
-          }
-          above += sh.hist[d];
-        }
-      }
-    }
-    __syncthreads();
-    prefix = (Key)((prefix << 8) | (Key)sh.digit);
-    rest -= sh.above;
+    const Key base = (b.lo & ~((mask << shift) | (((Key)1 << shift) - 1))) | ((Key)sh.digit << shift);
+    b.lo = base;
+    b.hi = base | (((Key)1 << shift) - 1);
+    b.above = sh.above;
+    b.inside = sh.inside;
+    if (shift == 0 || done(b)) return b;
+    high = shift - 1;
   }
-  *greater = k - rest;
-  return prefix;
+}
+
+// Sums of a and c over the CTA's threads and, for the CTAs of the cluster, the sums of a over
+// those before this one and of both over all. `slot`: this exchange's place in sh.pub.
+struct Counted {
+  int before_a, all_a, all_c;
+};
+__device__ Counted count_cluster(int a, int c, int slot, SelShared& sh, const Cluster& cl) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  a = __reduce_add_sync(0xffffffffu, a);
+  c = __reduce_add_sync(0xffffffffu, c);
+  if (lane == 0) {
+    sh.warp_sum[warp] = a;
+    sh.warp_sum2[warp] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned long long sa = 0, sc = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+      sa += sh.warp_sum[w];
+      sc += sh.warp_sum2[w];
+    }
+    sh.pub[slot][0] = sa;
+    sh.pub[slot][1] = sc;
+  }
+  cl.sync();
+  Counted t = {0, 0, 0};
+  for (int r = 0; r < cl.size; ++r) {
+    const int x = (int)cl.read(&sh.pub[slot][0], r);
+    if (r < cl.rank) t.before_a += x;
+    t.all_a += x;
+    t.all_c += (int)cl.read(&sh.pub[slot][1], r);
+  }
+  return t;
 }
 
 // Calls put(rank, i) for every i in [0, n) with pick(i), rank counting them in ascending
-// order; returns their number. Called by the whole CTA; each warp takes one run of indices.
+// order. Called by the whole CTA; each warp takes one run of indices.
 template <typename Pick, typename Put>
-__device__ int compact(int n, SelShared& sh, Pick pick, Put put) {
+__device__ void compact(int n, SelShared& sh, Pick pick, Put put) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int run = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
   const int i0 = warp * run, i1 = min(n, i0 + run);
   int mine = 0;
-  for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && pick(i + lane)));
-  if (lane == 0) sh.count[warp] = mine;
+  for (int i = i0; i < i1; i += 32)
+    mine += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && pick(i + lane)));
+  if (lane == 0) sh.warp_sum[warp] = mine;
   __syncthreads();
-  int at = 0, all = 0;
-#pragma unroll
-  for (int v = 0; v < kSelWarps; ++v) {
-    if (v < warp) at += sh.count[v];
-    all += sh.count[v];
-  }
+  int at = 0;
+  for (int w = 0; w < warp; ++w) at += sh.warp_sum[w];
   for (int i = i0; i < i1; i += 32) {
     const bool in = i + lane < i1 && pick(i + lane);
     const unsigned m = __ballot_sync(0xffffffffu, in);
@@ -257,26 +494,176 @@ __device__ int compact(int n, SelShared& sh, Pick pick, Put put) {
     at += __popc(m);
   }
   __syncthreads();
-  return all;
+}
+
+// Selection by the cluster: CTA `rank` holds the keys of m blocks from `first` on.
+__device__ void select_by_cluster(const Row& row, SelShared& sh, const Cluster& cl, uint32_t* key32,
+                                  unsigned long long* key64, uint32_t* cand, int m, int want,
+                                  int first, uint32_t kmin, uint32_t kmax, int32_t* out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t lo = 0, hi = 0, maybe, sure;
+  if (row.bounded) {
+    const Bin<uint32_t> bin = kth_largest<uint32_t>(
+        key32, m, want, kmin, kmax, sh.hist, sh, cl, [&](const Bin<uint32_t>& x) {
+          return x.lo != 0 && key_score(x.hi) - key_score(x.lo) <= row.eps;
+        });
+    lo = bin.lo;
+    hi = bin.hi;
+  }
+  border(row, lo, hi, &maybe, &sure);
+  int in = 0, surely = 0;
+  for (int i = threadIdx.x; i < m; i += kSelThreads) {
+    in += key32[i] >= maybe;
+    surely += key32[i] > sure;
+  }
+  Counted t = count_cluster(in, surely, 1, sh, cl);
+  uint32_t pass = maybe;  // keys from here on are taken
+  if (t.all_a > want) {
+    // More blocks in reach of the border than places: score them in fp64.
+    const int need = want - t.all_c;
+    for (int i = threadIdx.x; i < 8 * 256; i += kSelThreads) (&sh.hist[4][0])[i] = 0;
+    for (int i = threadIdx.x; i < m; i += kSelThreads)
+      if (key32[i] >= maybe && key32[i] <= sure) cand[atomicAdd(&sh.candidates, 1)] = i;
+    __syncthreads();
+    const int nc = sh.candidates;
+    unsigned long long lo64 = ~0ull, hi64 = 0;
+    for (int r = warp * 4; r < nc; r += kSelWarps * 4) {
+      if (row.exact) {
+        if (lane < 4 && r + lane < nc) key64[r + lane] = key32[cand[r + lane]];
+      } else {
+        score64(row, sh, cand + r, key64 + r, min(4, nc - r));
+      }
+      __syncwarp();
+      for (int s = r; s < min(nc, r + 4); ++s) {
+        lo64 = min(lo64, key64[s]);
+        hi64 = max(hi64, key64[s]);
+      }
+    }
+    if (lane == 0) {
+      sh.lo[warp] = lo64;
+      sh.hi[warp] = hi64;
+    }
+    if (threadIdx.x == 0) sh.pub[2][0] = nc;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kSelWarps; ++w) {
+        sh.lo[0] = min(sh.lo[0], sh.lo[w]);
+        sh.hi[0] = max(sh.hi[0], sh.hi[w]);
+      }
+      sh.pub[3][0] = sh.lo[0];
+      sh.pub[3][1] = sh.hi[0];
+    }
+    cl.sync();
+    int all = 0;
+    for (int r = 0; r < cl.size; ++r) all += (int)cl.read(&sh.pub[2][0], r);
+    if (all <= 32) {
+      // Few: lane l of the first warp of every CTA takes the l-th of them all and ranks it.
+      if (warp == 0) {
+        int owner = 0, at = lane;
+        for (; owner < cl.size; ++owner) {
+          const int theirs = (int)cl.read(&sh.pub[2][0], owner);
+          if (at < theirs) break;
+          at -= theirs;
+        }
+        const bool have = owner < cl.size;
+        const unsigned long long mine = have ? cl.read(key64 + at, owner) : 0;
+        const uint32_t i = have ? cl.read(cand + at, owner) : 0;
+        const uint32_t place = (uint32_t)owner << 16 | i;  // ascending blocks over the cluster
+        int rank = 0;
+        for (int s = 0; s < all; ++s) {
+          const unsigned long long other = __shfl_sync(0xffffffffu, mine, s);
+          const uint32_t where = __shfl_sync(0xffffffffu, place, s);
+          rank += other > mine || (other == mine && where < place);
+        }
+        if (owner == cl.rank) key32[i] = rank < need ? kTaken : 0u;
+      }
+      __syncthreads();
+    } else {
+      for (int r = 0; r < cl.size; ++r) {
+        lo64 = min(lo64, cl.read(&sh.pub[3][0], r));
+        hi64 = max(hi64, cl.read(&sh.pub[3][1], r));
+      }
+      // All keys of the bin are taken, or (one value) as many of the lowest blocks as it takes.
+      const Bin<unsigned long long> bin = kth_largest<unsigned long long>(
+          key64, nc, need, lo64, hi64, sh.hist + 4, sh, cl,
+          [&](const Bin<unsigned long long>& x) { return x.above + x.inside == need; });
+      int at_edge = 0;
+      for (int r = threadIdx.x; r < nc; r += kSelThreads) {
+        const bool edge = key64[r] >= bin.lo && key64[r] <= bin.hi;
+        at_edge += edge;
+        key32[cand[r]] = key64[r] > bin.hi ? kTaken : edge ? kEdge : 0u;
+      }
+      const int rest = need - bin.above - count_cluster(at_edge, 0, 4, sh, cl).before_a;
+      compact(
+          m, sh, [&](int i) { return key32[i] == kEdge; },
+          [&](int k, int i) { key32[i] = k < rest ? kTaken : 0u; });
+    }
+    pass = sure + 1;
+    in = 0;
+    for (int i = threadIdx.x; i < m; i += kSelThreads) in += key32[i] >= pass;
+    // The first exchange's place is free again: every CTA has read it and passed a barrier since.
+    t = count_cluster(in, 0, 1, sh, cl);
+  }
+  compact(
+      m, sh, [&](int i) { return key32[i] >= pass; },
+      [&](int r, int i) { out[t.before_a + r] = first + i; });
+  if (cl.size > 1) cl.sync();  // the others may still be reading this CTA's shared memory
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid_constant__ SelectArgs a) {
+// kRounds: groups of 8 blocks whose summaries a warp has in flight at a time.
+template <int kRounds>
+__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid_constant__ SelectArgs a,
+                                                                    int chunk_cap) {
   extern __shared__ unsigned long long sel_smem[];
   __shared__ SelShared sh;
-  __shared__ double coef64[2 * kDim];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const Cluster cl = {(int)cg::this_cluster().num_blocks(), (int)cg::this_cluster().block_rank()};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t seg = blockIdx.x / C;  // (query row, kv head)
+  const int64_t seg = blockIdx.x / cl.size;  // (query row, kv head)
   const int g = (int)(seg % a.Hkv);
-  const int64_t row = seg / a.Hkv;
-  const int b = (int)(row / a.q_len), qi = (int)(row % a.q_len);
+  const int64_t qrow = seg / a.Hkv;
+  const int b = (int)(qrow / a.q_len), qi = (int)(qrow % a.q_len);
   const int cap = a.max_blocks * kBs;
   const int raw = __ldg(a.seq_lens + b);
+
+  // ---- coefficients: thread d sums N (d < 128) or P of its channel over the heads, and what
+  // the fp32 sums leave out (the error of each addition, found exactly)
+  {
+    const int d = threadIdx.x;
+    const uint16_t* q = a.q + (qrow * a.H + (int64_t)g * a.n_rep) * kDim + d % kDim;
+    float sum = 0.f, low = 0.f;
+    uint32_t any = 0;
+    for (int h0 = 0; h0 < a.n_rep; h0 += 8) {
+      uint32_t bits[8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) bits[h] = h0 + h < a.n_rep ? __ldg(q + (h0 + h) * kDim) : 0u;
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        any |= bits[h] & 0x7fffu;
+        const float v = __uint_as_float(bits[h] << 16);
+        const float x = d < kDim ? min_nan(v, 0.f) : max_nan(v, 0.f);
+        const float s = add_ieee(sum, x);
+        const float back = add_ieee(s, -sum);
+        low = add_ieee(low, add_ieee(add_ieee(sum, -add_ieee(s, -back)), add_ieee(x, -back)));
+        sum = s;
+      }
+    }
+    sh.coef[d] = sum;
+    sh.coef_low[d] = fabsf(sum) < INFINITY ? low : 0.f;
+    float size = fabsf(sum);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) size = add_ieee(size, __shfl_xor_sync(0xffffffffu, size, o));
+    any = __reduce_or_sync(0xffffffffu, any);
+    if (lane == 0) {
+      sh.size[warp] = size;
+      sh.any_q[warp] = any;
+    }
+    if (threadIdx.x == 0) sh.candidates = 0;
+  }
+
   const int len = clamp_len(raw, cap);
-  if (len != raw && g == 0 && qi == 0 && rank == 0 && threadIdx.x == 0)
+  if (len != raw && g == 0 && qi == 0 && cl.rank == 0 && threadIdx.x == 0)
     flag_status(a.dev_status, PKV_DEV_BAD_LENGTH);
   const int row_len = len - a.q_len + 1 + qi;
   const int n = row_len > 0 ? (row_len + kBs - 1) / kBs : 0;
@@ -285,204 +672,149 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   // Blocks [0, e0) and [e1, n) are always taken; the others compete for `want` places.
   const int e0 = a.num_sink, e1 = n - a.num_recent;
   const int want = K - a.num_sink - a.num_recent;
-  if (n <= K || want == 0) {
-    if (rank == 0)
-      for (int i = threadIdx.x; i < K; i += kSelThreads)
-        out[i] = n <= K ? (i < n ? i : -1) : (i < e0 ? i : e1 + (i - e0));
-    return;  // the whole cluster takes this way
+  if (cl.rank == 0) {
+    if (n <= K) {
+      for (int i = threadIdx.x; i < K; i += kSelThreads) out[i] = i < n ? i : -1;
+    } else {
+      for (int i = threadIdx.x; i < e0; i += kSelThreads) out[i] = i;
+      for (int i = threadIdx.x; i < a.num_recent; i += kSelThreads) out[e0 + want + i] = e1 + i;
+    }
   }
-  const int m = e1 - e0;  // > want
-  unsigned long long* key64 = sel_smem;                                  // [max_blocks]
-  uint32_t* key32 = reinterpret_cast<uint32_t*>(sel_smem + a.max_blocks);  // [max_blocks]
-  uint32_t* key32_0 = cluster.map_shared_rank(key32, 0);
-  unsigned int* amax_0 = cluster.map_shared_rank(sh.amax, 0);
-  cluster.sync();  // the first CTA's shared memory may be stored into from here on
+  if (n <= K || want == 0) return;  // the whole cluster takes this way
+  out += e0;
+  const int total = e1 - e0;  // > want
+  // This CTA's run of competing blocks: [first, first + m).
+  const int chunk = ((total + cl.size - 1) / cl.size + 7) & ~7;
+  const int first = e0 + cl.rank * chunk;
+  const int m = max(0, min(chunk, e1 - first));
+  unsigned long long* key64 = sel_smem;                                 // [chunk_cap]
+  uint32_t* key32 = reinterpret_cast<uint32_t*>(sel_smem + chunk_cap);  // [chunk_cap]
+  uint32_t* cand = key32 + chunk_cap;                                   // [chunk_cap]
+  const bool by_warp = cl.size == 1 && m <= 32 * kWarpKeys;
+  if (!by_warp)
+    for (int i = threadIdx.x; i < 4 * 256; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+  __syncthreads();
 
   // ---- fp32 scores
-  const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
-  const int half = lane >> 4, c = lane & 15;
-  const uint16_t* q = a.q + (row * a.H + (int64_t)g * a.n_rep) * kDim;
-  float coef[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  uint32_t q_bits = 0;
-  for (int h = 0; h < a.n_rep; ++h) {
-    const uint4 x = ld_nc_v4(q + h * kDim + 8 * c);
-    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+  Row row;
+  row.table = a.block_table + (int64_t)b * a.max_blocks + first;
+  row.sum = a.summaries + (int64_t)g * kSumBytes + lane * 16;
+  row.sum_stride = (int64_t)a.Hkv * kSumBytes;
+  row.num_blocks = a.num_blocks;
+  float coef[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q_bits |= v[i] & 0x7fff7fffu;
-      const float lo = bf16lo(v[i]), hi = bf16hi(v[i]);
-      // A NaN goes into both sums (a maximum or minimum would drop it).
-      coef[2 * i] = add_ieee(coef[2 * i], lo != lo ? lo : half ? max_ieee(lo, 0.f) : min_ieee(lo, 0.f));
-      coef[2 * i + 1] =
-          add_ieee(coef[2 * i + 1], hi != hi ? hi : half ? max_ieee(hi, 0.f) : min_ieee(hi, 0.f));
-    }
-  }
+  for (int i = 0; i < 8; ++i) coef[i] = sh.coef[8 * lane + i];
+  constexpr int kGroup = 8 * kRounds;
   uint32_t vmax = 0;  // two 16-bit maxima of |summary| as bits: NaN above infinity above all
-  const uint8_t* sum0 = a.summaries + (int64_t)g * kSumBytes + lane * 16;
-  const int64_t sum_stride = (int64_t)a.Hkv * kSumBytes;
-  for (int j0 = (rank * kSelWarps + warp) * 8; j0 < m; j0 += C * kSelWarps * 8) {
-    int blk = -1;
-    if (lane < 8 && j0 + lane < m) {
-      blk = __ldg(table + e0 + j0 + lane);
-      if (blk < 0 || (int64_t)blk >= a.num_blocks) {
-        blk = -1;
-        flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
-      }
+  uint32_t kmin = 0xffffffffu, kmax = 0;
+  auto entry = [&](int j) { return lane < kGroup && j + lane < m ? __ldg(row.table + j + lane) : -1; };
+  int next = entry(warp * kGroup);
+  for (int j0 = warp * kGroup; j0 < m; j0 += kSelWarps * kGroup) {
+    int blk = next;
+    next = entry(j0 + kSelWarps * kGroup);
+    if (lane < kGroup && j0 + lane < m && (blk < 0 || (int64_t)blk >= a.num_blocks)) {
+      blk = -1;
+      flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
     }
-    uint4 x[8];
+    uint4 x[kGroup];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < kGroup; ++u) {
       const int p = __shfl_sync(0xffffffffu, blk, u);
-      x[u] = p >= 0 ? ld_nc_v4(sum0 + p * sum_stride) : make_uint4(0, 0, 0, 0);
+      x[u] = p >= 0 ? ld_nc_v4(row.sum + p * row.sum_stride) : make_uint4(0, 0, 0, 0);
     }
-    float v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float s = 0.f;
+    for (int u0 = 0; u0 < kGroup; u0 += 8) {
+      float v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s = fma_ieee(coef[2 * i], bf16lo(w[i]), s);
-        s = fma_ieee(coef[2 * i + 1], bf16hi(w[i]), s);
-        vmax = __vmaxu2(vmax, w[i] & 0x7fff7fffu);
-      }
-      v[u] = s;
-    }
-    // Sums over the 32 lanes of all 8 at once: each step halves the blocks a lane holds.
-#pragma unroll
-    for (int o = 16, k = 4; o >= 4; o >>= 1, k >>= 1) {
-      const bool up = lane & o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= k) continue;
-        const float send = up ? v[i] : v[i + k];
-        const float keep = up ? v[i + k] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-      }
-    }
-    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
-    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-    const int u = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-    const bool bad = __shfl_sync(0xffffffffu, blk, u) < 0;
-    if ((lane & 3) == 0 && j0 + u < m) key32_0[j0 + u] = bad ? 0u : order_key(v[0]);
-  }
-  {
-    const uint32_t one = max(vmax & 0xffffu, vmax >> 16);
-    const uint32_t all = __reduce_max_sync(0xffffffffu, one);
-    if (lane == 0) amax_0[rank * kSelWarps + warp] = all;
-  }
-  cluster.sync();
-  if (rank) return;
-
-  // ---- the border
-  // sum_d P_d + |N_d| over the warp's 32 lanes, the same in every warp.
-  float size = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) size = add_ieee(size, fabsf(coef[i]));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) size = add_ieee(size, __shfl_xor_sync(0xffffffffu, size, o));
-  uint32_t top = 0;
-  for (int i = lane; i < C * kSelWarps; i += 32) top = max(top, sh.amax[i]);
-  top = __reduce_max_sync(0xffffffffu, top);
-  const float reach = mul_ieee(size, __uint_as_float(top << 16));  // bounds |score|, partial sums
-  const bool q_zero = __reduce_or_sync(0xffffffffu, q_bits) == 0;
-  int greater;
-  const uint32_t tau = kth_largest(key32, m, want, sh, &greater);
-  // Keys above `sure` are in, keys below `maybe` are out.
-  uint32_t maybe = 0, sure = kNanKey;
-  if (q_zero && reach == 0.f) {
-    maybe = sure = tau;  // every finite score is an exact zero
-  } else if (reach < 1e37f && tau != 0) {
-    // The added constant covers sums flushed to zero. (A reach that is not finite bounds
-    // nothing, and a tau of 0 is a bad block's key, not a score: every block is scored again.)
-    const float eps = reach * 0x1p-18f + 1e-35f;
-    const float x = __uint_as_float((tau & 0x80000000u) ? tau & 0x7fffffffu : ~tau);
-    // Rounded outward: one more unit of 2^-23 of the larger operand.
-    const float pad = 2.f * eps + (fabsf(x) + 2.f * eps) * 0x1p-22f;
-    maybe = order_key(x - pad);
-    sure = order_key(x + pad);
-  }
-  __shared__ int n_sure, n_maybe;
-  if (threadIdx.x == 0) n_sure = n_maybe = 0;
-  __syncthreads();
-  {
-    int s = 0, t = 0;
-    for (int i = threadIdx.x; i < m; i += kSelThreads) {
-      s += key32[i] > sure;
-      t += key32[i] >= maybe;
-    }
-    s = __reduce_add_sync(0xffffffffu, s);
-    t = __reduce_add_sync(0xffffffffu, t);
-    if (lane == 0) {
-      atomicAdd(&n_sure, s);
-      atomicAdd(&n_maybe, t);
-    }
-  }
-  __syncthreads();
-  uint32_t pass = maybe;  // keys from here on are taken
-  if (n_maybe > want) {
-    // More blocks in reach of the border than places: score them in fp64.
-    const int need = want - n_sure;
-    uint32_t* cand = reinterpret_cast<uint32_t*>(key64 + a.max_blocks) + a.max_blocks;
-    const int nc = compact(
-        m, sh, [&](int i) { return key32[i] >= maybe && key32[i] <= sure; },
-        [&](int r, int i) { cand[r] = i; });
-    for (int d = threadIdx.x; d < 2 * kDim; d += kSelThreads) {
-      double s = 0.0;
-      for (int h = 0; h < a.n_rep; ++h) {
-        const uint32_t bits = q[h * kDim + d % kDim];
-        const double x = widen_ieee(__uint_as_float(bits << 16));
-        s += x != x ? x : d < kDim ? (x < 0.0 ? x : 0.0) : (x > 0.0 ? x : 0.0);
-      }
-      coef64[d] = s;
-    }
-    __syncthreads();
-    for (int r = warp; r < nc; r += kSelWarps) {
-      const int blk = __ldg(table + e0 + cand[r]);
-      unsigned long long key = 0;  // a bad block's
-      if (blk >= 0 && (int64_t)blk < a.num_blocks) {
-        const uint4 x = ld_nc_v4(sum0 + blk * sum_stride);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        double s = 0.0;
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t w[4] = {x[u0 + u].x, x[u0 + u].y, x[u0 + u].z, x[u0 + u].w};
+        float s = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s = fma(coef64[8 * lane + 2 * i], widen_ieee(bf16lo(w[i])), s);
-          s = fma(coef64[8 * lane + 2 * i + 1], widen_ieee(bf16hi(w[i])), s);
+          s = fma_ieee(coef[2 * i], bf16lo(w[i]), s);
+          s = fma_ieee(coef[2 * i + 1], bf16hi(w[i]), s);
+          vmax = __vmaxu2(vmax, w[i] & 0x7fff7fffu);
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        key = order_key(s);
+        v[u] = s;
       }
-      if (lane == 0) key64[r] = key;
+      // Sums over the 32 lanes of all 8 at once: each step halves the blocks a lane holds.
+#pragma unroll
+      for (int o = 16, k = 4; o >= 4; o >>= 1, k >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i >= k) continue;
+          const float send = up ? v[i] : v[i + k];
+          const float keep = up ? v[i + k] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+      const int u = u0 + ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+      const bool bad = __shfl_sync(0xffffffffu, blk, u) < 0;
+      if ((lane & 3) == 0 && j0 + u < m) {
+        const uint32_t key = bad ? 0u : order_key(v[0]);
+        key32[j0 + u] = key;
+        kmin = min(kmin, key);
+        kmax = max(kmax, key);
+      }
     }
-    __syncthreads();
-    int above;
-    const unsigned long long edge = kth_largest(key64, nc, need, sh, &above);
-    // Above the edge: in. At the edge: the lower blocks, as many as there are places.
-    for (int r = threadIdx.x; r < nc; r += kSelThreads) key32[cand[r]] = key64[r] > edge ? 0xffffffffu : 0u;
-    __syncthreads();
-    compact(
-        nc, sh, [&](int r) { return key64[r] == edge; },
-        [&](int k, int r) { if (k < need - above) key32[cand[r]] = 0xffffffffu; });
-    pass = sure + 1;
   }
-  for (int i = threadIdx.x; i < e0; i += kSelThreads) out[i] = i;
-  compact(
-      m, sh, [&](int i) { return key32[i] >= pass; }, [&](int r, int i) { out[e0 + r] = e0 + i; });
-  for (int i = threadIdx.x; i < a.num_recent; i += kSelThreads) out[e0 + want + i] = e1 + i;
+
+  // ---- range of the keys and of the summaries, over the cluster
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(vmax & 0xffffu, vmax >> 16));
+  if (lane == 0) {
+    sh.lo[warp] = kmin;
+    sh.hi[warp] = kmax;
+    sh.amax[warp] = top;
+  }
+  __syncthreads();
+  if (by_warp && warp) return;
+  top = __reduce_max_sync(0xffffffffu, sh.amax[lane & 7]);
+  if (!by_warp) {
+    if (threadIdx.x == 0) {
+      uint32_t lo = 0xffffffffu, hi = 0;
+      for (int w = 0; w < kSelWarps; ++w) {
+        lo = min(lo, (uint32_t)sh.lo[w]);
+        hi = max(hi, (uint32_t)sh.hi[w]);
+      }
+      sh.pub[0][0] = ((unsigned long long)lo << 32) | hi;
+      sh.pub[0][1] = top;
+    }
+    cl.sync();
+    kmin = 0xffffffffu, kmax = 0;
+    for (int r = 0; r < cl.size; ++r) {
+      const unsigned long long both = cl.read(&sh.pub[0][0], r);
+      kmin = min(kmin, (uint32_t)(both >> 32));
+      kmax = max(kmax, (uint32_t)both);
+      top = max(top, (uint32_t)cl.read(&sh.pub[0][1], r));
+    }
+  }
+  float size = 0.f;
+  uint32_t any = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    size = add_ieee(size, sh.size[w]);
+    any |= sh.any_q[w];
+  }
+  const float reach = mul_ieee(size, __uint_as_float(top << 16));  // bounds |score|, partial sums
+  // A reach that is not finite bounds nothing. The added constant covers sums flushed to zero.
+  row.bounded = reach < 1e37f;
+  row.exact = row.bounded && (any == 0 || top == 0);
+  row.eps = row.exact ? 0.f : reach * ((float)(a.n_rep + 14) * 0x1p-24f) + 1e-35f;
+  if (by_warp)
+    select_by_warp(row, sh, key32, key64, cand, m, want, first, out);
+  else
+    select_by_cluster(row, sh, cl, key32, key64, cand, m, want, first, kmin, kmax, out);
 }
 
-cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int num_sms) {
-  const int64_t segs = (int64_t)a.B * a.q_len * a.Hkv;
-  if (segs == 0) return cudaSuccess;
-  // A cluster is as wide as it takes to give every SM two CTAs, as long as each of its CTAs
-  // has a round of 64 blocks to score.
-  int C = 1;
-  while (C < 8 && segs * C < 2 * num_sms && a.max_blocks > C * kSelWarps * 8) C *= 2;
-  const size_t smem = (size_t)a.max_blocks * 16;  // fp64 keys, fp32 keys, candidates
-  cudaError_t e = cudaFuncSetAttribute(select_blocks_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+template <int kRounds>
+static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cudaStream_t stream) {
+  const int chunk_cap = ((a.max_blocks + C - 1) / C + 7) & ~7;
+  const size_t smem = (size_t)chunk_cap * 16;  // fp64 keys, fp32 keys, candidates
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * C));
   cfg.blockDim = dim3(kSelThreads);
@@ -495,7 +827,22 @@ cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int n
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_blocks_kernel, a);
+  return cudaLaunchKernelEx(&cfg, select_blocks_kernel<kRounds>, a, chunk_cap);
+}
+
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int num_sms) {
+  const int64_t segs = (int64_t)a.B * a.q_len * a.Hkv;
+  if (segs == 0) return cudaSuccess;
+  // A cluster is as wide as it takes to give every SM two CTAs, as long as each of its CTAs
+  // has a round of 64 blocks to score, and wide enough that a CTA's keys stay within 16 KB.
+  int C = 1;
+  while (C < kMaxCluster && (a.max_blocks > 1024 * C ||
+                             (segs * C < 2 * num_sms && a.max_blocks > C * kSelWarps * 8)))
+    C *= 2;
+  // Two groups of 8 blocks in flight where a warp has several to go (few CTAs per SM then, so
+  // loads in flight are what counts); one where the registers buy resident CTAs.
+  if (a.max_blocks > 4 * 64 * C) return launch_select_n<2>(a, C, segs, stream);
+  return launch_select_n<1>(a, C, segs, stream);
 }
 
 }  // namespace pkv
