@@ -152,10 +152,10 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream) {
 // reduced across the lanes together. Selection needs exact order only at the border, so the
 // kernel bounds the fp32 error,
 //
-//   |score32 - score| <= eps = (n_rep + 14) 2^-24 (sum_d P_d + |N_d|) max |summary|
+//   |score32 - score| <= eps = 14 2^-24 (sum_d P_d + |N_d|) max |summary|
 //
-// (n_rep - 1 roundings in P and N, 8 in a lane's sum of products, 5 in the reduction, and
-// room for the bound's own), finds the K-th largest fp32 score tau to within a bin narrower
+// (one rounding in P and N, 5 in a lane's sum of products, 5 in the reduction, and room for
+// the bound's own), finds the K-th largest fp32 score tau to within a bin narrower
 // than eps, takes every block above the bin by more than 2 eps and none below it by more, and
 // scores the blocks between again in fp64 where they are more than the places left. The
 // result is that of fp64 scores, ties to the lower block, whatever the order of the fp32 sums.
@@ -235,6 +235,15 @@ struct Row {
   bool exact;            // every good block's score is exactly zero
 };
 
+// A bf16 value as a double from its bits (conversions run at the rate of the fp64 units):
+// the exponent's bias moves from 127 to 1023. Subnormals, infinities and NaN are converted.
+__device__ __forceinline__ double bf16_double(uint32_t bits) {  // the value in the high half
+  const uint32_t e = bits & 0x7f800000u;
+  if (e - 0x00800000u < 0x7f000000u)
+    return __hiloint2double((int)((bits & 0x80000000u) | (((bits & 0x7fff0000u) >> 3) + (896u << 20))), 0);
+  return widen_ieee(__uint_as_float(bits));
+}
+
 // Keys of up to 4 candidates in fp64, by a warp; key64[r] for the blocks cand[r].
 __device__ void score64(const Row& row, const SelShared& sh, const uint32_t* cand,
                         unsigned long long* key64, int n) {
@@ -255,7 +264,7 @@ __device__ void score64(const Row& row, const SelShared& sh, const uint32_t* can
     for (int r = 0; r < 4; ++r) {
       if (r >= n) break;
       const uint32_t w = i < 2 ? x[r].x : i < 4 ? x[r].y : i < 6 ? x[r].z : x[r].w;
-      s[r] = fma(k, widen_ieee(i & 1 ? bf16hi(w) : bf16lo(w)), s[r]);
+      s[r] = fma(k, bf16_double(i & 1 ? w & 0xffff0000u : w << 16), s[r]);
     }
   }
 #pragma unroll
@@ -284,9 +293,9 @@ __device__ __forceinline__ void border(const Row& row, uint32_t lo, uint32_t hi,
 }
 
 // Selection by one warp: the `want` best of the m <= 256 blocks with keys key32[0, m), in
-// ascending order, to out[i] = first + block. Lane l holds blocks l, l + 32, ...: a count of
-// the keys from a threshold on is 8 comparisons and one warp sum, so the K-th largest is found
-// bit by bit, from the highest bit in which the keys differ down to a bin narrower than eps.
+// ascending order, to out[i] = first + block. Lane l holds blocks l, l + 32, ...: counting the
+// keys from a threshold on takes 8 comparisons and a warp sum, so the K-th largest is found two
+// bits at a time, from the highest in which the keys differ down to a bin narrower than eps.
 __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* key32,
                                unsigned long long* key64, uint32_t* cand, int m, int want, int first,
                                int32_t* out) {
@@ -302,22 +311,28 @@ __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* ke
   }
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
-  auto count = [&](uint32_t from) {
-    int c = 0;
-#pragma unroll
-    for (int u = 0; u < kWarpKeys; ++u) c += k[u] >= from;
-    return (int)__reduce_add_sync(0xffffffffu, c);
-  };
   uint32_t lo = kmin, hi = kmin, maybe, sure;
   if (kmin != kmax && row.bounded) {
-    int bit = 31 - __clz((int)(kmin ^ kmax));
-    lo = kmin & ~((2u << bit) - 1);
-    for (;; --bit) {
-      const uint32_t from = lo | (1u << bit);
-      if (count(from) >= want) lo = from;
-      hi = lo | ((1u << bit) - 1);
-      if (bit == 0 || (lo != 0 && key_score(hi) - key_score(lo) <= row.eps)) break;
-    }
+    // Two bits a step: keys from each of three thresholds on are counted in the fields of one
+    // word (a count is at most 256).
+    int bits = 32 - __clz((int)(kmin ^ kmax));  // undecided bits
+    bits += bits & 1;
+    lo = bits < 32 ? kmin & ~((1u << bits) - 1) : 0u;
+    do {
+      bits -= 2;
+      uint32_t c = 0;
+#pragma unroll
+      for (int u = 0; u < kWarpKeys; ++u)
+        c += (k[u] >= (lo | (1u << bits))) + ((k[u] >= (lo | (2u << bits))) << 10) +
+             ((k[u] >= (lo | (3u << bits))) << 20);
+      c = __reduce_add_sync(0xffffffffu, c);
+      const uint32_t digit = (c >> 20) >= (uint32_t)want             ? 3
+                             : ((c >> 10) & 1023u) >= (uint32_t)want ? 2
+                             : (c & 1023u) >= (uint32_t)want         ? 1
+                                                                     : 0;
+      lo |= digit << bits;
+      hi = lo | ((1u << bits) - 1);
+    } while (bits && (lo == 0 || key_score(hi) - key_score(lo) > row.eps));
   }
   border(row, lo, hi, &maybe, &sure);
   uint32_t pass = maybe;
@@ -412,7 +427,9 @@ __device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kma
     cl.sync();
     // Thread t holds digit 255 - t, so that a prefix sum counts the larger digits.
     int own = 0;
-    for (int r = 0; r < cl.size; ++r) own += cl.read(&hist[pass][255 - threadIdx.x], r);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)  // all reads at once
+      if (r < cl.size) own += cl.read(&hist[pass][255 - threadIdx.x], r);
     int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -463,13 +480,13 @@ __device__ Counted count_cluster(int a, int c, int slot, SelShared& sh, const Cl
     sh.pub[slot][1] = sc;
   }
   cl.sync();
-  Counted t = {0, 0, 0};
-  for (int r = 0; r < cl.size; ++r) {
-    const int x = (int)cl.read(&sh.pub[slot][0], r);
-    if (r < cl.rank) t.before_a += x;
-    t.all_a += x;
-    t.all_c += (int)cl.read(&sh.pub[slot][1], r);
-  }
+  // Lane r reads CTA r's pair.
+  const int x = lane < cl.size ? (int)cl.read(&sh.pub[slot][0], lane) : 0;
+  const int y = lane < cl.size ? (int)cl.read(&sh.pub[slot][1], lane) : 0;
+  Counted t;
+  t.before_a = __reduce_add_sync(0xffffffffu, lane < cl.rank ? x : 0);
+  t.all_a = __reduce_add_sync(0xffffffffu, x);
+  t.all_c = __reduce_add_sync(0xffffffffu, y);
   return t;
 }
 
@@ -554,16 +571,21 @@ __device__ void select_by_cluster(const Row& row, SelShared& sh, const Cluster& 
       sh.pub[3][1] = sh.hi[0];
     }
     cl.sync();
-    int all = 0;
-    for (int r = 0; r < cl.size; ++r) all += (int)cl.read(&sh.pub[2][0], r);
+    const int theirs = lane < cl.size ? (int)cl.read(&sh.pub[2][0], lane) : 0;
+    const int all = __reduce_add_sync(0xffffffffu, theirs);
     if (all <= 32) {
       // Few: lane l of the first warp of every CTA takes the l-th of them all and ranks it.
       if (warp == 0) {
-        int owner = 0, at = lane;
-        for (; owner < cl.size; ++owner) {
-          const int theirs = (int)cl.read(&sh.pub[2][0], owner);
-          if (at < theirs) break;
-          at -= theirs;
+        int owner = cl.size, at = lane;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          const int have = __shfl_sync(0xffffffffu, theirs, r);
+          if (owner == cl.size && r < cl.size) {
+            if (at < have)
+              owner = r;
+            else
+              at -= have;
+          }
         }
         const bool have = owner < cl.size;
         const unsigned long long mine = have ? cl.read(key64 + at, owner) : 0;
@@ -649,8 +671,12 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
         sum = s;
       }
     }
+    const float all = add_ieee(sum, low);
+    const bool finite = fabsf(all) < INFINITY;
+    low = finite ? add_ieee(low, add_ieee(sum, -all)) : 0.f;
+    sum = finite ? all : sum;
     sh.coef[d] = sum;
-    sh.coef_low[d] = fabsf(sum) < INFINITY ? low : 0.f;
+    sh.coef_low[d] = low;
     float size = fabsf(sum);
 #pragma unroll
     for (int o = 16; o; o >>= 1) size = add_ieee(size, __shfl_xor_sync(0xffffffffu, size, o));
@@ -701,26 +727,31 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   row.sum = a.summaries + (int64_t)g * kSumBytes + lane * 16;
   row.sum_stride = (int64_t)a.Hkv * kSumBytes;
   row.num_blocks = a.num_blocks;
-  float coef[8];
+  uint64_t coef[4];  // of channels 2i and 2i + 1
 #pragma unroll
-  for (int i = 0; i < 8; ++i) coef[i] = sh.coef[8 * lane + i];
+  for (int i = 0; i < 4; ++i) coef[i] = f2pack(sh.coef[8 * lane + 2 * i], sh.coef[8 * lane + 2 * i + 1]);
   constexpr int kGroup = 8 * kRounds;
-  uint32_t vmax = 0;  // two 16-bit maxima of |summary| as bits: NaN above infinity above all
+  uint32_t vmax = 0;  // the largest |summary| of the even and the odd channels (NaN: the largest bits)
   uint32_t kmin = 0xffffffffu, kmax = 0;
-  auto entry = [&](int j) { return lane < kGroup && j + lane < m ? __ldg(row.table + j + lane) : -1; };
+  // Table entries of a group, one per lane; a group that ends the run repeats its last block,
+  // so that every load below is unconditional and all of them are in flight together.
+  auto entry = [&](int j) { return j < m ? __ldg(row.table + min(j + (lane & (kGroup - 1)), m - 1)) : 0; };
   int next = entry(warp * kGroup);
   for (int j0 = warp * kGroup; j0 < m; j0 += kSelWarps * kGroup) {
-    int blk = next;
+    const int blk = next;
     next = entry(j0 + kSelWarps * kGroup);
-    if (lane < kGroup && j0 + lane < m && (blk < 0 || (int64_t)blk >= a.num_blocks)) {
-      blk = -1;
-      flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
-    }
+    const bool bad = blk < 0 || (int64_t)blk >= a.num_blocks;
+    const int from = bad ? 0 : blk;
     uint4 x[kGroup];
 #pragma unroll
-    for (int u = 0; u < kGroup; ++u) {
-      const int p = __shfl_sync(0xffffffffu, blk, u);
-      x[u] = p >= 0 ? ld_nc_v4(row.sum + p * row.sum_stride) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < kGroup; ++u)
+      x[u] = ld_nc_v4(row.sum + __shfl_sync(0xffffffffu, from, u) * row.sum_stride);
+    const unsigned bad_mask = __ballot_sync(0xffffffffu, bad);
+    if (bad_mask) {  // block 0 stood in for them: it must not count in vmax
+      if (bad) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u)
+        if (bad_mask >> u & 1) x[u] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u0 = 0; u0 < kGroup; u0 += 8) {
@@ -728,14 +759,14 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const uint32_t w[4] = {x[u0 + u].x, x[u0 + u].y, x[u0 + u].z, x[u0 + u].w};
-        float s = 0.f;
+        uint64_t s = 0;  // two sums of four products
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s = fma_ieee(coef[2 * i], bf16lo(w[i]), s);
-          s = fma_ieee(coef[2 * i + 1], bf16hi(w[i]), s);
-          vmax = __vmaxu2(vmax, w[i] & 0x7fff7fffu);
+          s = ffma2(coef[i], f2pack(bf16lo(w[i]), bf16hi(w[i])), s);
+          vmax = max2(vmax, w[i] & 0x7fff7fffu);
         }
-        v[u] = s;
+        const float2 both = f2unpack(s);
+        v[u] = both.x + both.y;
       }
       // Sums over the 32 lanes of all 8 at once: each step halves the blocks a lane holds.
 #pragma unroll
@@ -752,9 +783,8 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
       v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
       v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
       const int u = u0 + ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-      const bool bad = __shfl_sync(0xffffffffu, blk, u) < 0;
       if ((lane & 3) == 0 && j0 + u < m) {
-        const uint32_t key = bad ? 0u : order_key(v[0]);
+        const uint32_t key = bad_mask >> u & 1 ? 0u : order_key(v[0]);
         key32[j0 + u] = key;
         kmin = min(kmin, key);
         kmax = max(kmax, key);
@@ -785,13 +815,11 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
       sh.pub[0][1] = top;
     }
     cl.sync();
-    kmin = 0xffffffffu, kmax = 0;
-    for (int r = 0; r < cl.size; ++r) {
-      const unsigned long long both = cl.read(&sh.pub[0][0], r);
-      kmin = min(kmin, (uint32_t)(both >> 32));
-      kmax = max(kmax, (uint32_t)both);
-      top = max(top, (uint32_t)cl.read(&sh.pub[0][1], r));
-    }
+    const int r = lane < cl.size ? lane : 0;  // lane r reads CTA r's numbers
+    const unsigned long long both = cl.read(&sh.pub[0][0], r);
+    kmin = __reduce_min_sync(0xffffffffu, (uint32_t)(both >> 32));
+    kmax = __reduce_max_sync(0xffffffffu, (uint32_t)both);
+    top = __reduce_max_sync(0xffffffffu, (uint32_t)cl.read(&sh.pub[0][1], r));
   }
   float size = 0.f;
   uint32_t any = 0;
@@ -804,7 +832,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   // A reach that is not finite bounds nothing. The added constant covers sums flushed to zero.
   row.bounded = reach < 1e37f;
   row.exact = row.bounded && (any == 0 || top == 0);
-  row.eps = row.exact ? 0.f : reach * ((float)(a.n_rep + 14) * 0x1p-24f) + 1e-35f;
+  row.eps = row.exact ? 0.f : reach * (14.f * 0x1p-24f) + 1e-35f;
   if (by_warp)
     select_by_warp(row, sh, key32, key64, cand, m, want, first, out);
   else
