@@ -166,6 +166,8 @@ namespace {
 constexpr int kSelWarps = 8;
 constexpr int kSelThreads = 32 * kSelWarps;
 constexpr int kMaxCluster = 8;
+constexpr int kDigitBits = 9;             // two digits of this size decide most 32-bit searches
+constexpr int kDigits = 1 << kDigitBits;  // two per thread
 constexpr int kWarpKeys = 8;              // keys of a lane where one warp selects
 constexpr uint32_t kNanKey = 0xfffffffeu;
 constexpr uint32_t kTaken = 0xffffffffu;  // above every score's key
@@ -202,7 +204,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // is enough.
 struct SelShared {
   float coef[2 * kDim], coef_low[2 * kDim];  // N, then P: their fp32 sums and what those left out
-  int hist[4 + 8][256];                  // digit counts: 4 passes over 32-bit keys, 8 over 64
+  int hist[4 + 8][kDigits];              // digit counts: 4 passes over 32-bit keys, 8 over 64
   unsigned long long pub[5][2];          // a pair of numbers per exchange
   unsigned long long lo[kSelWarps], hi[kSelWarps];
   float size[kSelWarps];
@@ -235,13 +237,13 @@ struct Row {
   bool exact;            // every good block's score is exactly zero
 };
 
-// A bf16 value as a double from its bits (conversions run at the rate of the fp64 units):
-// the exponent's bias moves from 127 to 1023. Subnormals, infinities and NaN are converted.
-__device__ __forceinline__ double bf16_double(uint32_t bits) {  // the value in the high half
-  const uint32_t e = bits & 0x7f800000u;
-  if (e - 0x00800000u < 0x7f000000u)
-    return __hiloint2double((int)((bits & 0x80000000u) | (((bits & 0x7fff0000u) >> 3) + (896u << 20))), 0);
-  return widen_ieee(__uint_as_float(bits));
+// An fp32 value as a double from its bits (conversions run at the rate of the fp64 units): the
+// exponent's bias moves from 127 to 1023. Subnormals, infinities and NaN are converted.
+__device__ __forceinline__ double widen_bits(uint32_t bits) {
+  if ((bits & 0x7f800000u) - 0x00800000u < 0x7f000000u)
+    return __hiloint2double((int)((bits & 0x80000000u) | (((bits & 0x7fffffffu) >> 3) + (896u << 20))),
+                            (int)(bits << 29));
+  return (bits & 0x7fffffffu) ? widen_ieee(__uint_as_float(bits)) : 0.0;
 }
 
 // Keys of up to 4 candidates in fp64, by a warp; key64[r] for the blocks cand[r].
@@ -256,24 +258,33 @@ __device__ void score64(const Row& row, const SelShared& sh, const uint32_t* can
     good[r] = blk >= 0 && (int64_t)blk < row.num_blocks;
     x[r] = good[r] ? ld_nc_v4(row.sum + blk * row.sum_stride) : make_uint4(0, 0, 0, 0);
   }
-  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  double k[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const double k = widen_ieee(sh.coef[8 * lane + i]) + widen_ieee(sh.coef_low[8 * lane + i]);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (r >= n) break;
-      const uint32_t w = i < 2 ? x[r].x : i < 4 ? x[r].y : i < 6 ? x[r].z : x[r].w;
-      s[r] = fma(k, bf16_double(i & 1 ? w & 0xffff0000u : w << 16), s[r]);
-    }
-  }
+  for (int i = 0; i < 8; ++i)
+    k[i] = widen_bits(__float_as_uint(sh.coef[8 * lane + i])) +
+           widen_bits(__float_as_uint(sh.coef_low[8 * lane + i]));
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (r >= n) break;
+    const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+    double s[4];  // short chains: an fp64 operation takes long
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
-    if (lane == 0) key64[r] = good[r] ? order_key(s[r]) : 0ull;
+    for (int i = 0; i < 4; ++i)
+      s[i] = fma(k[2 * i], widen_bits(w[i] << 16), k[2 * i + 1] * widen_bits(w[i] & 0xffff0000u));
+    s[0] = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+    if (lane == 0) key64[r] = good[r] ? order_key(s[0]) : 0ull;
   }
+}
+
+// Low bits of the keys that need not be decided: a bin of 2^bits keys in [kmin, kmax] is
+// narrower than eps, for its scores are at most the largest magnitude's 2^-23 apart.
+__device__ __forceinline__ int spare_bits(const Row& row, uint32_t kmin, uint32_t kmax) {
+  if (kmin == 0 || row.exact) return 0;  // bad blocks among them
+  const uint32_t top = __float_as_uint(fmaxf(fabsf(key_score(kmin)), fabsf(key_score(kmax)))) >> 23;
+  const int bits = (int)(__float_as_uint(row.eps) >> 23) - ((int)top - 23);
+  return min(max(bits, 0), 31);
 }
 
 // [maybe, sure] from the bin [lo, hi] that holds the K-th largest key: keys above `sure` are
@@ -315,6 +326,7 @@ __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* ke
   if (kmin != kmax && row.bounded) {
     // Two bits a step: keys from each of three thresholds on are counted in the fields of one
     // word (a count is at most 256).
+    const int spare = spare_bits(row, kmin, kmax);
     int bits = 32 - __clz((int)(kmin ^ kmax));  // undecided bits
     bits += bits & 1;
     lo = bits < 32 ? kmin & ~((1u << bits) - 1) : 0u;
@@ -331,8 +343,8 @@ __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* ke
                              : (c & 1023u) >= (uint32_t)want         ? 1
                                                                      : 0;
       lo |= digit << bits;
-      hi = lo | ((1u << bits) - 1);
-    } while (bits && (lo == 0 || key_score(hi) - key_score(lo) > row.eps));
+    } while (bits > spare);
+    hi = lo | ((1u << bits) - 1);
   }
   border(row, lo, hi, &maybe, &sure);
   uint32_t pass = maybe;
@@ -407,29 +419,35 @@ struct Bin {
 };
 
 // The k-th largest of the cluster's keys (this CTA's are keys[0, n); all are in [kmin, kmax])
-// to within a bin that `done` accepts, by 8 bits at a time below the bits they share. Every
-// pass counts digits in its own histogram hist[pass], zero beforehand.
+// to within a bin of 2^spare values, or one that `done` accepts, by 9 bits at a time below the
+// bits they share. Every pass counts digits in its own histogram hist[pass], zero beforehand.
 template <typename Key, typename Done>
-__device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kmax, int (*hist)[256],
-                                SelShared& sh, const Cluster& cl, Done done) {
+__device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kmax, int spare,
+                                int (*hist)[kDigits], SelShared& sh, const Cluster& cl, Done done) {
   Bin<Key> b = {kmin, kmax, 0, 0};
   if (kmin == kmax) return b;
   const int top = 8 * (int)sizeof(Key) - 1 -
                   (sizeof(Key) == 8 ? __clzll((long long)(kmin ^ kmax)) : __clz((int)(kmin ^ kmax)));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int pass = 0, high = top;; ++pass) {
-    const int shift = high > 7 ? high - 7 : 0;  // digit: bits [shift, high]
+    const int shift = high >= kDigitBits ? high - kDigitBits + 1 : 0;  // digit: bits [shift, high]
     const Key mask = (Key)((1u << (high - shift + 1)) - 1);
     for (int i = threadIdx.x; i < n; i += kSelThreads) {
       const Key key = keys[i];
       if (key >= b.lo && key <= b.hi) atomicAdd(&hist[pass][(int)((key >> shift) & mask)], 1);
     }
     cl.sync();
-    // Thread t holds digit 255 - t, so that a prefix sum counts the larger digits.
-    int own = 0;
+    // Thread t holds digits 511 - 2t and 510 - 2t, so that a prefix sum counts the larger ones.
+    int upper = 0, lower = 0;
+    const int d = kDigits - 2 - 2 * threadIdx.x;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)  // all reads at once
-      if (r < cl.size) own += cl.read(&hist[pass][255 - threadIdx.x], r);
+    for (int r = 0; r < kMaxCluster; ++r) {  // all reads at once
+      if (r >= cl.size) continue;
+      const int2 two = cl.read(reinterpret_cast<int2*>(&hist[pass][d]), r);
+      lower += two.x;
+      upper += two.y;
+    }
+    const int own = upper + lower;
     int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -439,11 +457,13 @@ __device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kma
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
     int before = b.above + incl - own;
-    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) before += w < warp ? sh.warp_sum[w] : 0;
     if (before < k && k <= before + own) {  // one thread
-      sh.digit = 255 - threadIdx.x;
-      sh.above = before;
-      sh.inside = own;
+      const bool up = k <= before + upper;
+      sh.digit = d + up;
+      sh.above = up ? before : before + upper;
+      sh.inside = up ? upper : lower;
     }
     __syncthreads();
     const Key base = (b.lo & ~((mask << shift) | (((Key)1 << shift) - 1))) | ((Key)sh.digit << shift);
@@ -451,7 +471,7 @@ __device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kma
     b.hi = base | (((Key)1 << shift) - 1);
     b.above = sh.above;
     b.inside = sh.inside;
-    if (shift == 0 || done(b)) return b;
+    if (shift <= spare || done(b)) return b;
     high = shift - 1;
   }
 }
@@ -521,9 +541,8 @@ __device__ void select_by_cluster(const Row& row, SelShared& sh, const Cluster& 
   uint32_t lo = 0, hi = 0, maybe, sure;
   if (row.bounded) {
     const Bin<uint32_t> bin = kth_largest<uint32_t>(
-        key32, m, want, kmin, kmax, sh.hist, sh, cl, [&](const Bin<uint32_t>& x) {
-          return x.lo != 0 && key_score(x.hi) - key_score(x.lo) <= row.eps;
-        });
+        key32, m, want, kmin, kmax, spare_bits(row, kmin, kmax), sh.hist, sh, cl,
+        [](const Bin<uint32_t>&) { return false; });
     lo = bin.lo;
     hi = bin.hi;
   }
@@ -538,7 +557,7 @@ __device__ void select_by_cluster(const Row& row, SelShared& sh, const Cluster& 
   if (t.all_a > want) {
     // More blocks in reach of the border than places: score them in fp64.
     const int need = want - t.all_c;
-    for (int i = threadIdx.x; i < 8 * 256; i += kSelThreads) (&sh.hist[4][0])[i] = 0;
+    for (int i = threadIdx.x; i < 8 * kDigits; i += kSelThreads) (&sh.hist[4][0])[i] = 0;
     for (int i = threadIdx.x; i < m; i += kSelThreads)
       if (key32[i] >= maybe && key32[i] <= sure) cand[atomicAdd(&sh.candidates, 1)] = i;
     __syncthreads();
@@ -607,7 +626,7 @@ __device__ void select_by_cluster(const Row& row, SelShared& sh, const Cluster& 
       }
       // All keys of the bin are taken, or (one value) as many of the lowest blocks as it takes.
       const Bin<unsigned long long> bin = kth_largest<unsigned long long>(
-          key64, nc, need, lo64, hi64, sh.hist + 4, sh, cl,
+          key64, nc, need, lo64, hi64, 0, sh.hist + 4, sh, cl,
           [&](const Bin<unsigned long long>& x) { return x.above + x.inside == need; });
       int at_edge = 0;
       for (int r = threadIdx.x; r < nc; r += kSelThreads) {
@@ -636,8 +655,8 @@ __device__ void select_by_cluster(const Row& row, SelShared& sh, const Cluster& 
 
 // kRounds: groups of 8 blocks whose summaries a warp has in flight at a time.
 template <int kRounds>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid_constant__ SelectArgs a,
-                                                                    int chunk_cap) {
+__global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
+    select_blocks_kernel(const __grid_constant__ SelectArgs a, int chunk_cap) {
   extern __shared__ unsigned long long sel_smem[];
   __shared__ SelShared sh;
   const Cluster cl = {(int)cg::this_cluster().num_blocks(), (int)cg::this_cluster().block_rank()};
@@ -718,7 +737,7 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const __grid
   uint32_t* cand = key32 + chunk_cap;                                   // [chunk_cap]
   const bool by_warp = cl.size == 1 && m <= 32 * kWarpKeys;
   if (!by_warp)
-    for (int i = threadIdx.x; i < 4 * 256; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < 4 * kDigits; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
   __syncthreads();
 
   // ---- fp32 scores
