@@ -8,6 +8,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes as C
+from array import array
 
 import numpy as np
 import torch
@@ -78,6 +79,26 @@ def check_current_device(device) -> None:
     if device.type == "cuda" and device.index != torch.cuda.current_device():
         raise ValueError(f"tensors are on {device} but the current CUDA device is "
                          f"cuda:{torch.cuda.current_device()}; call under torch.cuda.device(...)")
+
+
+# The same two checks by device index, for the calls of a decode step whose kernels take a few
+# microseconds: comparing torch.device objects tensor by tensor takes longer than the rest of
+# a call's checks together.
+def _check_gpu(index, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _launch_stream(index, stream=None):
+    """The raw stream of a launch on device `index`, which must be the current one."""
+    current = torch.cuda.current_device()
+    if index != current:
+        raise ValueError(f"tensors are on cuda:{index} but the current CUDA device is "
+                         f"cuda:{current}; call under torch.cuda.device(...)")
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(current) if _raw_stream is not None else _stream()
 
 
 def check_shape(t, shape, name) -> None:
@@ -497,66 +518,78 @@ def kv_cache_write_fp8(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, d
 
 
 def _rope_rows(t, T, d, name):
-    """Token stride of rows [T, heads, d]: bf16 on the GPU, the heads of a token contiguous,
-    tokens any multiple of 8 elements apart (a slice of a projection's output will do)."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16):
+    """(heads, token stride) of rows [T, heads, d]: bf16 on the GPU, the heads of a token
+    contiguous, tokens any multiple of 8 elements apart (a slice of a projection's output
+    will do)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.is_cuda):
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
-        raise ValueError(f"{name} has shape {_shape_str(t.shape)}, expected [{T}, heads, {d}]")
-    heads = t.shape[1]
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d:
+        raise ValueError(f"{name} has shape {_shape_str(shape)}, expected [{T}, heads, {d}]")
+    heads = shape[1]
     st = t.stride()
     if st[2] != 1 or (heads > 1 and st[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st[0] if T > 1 else heads * d
+    return heads, st[0] if T > 1 else heads * d
 
 
 def _axis_array(pair_axis, rope_dim):
-    """pair_axis as the int32 host array the library reads (None: NULL, every pair axis 0)."""
+    """(array, address) of pair_axis as the int32 host array the library reads; None: NULL,
+    every pair axis 0. The array must outlive the call."""
     if pair_axis is None:
-        return None
-    arr = np.ascontiguousarray(pair_axis, dtype=np.int32)
-    if arr.shape != (rope_dim // 2,):
+        return None, None
+    if isinstance(pair_axis, (list, tuple)):
+        arr = array("i", pair_axis)
+        n, address = len(arr), arr.buffer_info()[0]
+    else:
+        arr = np.ascontiguousarray(pair_axis, dtype=np.int32)
+        n, address = arr.size if arr.ndim == 1 else -1, _np_ptr(arr)
+    if n != rope_dim // 2:
         raise ValueError(f"pair_axis must have rope_dim / 2 = {rope_dim // 2} entries")
-    return arr
+    return arr, address
 
 
 def _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions, slot_mapping, pair_axis, q_out,
-                 dev_status):
-    """Checks shared by the two rotary writes; returns q_out and the C arguments from q_out
-    to slot_mapping's sizes (the caches go in front, dev_status and the stream behind)."""
+                 dev_status, stream):
+    """Checks shared by the two rotary writes; returns q_out, the device index, and the C
+    arguments from q_out to pair_axis (the caches go in front, `interleaved` behind) and from
+    slot_mapping to the stream, with the pair_axis array that the call must keep."""
     nb, bs, hkv, d = _cache_dims(k_cache, "k_cache")
     check_shape(v_cache, (nb, bs, hkv, d), "v_cache")
     _dev_i32(slot_mapping, "slot_mapping")
     T = slot_mapping.numel()
-    qs, ks, vs = _rope_rows(q, T, d, "q"), _rope_rows(k, T, d, "k"), _rope_rows(v, T, d, "v")
-    H = q.shape[1]
-    if k.shape[1] != hkv or v.shape[1] != hkv:
+    H, qs = _rope_rows(q, T, d, "q")
+    kh, ks = _rope_rows(k, T, d, "k")
+    vh, vs = _rope_rows(v, T, d, "v")
+    if kh != hkv or vh != hkv:
         raise ValueError(f"k and v must have the cache's {hkv} heads")
     _f32_dev(rope_table, "rope_table")
     if rope_table.dim() != 2:
         raise ValueError("rope_table must be [max_pos, rope_dim]")
     max_pos, rope_dim = rope_table.shape
     _dev_i32(positions, "positions")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.shape != ((T,) if positions.dim() == 1 else (axes, T)):
-        raise ValueError(f"positions must be [T={T}] or [axes, T={T}], "
-                         f"got {_shape_str(positions.shape)}")
+    shape = positions.shape
+    axes = 1 if len(shape) == 1 else shape[0]
+    if shape != ((T,) if len(shape) == 1 else (axes, T)):
+        raise ValueError(f"positions must be [T={T}] or [axes, T={T}], got {_shape_str(shape)}")
     if q_out is None:
         q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        qos = H * d
     else:
-        if not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    qos = _rope_rows(q_out, T, d, "q_out")
-    dev = k_cache.device
-    check_same_device(dev, v_cache=v_cache, q=q, k=k, v=v, rope_table=rope_table,
-                      positions=positions, slot_mapping=slot_mapping, q_out=q_out)
-    check_current_device(dev)
-    status_buffer(dev_status, dev)
-    arr = _axis_array(pair_axis, rope_dim)
-    args = (_ptr(q_out), qos, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(rope_table), max_pos,
-            rope_dim, _ptr(positions), axes, None if arr is None else _np_ptr(arr))
-    sizes = (_ptr(slot_mapping), T, nb, bs, H, hkv, d, _ptr(dev_status))
-    return q_out, args, sizes, arr
+        heads, qos = _rope_rows(q_out, T, d, "q_out")
+        if heads != H:
+            raise ValueError(f"q_out must have q's {H} heads")
+    index = k_cache.get_device()
+    _check_gpu(index, v_cache=v_cache, q=q, k=k, v=v, rope_table=rope_table, positions=positions,
+               slot_mapping=slot_mapping, q_out=q_out)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, k_cache.device)
+    arr, address = _axis_array(pair_axis, rope_dim)
+    args = (q_out.data_ptr(), qos, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            rope_table.data_ptr(), max_pos, rope_dim, positions.data_ptr(), axes, address)
+    sizes = (slot_mapping.data_ptr(), T, nb, bs, H, hkv, d, _ptr(dev_status), raw)
+    return q_out, index, args, sizes, arr
 
 
 def rope_kv_cache_write(k_cache, v_cache, q, k, v, rope_table, positions, slot_mapping,
@@ -571,10 +604,10 @@ def rope_kv_cache_write(k_cache, v_cache, q, k, v, rope_table, positions, slot_m
     i + rope_dim / 2. Returns the rotated q (`q_out`, which may be q itself)."""
     _dev_bf16(k_cache, "k_cache")
     _dev_bf16(v_cache, "v_cache")
-    q_out, args, sizes, _keep = _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions,
-                                             slot_mapping, pair_axis, q_out, dev_status)
-    check(load().pkv_rope_kv_cache_write(_ptr(k_cache), _ptr(v_cache), *args, int(bool(interleaved)),
-                                         *sizes, _stream(stream)), "pkv_rope_kv_cache_write")
+    q_out, _, args, sizes, _keep = _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions,
+                                                slot_mapping, pair_axis, q_out, dev_status, stream)
+    check(load().pkv_rope_kv_cache_write(k_cache.data_ptr(), v_cache.data_ptr(), *args,
+                                         int(bool(interleaved)), *sizes), "pkv_rope_kv_cache_write")
     return q_out
 
 
@@ -587,15 +620,16 @@ def rope_kv_cache_write_fp8(k_cache, v_cache, k_scale, v_scale, q, k, v, rope_ta
     _fp8_cache(v_cache, "v_cache")
     _f32_dev(k_scale, "k_scale")
     _f32_dev(v_scale, "v_scale")
-    q_out, args, sizes, _keep = _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions,
-                                             slot_mapping, pair_axis, q_out, dev_status)
+    q_out, index, args, sizes, _keep = _rope_inputs(
+        k_cache, v_cache, q, k, v, rope_table, positions, slot_mapping, pair_axis, q_out, dev_status,
+        stream)
     nb, bs, hkv, _ = k_cache.shape
     check_shape(k_scale, (nb, hkv, bs), "k_scale")
     check_shape(v_scale, (nb, hkv, bs), "v_scale")
-    check_same_device(k_cache.device, k_scale=k_scale, v_scale=v_scale)
+    _check_gpu(index, k_scale=k_scale, v_scale=v_scale)
     check(load().pkv_rope_kv_cache_write_fp8(
-        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), *args, int(bool(interleaved)),
-        *sizes, _stream(stream)), "pkv_rope_kv_cache_write_fp8")
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *args,
+        int(bool(interleaved)), *sizes), "pkv_rope_kv_cache_write_fp8")
     return q_out
 
 
@@ -613,23 +647,23 @@ def kv_cache_read_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=No
     check_shape(k_scale, (nb, hkv, bs), "k_scale")
     check_shape(v_scale, (nb, hkv, bs), "v_scale")
     T = slot_mapping.numel()
-    dev = k_cache.device
-    outs = []
+    if k_out is None:
+        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=dev)
         _dev_bf16(t, n)
         check_shape(t, (T, hkv, d), n)
-        outs.append(t)
-    k_out, v_out = outs
-    check_same_device(dev, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                      slot_mapping=slot_mapping, k_out=k_out, v_out=v_out)
-    check_current_device(dev)
-    status_buffer(dev_status, dev)
-    check(load().pkv_kv_cache_read_fp8(_ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache),
-                                       _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping), T, nb, bs,
-                                       hkv, d, _ptr(dev_status), _stream(stream)),
-          "pkv_kv_cache_read_fp8")
+    index = k_cache.get_device()
+    _check_gpu(index, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, slot_mapping=slot_mapping,
+               k_out=k_out, v_out=v_out)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, k_cache.device)
+    check(load().pkv_kv_cache_read_fp8(
+        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), T, nb, bs, hkv, d,
+        _ptr(dev_status), raw), "pkv_kv_cache_read_fp8")
     return k_out, v_out
 
 
@@ -760,15 +794,16 @@ def update_block_summaries(summaries, k_cache, block_table, seq_lens, num_new, m
     B = num_new.numel()
     _table_and_lens(block_table, seq_lens, B)
     check_shape(num_new, (B,), "num_new")
-    dev = k_cache.device
-    check_same_device(dev, summaries=summaries, block_table=block_table, seq_lens=seq_lens,
-                      num_new=num_new)
-    check_current_device(dev)
-    status_buffer(dev_status, dev)
+    index = k_cache.get_device()
+    _check_gpu(index, summaries=summaries, block_table=block_table, seq_lens=seq_lens,
+               num_new=num_new)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, k_cache.device)
     check(load().pkv_update_block_summaries(
-        _ptr(summaries), _ptr(k_cache), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
-        _ptr(num_new), int(max_new), B, hkv, d, bs, nb, _ptr(dev_status), _stream(stream)),
-        "pkv_update_block_summaries")
+        summaries.data_ptr(), k_cache.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), num_new.data_ptr(), int(max_new), B, hkv, d, bs, nb, _ptr(dev_status),
+        raw), "pkv_update_block_summaries")
 
 
 def _query_rows(q):
@@ -797,22 +832,23 @@ def select_blocks(q, summaries, block_table, seq_lens, num_selected: int, num_si
     _table_and_lens(block_table, seq_lens, B)
     if num_selected < 1:
         raise ValueError("num_selected must be positive")
-    dev = q.device
     shape = (B, hkv, num_selected) if q.dim() == 3 else (B, Q, hkv, num_selected)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=dev)
+        out = torch.empty(shape, dtype=torch.int32, device=q.device)
     else:
         _dev_i32(out, "out")
         check_shape(out, shape, "out")
-    check_same_device(dev, summaries=summaries, block_table=block_table, seq_lens=seq_lens, out=out)
-    check_current_device(dev)
-    status_buffer(dev_status, dev)
+    index = q.get_device()
+    _check_gpu(index, summaries=summaries, block_table=block_table, seq_lens=seq_lens, out=out)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, q.device)
     if Q == 0:
         return out
     check(load().pkv_select_blocks(
-        _ptr(out), _ptr(q), _ptr(summaries), _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), B, Q, H, hkv, d, 128, nb, num_selected, num_sink, num_recent,
-        _ptr(dev_status), _stream(stream)), "pkv_select_blocks")
+        out.data_ptr(), q.data_ptr(), summaries.data_ptr(), block_table.data_ptr(),
+        block_table.shape[1], seq_lens.data_ptr(), B, Q, H, hkv, d, 128, nb, num_selected, num_sink,
+        num_recent, _ptr(dev_status), raw), "pkv_select_blocks")
     return out
 
 
@@ -839,10 +875,11 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_table, seq_lens, bl
     K = block_indices.shape[-1] if block_indices.dim() else 0
     lead = tuple(q.shape[:-2])
     check_shape(block_indices, lead + (hkv, K), "block_indices")
+    index = q.get_device()
+    _check_gpu(index, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
+               block_indices=block_indices)
+    raw = _launch_stream(index, stream)
     dev = q.device
-    check_same_device(dev, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                      seq_lens=seq_lens, block_indices=block_indices)
-    check_current_device(dev)
     out = out_buffer(out, q.shape, out_dtype, dev)
     lse_buffer(lse, lead + (H,), dev)
     status_buffer(dev_status, dev)
@@ -852,10 +889,10 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_table, seq_lens, bl
     workspace, ws_bytes = workspace_buffer(workspace,
                                            decode_sparse_workspace_size(B, Q, H, hkv, d), dev)
     check(load().pkv_paged_attention_decode_sparse(
-        _ptr(out), code, _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), _ptr(block_indices), K, B, Q, H, hkv, d, bs, nb,
-        float(scale), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream)),
-        "pkv_paged_attention_decode_sparse")
+        out.data_ptr(), code, _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), block_indices.data_ptr(),
+        K, B, Q, H, hkv, d, bs, nb, float(scale), workspace.data_ptr(), ws_bytes, _ptr(dev_status),
+        raw), "pkv_paged_attention_decode_sparse")
     return out
 
 

@@ -44,15 +44,16 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 
 // ------------------------------------------------------------------ summaries
 // One group of kWarps warps per (sequence, touched block, kv head). Half a warp holds a row of
-// 256 bytes (16 bytes a lane), so a warp takes two rows at a time; all of a lane's rows are
-// loaded before the first comparison. The halves meet by a shuffle, the warps through shared
+// 256 bytes (16 bytes a lane), so a warp takes two rows at a time; a lane has four in flight. The halves meet by a shuffle, the warps through shared
 // memory, and the old summary joins in where the block held rows before this step.
 // Roofline: HBM; 256 B per new key and kv head read, 512 B per touched block and kv head
 // written, and read where the block was begun earlier.
 template <int kWarps>
-__global__ void __launch_bounds__(256) block_summary_kernel(const __grid_constant__ SummaryArgs a) {
+__global__ void __launch_bounds__(256, 6) block_summary_kernel(const __grid_constant__ SummaryArgs a) {
   constexpr int kGroups = 8 / kWarps;            // groups of a 256-thread CTA
-  constexpr int kRowsAtOnce = kWarps == 1 ? 4 : 8;  // row pairs a lane holds at a time
+  // Rows a lane holds at a time. 4 and six resident CTAs per SM take 26.6 us for prefill chunks
+  // of 16 sequences; 8 and four CTAs 29.0, 8 and three 35.0 (GB300, 127 MB).
+  constexpr int kRowsAtOnce = 4;
   __shared__ uint4 part[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / kWarps, w = warp % kWarps;
