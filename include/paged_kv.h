@@ -378,7 +378,9 @@ int pkv_paged_attention_decode_spec(void* out, int32_t out_dtype, float* lse, co
  * pkv_update_block_summaries: for each sequence b, the rows at positions
  * [seq_lens[b] - num_new[b], seq_lens[b]), already in k_cache, enter the summaries of the
  * blocks that hold them. A block whose first row is among them starts over; any other
- * keeps what its summary says of its earlier rows. A NaN key makes its channel NaN.
+ * keeps what its summary says of its earlier rows. A NaN key makes its channel NaN. Rows
+ * that are overwritten later (rejected drafts) go on counting until their block starts
+ * over: the bounds stay bounds, only looser.
  *   max_new: at least every num_new[b] (host value; the launch is sized by it)
  * num_new 0 leaves a sequence as it is. num_new outside [0, max_new] or above seq_lens[b],
  * or seq_lens[b] > max_blocks_per_seq * block_size, skips the sequence and sets
@@ -396,8 +398,8 @@ int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32
  * at position len_b - q_len + i and sees n = ceil((len_b - q_len + 1 + i) / block_size)
  * blocks (none if that is negative). Block j's score is
  *   sum_d (P_d max_jd + N_d min_jd), P_d = sum_h max(q_hd, 0), N_d = sum_h min(q_hd, 0)
- * over the H / H_kv heads h of g: no key of the block has a larger summed dot product with
- * them. Scores decide as they would in 64 bits, whatever the order of the sums; equal ones
+ * over the H / H_kv heads h of g (sums past fp32's range count as infinite): no key of the
+ * block has a larger summed dot product with them. Scores decide as they would in 64 bits, whatever the order of the sums; equal ones
  * in favour of the lower block; a NaN score ranks above all. Blocks [0, num_sink) and the
  * last num_recent that the row sees are always among the selected. A row with
  * n <= num_selected takes every block, and no summary is read for it. A summary also

@@ -830,6 +830,7 @@ def select_blocks(q, summaries, block_table, seq_lens, num_selected: int, num_si
     if sd != d:
         raise ValueError(f"summaries head_dim {sd} differs from q's {d}")
     _table_and_lens(block_table, seq_lens, B)
+    num_selected = int(num_selected)
     if num_selected < 1:
         raise ValueError("num_selected must be positive")
     shape = (B, hkv, num_selected) if q.dim() == 3 else (B, Q, hkv, num_selected)
@@ -847,8 +848,8 @@ def select_blocks(q, summaries, block_table, seq_lens, num_selected: int, num_si
         return out
     check(load().pkv_select_blocks(
         out.data_ptr(), q.data_ptr(), summaries.data_ptr(), block_table.data_ptr(),
-        block_table.shape[1], seq_lens.data_ptr(), B, Q, H, hkv, d, 128, nb, num_selected, num_sink,
-        num_recent, _ptr(dev_status), raw), "pkv_select_blocks")
+        block_table.shape[1], seq_lens.data_ptr(), B, Q, H, hkv, d, 128, nb, num_selected,
+        int(num_sink), int(num_recent), _ptr(dev_status), raw), "pkv_select_blocks")
     return out
 
 

@@ -478,7 +478,7 @@ int pkv_paged_attention_decode_sparse(void* out, int32_t out_dtype, float* lse, 
                                       size_t workspace_bytes, int* dev_status, void* stream) {
   const char* what = "pkv_paged_attention_decode_sparse";
   PKV_REQUIRE(q_len >= 1 && num_selected >= 1, PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
-  // Rows of all sequences are numbered together, and the merge has a block per row and kv head.
+  // Rows of all sequences are numbered together, and so are their kv heads.
   PKV_REQUIRE(B < 0 || H_kv < 0 || (int64_t)B * q_len <= INT32_MAX / (H_kv > 0 ? H_kv : 1),
               PKV_ERR_UNSUPPORTED, "%s: B * q_len * H_kv must fit in int32", what);
   PKV_REQUIRE(max_blocks_per_seq <= INT32_MAX / 128, PKV_ERR_UNSUPPORTED,
@@ -495,10 +495,7 @@ int pkv_paged_attention_decode_sparse(void* out, int32_t out_dtype, float* lse, 
   a.num_selected = num_selected;
   a.rows_per_seq = q_len;
   clear_error();
-  cudaStream_t s = (cudaStream_t)stream;
-  int rc = launch_status(launch_decode_sparse(a, s), "pkv_paged_attention_decode_sparse (attention)");
-  if (rc != PKV_OK) return rc;
-  return launch_status(launch_decode_merge(a, s), "pkv_paged_attention_decode_sparse (merge)");
+  return launch_status(launch_decode_sparse(a, (cudaStream_t)stream), what);
 }
 
 int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32_t* block_table,

@@ -16,6 +16,7 @@
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
+#include "ieee_math.cuh"
 #include "launch.h"
 
 namespace pkv {
@@ -49,7 +50,7 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 // Roofline: HBM; 256 B per new key and kv head read, 512 B per touched block and kv head
 // written, and read where the block was begun earlier.
 template <int kWarps>
-__global__ void __launch_bounds__(256, 6) block_summary_kernel(const __grid_constant__ SummaryArgs a) {
+__global__ void __launch_bounds__(256, kWarps == 1 ? 4 : 6) block_summary_kernel(const __grid_constant__ SummaryArgs a) {
   constexpr int kGroups = 8 / kWarps;            // groups of a 256-thread CTA
   // Rows a lane holds at a time. 4 and six resident CTAs per SM take 26.6 us for prefill chunks
   // of 16 sequences; 8 and four CTAs 29.0, 8 and three 35.0 (GB300, 127 MB).
@@ -144,9 +145,9 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream) {
 // ------------------------------------------------------------------ selection
 // One cluster of C CTAs per (query row, kv head). Each CTA scores one run of the row's blocks
 // and keeps their keys (order-preserving whole numbers) in its shared memory. A row of at most
-// 256 competing blocks (C = 1) is then selected by one warp with the keys in registers; for
-// longer ones the CTAs select together, exchanging histograms and counts through distributed
-// shared memory.
+// 256 competing blocks is one CTA's, and is selected by one warp with the keys in registers;
+// for longer ones the CTAs select together, exchanging histograms and counts through
+// distributed shared memory.
 //
 // Scores are taken in fp32, 512 coalesced bytes per block (lanes 0-15 hold the minima and N,
 // lanes 16-31 the maxima and P, 8 channels each), 8 blocks per warp at a time whose sums are
@@ -729,14 +730,16 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
   if (n <= K || want == 0) return;  // the whole cluster takes this way
   out += e0;
   const int total = e1 - e0;  // > want
+  // Few blocks are one CTA's work, however wide the table and with it the cluster.
+  const bool by_warp = total <= 32 * kWarpKeys;
+  if (by_warp && cl.rank) return;
   // This CTA's run of competing blocks: [first, first + m).
-  const int chunk = ((total + cl.size - 1) / cl.size + 7) & ~7;
+  const int chunk = by_warp ? total : ((total + cl.size - 1) / cl.size + 7) & ~7;
   const int first = e0 + cl.rank * chunk;
   const int m = max(0, min(chunk, e1 - first));
   unsigned long long* key64 = sel_smem;                                 // [chunk_cap]
   uint32_t* key32 = reinterpret_cast<uint32_t*>(sel_smem + chunk_cap);  // [chunk_cap]
   uint32_t* cand = key32 + chunk_cap;                                   // [chunk_cap]
-  const bool by_warp = cl.size == 1 && m <= 32 * kWarpKeys;
   if (!by_warp)
     for (int i = threadIdx.x; i < 4 * kDigits; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
   __syncthreads();
@@ -861,7 +864,9 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
 
 template <int kRounds>
 static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cudaStream_t stream) {
-  const int chunk_cap = ((a.max_blocks + C - 1) / C + 7) & ~7;
+  const int alone = a.max_blocks < 32 * kWarpKeys ? a.max_blocks : 32 * kWarpKeys;
+  int chunk_cap = ((a.max_blocks + C - 1) / C + 7) & ~7;
+  if (chunk_cap < alone) chunk_cap = alone;
   const size_t smem = (size_t)chunk_cap * 16;  // fp64 keys, fp32 keys, candidates
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * C));

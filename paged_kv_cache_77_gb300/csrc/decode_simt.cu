@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(simt::THREADS, 1) decode_simt_kernel(DecodeArg
 // elements. Segments finished inside one attention CTA are skipped; empty
 // sequences get o = 0, lse = -inf.
 // --------------------------------------------------------------------------
-template <bool SPARSE>
 __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   constexpr int D = 128;
   const int seg = blockIdx.x;  // b * Hkv + g
@@ -254,15 +253,9 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   if (h >= n_rep) return;
   const int bs = 128;
   const int cap = a.max_blocks * bs;
-  const auto rows = [&] {
-    if constexpr (SPARSE)
-      return SparseRows{a.seq_lens, bs, a.rows_per_seq, a.num_selected, cap};
-    else
-      return DenseRows{a.seq_lens, bs, a.window, cap};
-  }();
   int64_t tot = 0, before = 0;
   for (int bb = lane; bb < a.B; bb += 32) {
-    const int n = rows.blocks(rows.len(bb)).n;
+    const int n = live_blocks(clamp_len(__ldg(a.seq_lens + bb), cap), bs, a.window).n;
     tot += n;
     if (bb < b) before += n;
   }
@@ -272,7 +265,7 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
   const int64_t T = tot * a.Hkv, G = a.num_ctas;
-  const int n = rows.blocks(rows.len(b)).n;
+  const int n = live_blocks(clamp_len(__ldg(a.seq_lens + b), cap), bs, a.window).n;
   const int64_t base = before * a.Hkv + (int64_t)g * n;
   const int64_t row =
       ((int64_t)b * a.q_len + h / a.n_rep) * a.H + (int64_t)g * a.n_rep + h % a.n_rep;
@@ -393,9 +386,7 @@ cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream) {
   if (a.B * a.Hkv == 0) return cudaSuccess;
   const int rows = a.n_rep * a.q_len;
   const dim3 grid(a.B * a.Hkv, (rows + 15) / 16);
-  const dim3 block(32 * (rows < 16 ? rows : 16));
-  if (a.block_indices) return launch_dependent(decode_merge_kernel<true>, grid, block, 0, stream, a);
-  return launch_dependent(decode_merge_kernel<false>, grid, block, 0, stream, a);
+  return launch_dependent(decode_merge_kernel, grid, dim3(32 * (rows < 16 ? rows : 16)), 0, stream, a);
 }
 
 }  // namespace pkv

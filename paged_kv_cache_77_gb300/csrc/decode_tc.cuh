@@ -23,7 +23,7 @@
 // producer looks a tile's block up in the row's list and leaves its place in the sequence
 // for the softmax.
 //
-// Work split: the balanced (b, kv head, block) tile list of device_common.cuh, one
+// Work split: the balanced (b, kv head, block) tile list of row_cursor.cuh, one
 // persistent CTA per SM. Warp roles:
 //   warp 0      TMA producer: Q of each piece (box {64 d, n_rep heads, QL tokens}),
 //               K and V halves of each tile (box {64 d, 1 head, 128 tokens}),
@@ -48,6 +48,7 @@
 
 #include "device_common.cuh"
 #include "launch.h"
+#include "row_cursor.cuh"
 #include "tc_ptx.cuh"
 
 namespace pkv {
@@ -146,8 +147,14 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
   using namespace tcd;
   using namespace tc;
   using L = Shape<NREP, QL>;
-  pdl_launch_dependents();  // the merge may launch now; it waits for this grid
-  pdl_wait_primary();      // inputs may come from the kernel before (the cache write)
+  if constexpr (SPARSE) {
+    // The merge reads the lengths before its own wait, so it may launch once they are visible.
+    pdl_wait_primary();
+    pdl_launch_dependents();
+  } else {
+    pdl_launch_dependents();  // the merge may launch now; it waits for this grid
+    pdl_wait_primary();       // inputs may come from the kernel before (the cache write)
+  }
   constexpr int NR = L::NR, N = L::N, NCH = L::NCH, CW = L::CW;
   constexpr int QBUF = L::QBUF, PBUF = L::PBUF;
   constexpr int OFF_K = L::OFF_K, OFF_V = L::OFF_V, OFF_Q = L::OFF_Q, OFF_P = L::OFF_P;
@@ -196,9 +203,17 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  [[maybe_unused]] __shared__ TileCursor first_tile;  // sparse: the CTA's range, sought once
   if (warp == 0) {
     const int64_t tot = total_live_blocks(rows, a.B, a.dev_status);
     if (lane == 0) *total_s = tot * a.Hkv;
+    if constexpr (SPARSE) {
+      const int64_t G = gridDim.x, T = tot * a.Hkv;
+      TileCursor c;
+      cursor_seek_warp(c, rows, a.B, a.Hkv, cta_tile_start(blockIdx.x, T, G),
+                       cta_tile_start(blockIdx.x + 1, T, G));
+      if (lane == 0) first_tile = c;
+    }
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -229,6 +244,12 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
   const int64_t t0 = cta_tile_start(blockIdx.x, T, G), t1 = cta_tile_start(blockIdx.x + 1, T, G);
   const int ntiles = (int)(t1 - t0);
 
+  auto seek = [&](TileCursor& c) {
+    if constexpr (SPARSE)
+      c = first_tile;
+    else
+      cursor_seek(c, rows, a.B, a.Hkv, t0, t1);
+  };
   auto fail = [&]() {
     *abort_flag = 1;
     flag_status(a.dev_status, PKV_DEV_TIMEOUT);
@@ -237,7 +258,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
   if (ntiles > 0 && warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
     TileCursor c;
-    cursor_seek(c, rows, a.B, a.Hkv, t0, t1);
+    seek(c);
     int piece = 0;
     const int rows_oob = (int)(a.num_blocks * BS);  // first row past the cache: zero fill
     // Sparse rows find a tile's block through the row's list and then the table. The list
@@ -320,7 +341,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
     // commits track only its own MMAs.
     constexpr uint32_t ID_S = idesc_bf16(128, N, 0, 0);  // K (K-major) x Q^T (K-major)
     TileCursor c;
-    cursor_seek(c, rows, a.B, a.Hkv, t0, t1);
+    seek(c);
     int piece = -1;
     bool ok = true;
     for (int j = 0; j < ntiles && !*abort_flag; ++j) {
@@ -365,7 +386,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
     // zero query row: their scores are 0 or masked, and nothing reads them.
     const int nreal = NR - qbase < CW ? NR - qbase : CW;
     TileCursor c;
-    cursor_seek(c, rows, a.B, a.Hkv, t0, t1);
+    seek(c);
     // Online softmax with a lazily moved reference: m_run (log2 units) changes only
     // when a block's max exceeds it by more than kLazy, so most tiles skip the
     // rescale; weights stay below 2^kLazy, well inside bf16 and fp32. The result is

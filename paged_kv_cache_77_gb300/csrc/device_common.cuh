@@ -69,44 +69,6 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Arithmetic that keeps subnormals whatever the build's flags: each result is the IEEE one.
-__device__ __forceinline__ float mul_ieee(float a, float b) {
-  float r;
-  asm("mul.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float add_ieee(float a, float b) {
-  float r;
-  asm("add.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float fma_ieee(float a, float b, float c) {
-  float r;
-  asm("fma.rn.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float div_ieee(float a, float b) {
-  float r;
-  asm("div.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-// Maximum and minimum; a NaN gives way to the other operand.
-__device__ __forceinline__ float max_ieee(float a, float b) {
-  float r;
-  asm("max.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float min_ieee(float a, float b) {
-  float r;
-  asm("min.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ double widen_ieee(float a) {
-  double r;
-  asm("cvt.f64.f32 %0, %1;\n" : "=d"(r) : "f"(a));
-  return r;
-}
-
 // Maximum of v over the 32 lanes of a full warp (one redux instruction; NaN inputs
 // are ignored like fmaxf does).
 __device__ __forceinline__ float warp_max(float v) {
@@ -195,58 +157,24 @@ struct TileCursor {
   int64_t t, t_end;     // current global tile index, end of this CTA's range
 };
 
-// The rows whose tiles a decode call walks. Dense attention: one per sequence, reading its
-// live blocks in order. Sparse attention: one per query row, reading at most `keep` blocks
-// of the row's own list; row r is query r % q_len of sequence r / q_len and sees the first
-// len - q_len + 1 + r % q_len positions of it.
-struct DenseRows {
-  const int* seq_lens;
-  int bs, window, cap;
-  __device__ __forceinline__ int raw(int b) const { return __ldg(seq_lens + b); }
-  __device__ __forceinline__ int len(int b) const { return clamp_len(raw(b), cap); }
-  __device__ __forceinline__ SeqRange blocks(int len) const { return live_blocks(len, bs, window); }
-};
-struct SparseRows {
-  const int* seq_lens;
-  int bs, q_len, keep, cap;
-  __device__ __forceinline__ int raw(int r) const { return __ldg(seq_lens + r / q_len); }
-  __device__ __forceinline__ int len(int r) const {
-    const int n = clamp_len(raw(r), cap) - q_len + 1 + r % q_len;
-    return n > 0 ? n : 0;
-  }
-  __device__ __forceinline__ SeqRange blocks(int len) const {
-    SeqRange s;
-    s.jlo = 0;
-    s.n = (len + bs - 1) / bs;
-    if (s.n > keep) s.n = keep;
-    return s;
-  }
-};
-
-// Sum of live blocks over all rows (one warp, result in every lane).
-template <typename Rows>
-__device__ __forceinline__ int64_t total_live_blocks(const Rows& rows, int B, int* dev_status) {
+// Sum of live blocks over all sequences (one warp, result in every lane).
+__device__ __forceinline__ int64_t total_live_blocks(const int* seq_lens, int B, int bs, int window,
+                                                     int cap, int* dev_status) {
   int64_t s = 0;
   for (int b = threadIdx.x & 31; b < B; b += 32) {
-    const int raw = rows.raw(b);
-    if (clamp_len(raw, rows.cap) != raw && blockIdx.x == 0) flag_status(dev_status, PKV_DEV_BAD_LENGTH);
-    s += rows.blocks(rows.len(b)).n;
+    const int raw = __ldg(seq_lens + b);
+    const int len = clamp_len(raw, cap);
+    if (len != raw && blockIdx.x == 0) flag_status(dev_status, PKV_DEV_BAD_LENGTH);
+    s += live_blocks(len, bs, window).n;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
-// The same over dense rows (the kernels that have no sparse form).
-__device__ __forceinline__ int64_t total_live_blocks(const int* seq_lens, int B, int bs, int window,
-                                                     int cap, int* dev_status) {
-  return total_live_blocks(DenseRows{seq_lens, bs, window, cap}, B, dev_status);
-}
-
 // Position the cursor at global tile t (a single thread's scan; B is small).
-template <typename Rows>
-__device__ inline void cursor_seek(TileCursor& c, const Rows& rows, int B, int Hkv, int64_t t,
-                                   int64_t t_end) {
+__device__ inline void cursor_seek(TileCursor& c, const int* seq_lens, int B, int Hkv, int bs,
+                                   int window, int cap, int64_t t, int64_t t_end) {
   c.t = t;
   c.t_end = t_end;
   int64_t base = 0;
@@ -259,8 +187,8 @@ __device__ inline void cursor_seek(TileCursor& c, const Rows& rows, int B, int H
   c.seg_base = 0;
   if (t >= t_end) return;
   for (int b = 0; b < B; ++b) {
-    int len = rows.len(b);
-    SeqRange r = rows.blocks(len);
+    int len = clamp_len(__ldg(seq_lens + b), cap);
+    SeqRange r = live_blocks(len, bs, window);
     int64_t seg = (int64_t)r.n * Hkv;
     if (t < base + seg) {
       int64_t off = t - base;
@@ -277,14 +205,9 @@ __device__ inline void cursor_seek(TileCursor& c, const Rows& rows, int B, int H
   }
 }
 
-__device__ inline void cursor_seek(TileCursor& c, const int* seq_lens, int B, int Hkv, int bs,
-                                   int window, int cap, int64_t t, int64_t t_end) {
-  cursor_seek(c, DenseRows{seq_lens, bs, window, cap}, B, Hkv, t, t_end);
-}
-
 // Advance to the next tile; returns false when the CTA's range is exhausted.
-template <typename Rows>
-__device__ inline bool cursor_next(TileCursor& c, const Rows& rows, int B, int Hkv) {
+__device__ inline bool cursor_next(TileCursor& c, const int* seq_lens, int B, int Hkv, int bs,
+                                   int window, int cap) {
   ++c.t;
   if (c.t >= c.t_end) return false;
   if (++c.j < c.n) return true;
@@ -294,16 +217,12 @@ __device__ inline bool cursor_next(TileCursor& c, const Rows& rows, int B, int H
   c.g = 0;
   for (;;) {
     if (++c.b >= B) return false;
-    c.len = rows.len(c.b);
-    SeqRange r = rows.blocks(c.len);
+    c.len = clamp_len(__ldg(seq_lens + c.b), cap);
+    SeqRange r = live_blocks(c.len, bs, window);
     c.jlo = r.jlo;
     c.n = r.n;
     if (r.n > 0) return true;
   }
-}
-__device__ inline bool cursor_next(TileCursor& c, const int* seq_lens, int B, int Hkv, int bs,
-                                   int window, int cap) {
-  return cursor_next(c, DenseRows{seq_lens, bs, window, cap}, B, Hkv);
 }
 
 // First CTA whose range starts at or before tile `t`.

@@ -45,7 +45,7 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_write(const RopeArgs& a, bool fp8, bool interleaved, cudaStream_t stream,
                               int num_sms);
-// Rows of an FP8 cache widened to bf16 (kv_write.cu).
+// Rows of an FP8 cache widened to bf16 (kv_read.cu).
 cudaError_t launch_kv_read_fp8(void* k, void* v, const void* k_cache, const void* v_cache,
                                const float* k_scale, const float* v_scale, const int32_t* slots,
                                int64_t num_tokens, int64_t num_blocks, int block_size, int hkv,
@@ -113,7 +113,7 @@ cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t stream);
 // The same kernel for q_len 1..4 query rows per sequence (q_len * n_rep <= 32).
 cudaError_t launch_decode_spec(const DecodeArgs& a, cudaStream_t stream);
-// The same kernel over the blocks that each query row lists (a.block_indices).
+// The same kernel over the blocks that each query row lists (a.block_indices), and its merge.
 cudaError_t launch_decode_sparse(const DecodeArgs& a, cudaStream_t stream);
 // tcgen05 split-KV decode over an FP8 (E4M3) cache with per-row scales; same
 // partials and merge as above.

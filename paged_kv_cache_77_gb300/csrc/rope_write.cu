@@ -25,6 +25,7 @@
 #include <cuda_fp8.h>
 
 #include "device_common.cuh"
+#include "ieee_math.cuh"
 #include "launch.h"
 
 namespace pkv {

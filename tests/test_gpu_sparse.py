@@ -173,6 +173,17 @@ def test_selection_over_clusters_of_every_width(B, width, n):
     check_select(q, random_summaries(rng, nb, 1), table, lens, 33, 1, 1)
 
 
+def test_selection_of_short_rows_under_a_wide_table():
+    """A table as wide as the model's context: rows far shorter than it, of every length around
+    the limit of one CTA, next to long ones."""
+    rng = np.random.default_rng(9)
+    lens = np.array([300, 256 * BS, 257 * BS, 258 * BS + 1, 259 * BS, 1, 0, 700 * BS])
+    table, nb = make_table(rng, lens, 8192)
+    for H in (1, 8):
+        q = torch.from_numpy(rng.standard_normal((8, H, D))).to(torch.bfloat16).cuda()
+        check_select(q, random_summaries(rng, nb, 1), table, lens, 5, 1, 1)
+
+
 def _torch_select(q, s, table, lens, K, recent=1):
     """The selection of large cases: fp64 scores on the GPU (sums exact for these inputs)."""
     B, H, _ = q.shape
@@ -401,6 +412,34 @@ def test_sparse_decode_splits_long_lists_and_uses_its_own_workspace():
     need = api.decode_sparse_workspace_size(2, 1, 4, 1, D)
     ws = torch.full((need // 4 + 64,), float("nan"), device="cuda")
     check_attend(q, kc, vc, table, lens, idx, workspace=ws)
+
+
+def test_sparse_decode_of_many_query_rows():
+    """Hundreds of rows (a chunk of a prompt, row by row): several seek rounds per CTA."""
+    rng = np.random.default_rng(24)
+    lens = np.array([333, 0, 90, 1500])
+    table, nb = make_table(rng, lens)
+    kc, vc = caches(nb, 1)
+    Q = 150
+    idx = random_lists(rng, lens, Q, 1, 2)
+    q = torch.from_numpy(rng.standard_normal((4, Q, 2, D))).to(torch.bfloat16).cuda()
+    check_attend(q, kc, vc, table, lens, idx)
+
+
+def test_summaries_and_selection_after_rejected_drafts():
+    """Rows written as drafts and overwritten later go on counting in their block; a block that
+    starts over forgets them."""
+    k = torch.zeros((3, BS, 1, D), dtype=torch.bfloat16, device="cuda")
+    s = torch.zeros((3, 1, 2, D), dtype=torch.bfloat16, device="cuda")
+    t = ints([[1, 2]])
+    k[1, :127] = torch.randn((127, 1, D), device="cuda").to(torch.bfloat16)
+    api.update_block_summaries(s, k, t, ints([127]), ints([127]), 127)
+    k[1, 127], k[2, 0] = 50.0, 60.0  # two drafts; the second opens a block
+    api.update_block_summaries(s, k, t, ints([129]), ints([2]), 2)
+    assert (s[1, 0, 1] == 50).all() and (s[2, 0] == 60).all()
+    k[1, 127], k[2, 0] = 1.0, -1.0   # both rejected and written anew
+    api.update_block_summaries(s, k, t, ints([129]), ints([2]), 2)
+    assert (s[1, 0, 1] == 50).all() and (s[2, 0] == -1).all()
 
 
 def test_sparse_decode_empty_batches():
