@@ -18,6 +18,7 @@
 #include "device_common.cuh"
 #include "ieee_math.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 
 namespace pkv {
 
@@ -56,6 +57,7 @@ __global__ void __launch_bounds__(256, kWarps == 1 ? 4 : 6) block_summary_kernel
   // of 16 sequences; 8 and four CTAs 29.0, 8 and three 35.0 (GB300, 127 MB).
   constexpr int kRowsAtOnce = 4;
   __shared__ uint4 part[8][32];
+  pdl_wait_then_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / kWarps, w = warp % kWarps;
   const int64_t item = (int64_t)blockIdx.x * kGroups + group;
@@ -136,10 +138,8 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream) {
   // Few new rows per block: a warp per (block, head) reads them in one go. From 16 rows on a
   // whole CTA shares a block's rows.
   if (a.max_new <= 16)
-    block_summary_kernel<1><<<(unsigned)((items + 7) / 8), 256, 0, stream>>>(a);
-  else
-    block_summary_kernel<8><<<(unsigned)items, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+    return launch_dependent(block_summary_kernel<1>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, stream, a);
+  return launch_dependent(block_summary_kernel<8>, dim3((unsigned)items), dim3(256), 0, stream, a);
 }
 
 // ------------------------------------------------------------------ selection
@@ -661,6 +661,7 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
     select_blocks_kernel(const __grid_constant__ SelectArgs a, int chunk_cap) {
   extern __shared__ unsigned long long sel_smem[];
   __shared__ SelShared sh;
+  pdl_wait_then_launch();
   const Cluster cl = {(int)cg::this_cluster().num_blocks(), (int)cg::this_cluster().block_rank()};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t seg = blockIdx.x / cl.size;  // (query row, kv head)
@@ -873,13 +874,15 @@ static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cud
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, select_blocks_kernel<kRounds>, a, chunk_cap);
 }
 

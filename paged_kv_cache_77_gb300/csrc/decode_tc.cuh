@@ -48,6 +48,7 @@
 
 #include "device_common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 #include "row_cursor.cuh"
 #include "tc_ptx.cuh"
 
@@ -148,9 +149,7 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
   using namespace tc;
   using L = Shape<NREP, QL>;
   if constexpr (SPARSE) {
-    // The merge reads the lengths before its own wait, so it may launch once they are visible.
-    pdl_wait_primary();
-    pdl_launch_dependents();
+    pdl_wait_then_launch();
   } else {
     pdl_launch_dependents();  // the merge may launch now; it waits for this grid
     pdl_wait_primary();       // inputs may come from the kernel before (the cache write)

@@ -10,6 +10,7 @@
 #include "device_common.cuh"
 #include "ieee_math.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 
 namespace pkv {
 
@@ -18,6 +19,7 @@ __global__ void __launch_bounds__(256) kv_read_fp8_kernel(
     const uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
     const float* __restrict__ v_scale, const int32_t* __restrict__ slots, int64_t num_tokens,
     int64_t num_slots, int hkv, int block_size, int* dev_status) {
+  pdl_wait_then_launch();
   const int c = threadIdx.x & 7;
   const int64_t rows = num_tokens * hkv * 2;
   for (int64_t w = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 3; w < rows;
@@ -67,10 +69,9 @@ cudaError_t launch_kv_read_fp8(void* k, void* v, const void* k_cache, const void
   // 153 us with 8. Two or four rows per lane at a time measured 135 to 180 us.
   const int64_t cap = (int64_t)num_sms * 64;
   if (blocks > cap) blocks = cap;
-  kv_read_fp8_kernel<<<(unsigned)blocks, 256, 0, stream>>>(
-      (uint8_t*)k, (uint8_t*)v, (const uint8_t*)k_cache, (const uint8_t*)v_cache, k_scale, v_scale,
-      slots, num_tokens, num_blocks * block_size, hkv, block_size, dev_status);
-  return cudaGetLastError();
+  return launch_dependent(kv_read_fp8_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, (uint8_t*)k,
+                          (uint8_t*)v, (const uint8_t*)k_cache, (const uint8_t*)v_cache, k_scale, v_scale,
+                          slots, num_tokens, num_blocks * block_size, hkv, block_size, dev_status);
 }
 
 }  // namespace pkv

@@ -27,6 +27,7 @@
 #include "device_common.cuh"
 #include "ieee_math.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 
 namespace pkv {
 
@@ -88,6 +89,7 @@ constexpr int kUnroll = 4;
 constexpr int kCtasPerSm = 3;
 template <bool FP8, bool INTERLEAVED>
 __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __grid_constant__ RopeArgs a) {
+  pdl_wait_then_launch();
   const int lane = threadIdx.x & 31;
   const int lanes = a.head_dim / 16;       // lanes of one head
   const int per_pass = 32 / lanes;         // heads a warp holds at a time
@@ -224,8 +226,7 @@ static cudaError_t launch_rope_n(const RopeArgs& a, cudaStream_t stream, int num
   int64_t blocks = (items + 7) / 8;
   const int64_t cap = (int64_t)num_sms * kCtasPerSm;
   if (blocks > cap) blocks = cap;
-  rope_write_kernel<FP8, INTERLEAVED><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(rope_write_kernel<FP8, INTERLEAVED>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
 }
 
 cudaError_t launch_rope_write(const RopeArgs& a, bool fp8, bool interleaved, cudaStream_t stream,
