@@ -42,6 +42,13 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Largest magnitudes, NaN if either is; the sign bits of the result mean nothing.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ summaries
@@ -787,7 +794,7 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           s = ffma2(coef[i], f2pack(bf16lo(w[i]), bf16hi(w[i])), s);
-          vmax = max2(vmax, w[i] & 0x7fff7fffu);
+          vmax = max_abs2(vmax, w[i]);
         }
         const float2 both = f2unpack(s);
         v[u] = both.x + both.y;
@@ -819,7 +826,7 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
   // ---- range of the keys and of the summaries, over the cluster
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
-  uint32_t top = __reduce_max_sync(0xffffffffu, max(vmax & 0xffffu, vmax >> 16));
+  uint32_t top = __reduce_max_sync(0xffffffffu, max(vmax & 0x7fffu, vmax >> 16 & 0x7fffu));
   if (lane == 0) {
     sh.lo[warp] = kmin;
     sh.hi[warp] = kmax;
@@ -896,7 +903,9 @@ cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int n
                              (segs * C < 2 * num_sms && a.max_blocks > C * kSelWarps * 8)))
     C *= 2;
   // Two groups of 8 blocks in flight where a warp has several to go (few CTAs per SM then, so
-  // loads in flight are what counts); one where the registers buy resident CTAs.
+  // loads in flight are what counts): 2 x 2 rows of 8 kv heads over a million tokens take 32 us
+  // with two on GB300, 42 us with one. One where the registers buy resident CTAs: 512 rows of up
+  // to 256 blocks, 15.2 us.
   if (a.max_blocks > 4 * 64 * C) return launch_select_n<2>(a, C, segs, stream);
   return launch_select_n<1>(a, C, segs, stream);
 }
