@@ -255,7 +255,10 @@ __device__ __forceinline__ double widen_bits(uint32_t bits) {
   return (bits & 0x7fffffffu) ? widen_ieee(__uint_as_float(bits)) : 0.0;
 }
 
-// Keys of up to 4 candidates in fp64, by a warp; key64[r] for the blocks cand[r].
+// Keys of up to 4 candidates in fp64, by a warp; key64[r] for the blocks cand[r]. An fp64
+// operation of a warp costs some 70 to 90 cycles here, so there are few: 8 additions for the
+// coefficients and 16 operations a candidate, no conversions (a smaller version with
+// conversions, always four candidates, took 9.7k cycles instead of 6k).
 __device__ void score64(const Row& row, const SelShared& sh, const uint32_t* cand,
                         unsigned long long* key64, int n) {
   const int lane = threadIdx.x & 31;
