@@ -407,7 +407,9 @@ int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32
  *   block_indices [B, q_len, H_kv, num_selected] int32 (written)
  *   q [B, q_len, H, head_dim] bf16; block_table, seq_lens as for decode
  * Table entries outside [0, num_blocks) rank below every block and set
- * PKV_DEV_BAD_BLOCK; a length past the table is clamped (PKV_DEV_BAD_LENGTH).
+ * PKV_DEV_BAD_BLOCK; a length past the table is clamped (PKV_DEV_BAD_LENGTH). Every block
+ * that a row sees competes: a table whose expired entries hold the null block (a sliding
+ * window's) does not go with it.
  * Supported: head_dim 128, block_size 128, H % H_kv == 0, H / H_kv <= 16,
  * num_sink + num_recent <= num_selected, max_blocks_per_seq <= 8192 (1,048,576 tokens).
  * No workspace. */

@@ -698,18 +698,18 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
         const float v = __uint_as_float(bits[h] << 16);
         const float x = d < kDim ? min_nan(v, 0.f) : max_nan(v, 0.f);
         const float s = add_ieee(sum, x);
-        const float back = add_ieee(s, -sum);
-        low = add_ieee(low, add_ieee(add_ieee(sum, -add_ieee(s, -back)), add_ieee(x, -back)));
+        const float back = sub_ieee(s, sum);
+        low = add_ieee(low, add_ieee(sub_ieee(sum, sub_ieee(s, back)), sub_ieee(x, back)));
         sum = s;
       }
     }
     const float all = add_ieee(sum, low);
-    const bool finite = fabsf(all) < INFINITY;
-    low = finite ? add_ieee(low, add_ieee(sum, -all)) : 0.f;
+    const bool finite = abs_ieee(all) < INFINITY;
+    low = finite ? add_ieee(low, sub_ieee(sum, all)) : 0.f;
     sum = finite ? all : sum;
     sh.coef[d] = sum;
     sh.coef_low[d] = low;
-    float size = fabsf(sum);
+    float size = abs_ieee(sum);
 #pragma unroll
     for (int o = 16; o; o >>= 1) size = add_ieee(size, __shfl_xor_sync(0xffffffffu, size, o));
     any = __reduce_or_sync(0xffffffffu, any);

@@ -55,7 +55,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // E4M3 codes of 8 values over the row's scale (0: an all-zero row, zero codes).
 __device__ __forceinline__ uint2 codes8(const float* f, float scale) {
   uint32_t u[2] = {0, 0};
-  if (scale > 0.f) {
+  if (__float_as_uint(scale)) {  // not a comparison, which would take a subnormal for zero
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(
@@ -74,7 +74,7 @@ __device__ __forceinline__ void rotate(float* f, const float* c, const float* s)
   for (int i = 0; i < 8; ++i) {
     float& a = f[INTERLEAVED ? 2 * i : i];
     float& b = f[INTERLEAVED ? 2 * i + 1 : 8 + i];
-    const float x = fma_ieee(a, c[i], -mul_ieee(b, s[i]));
+    const float x = fma_ieee(a, c[i], neg_ieee(mul_ieee(b, s[i])));
     b = fma_ieee(b, c[i], mul_ieee(a, s[i]));
     a = x;
   }
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
       // Largest magnitude of the row, over its 8 lanes (head_dim is 128).
       float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = max_ieee(amax, fabsf(f[i]));
+      for (int i = 0; i < 16; ++i) amax = max_ieee(amax, abs_ieee(f[i]));
 #pragma unroll
       for (int o = 4; o; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (head0 >= heads || !store) continue;

@@ -153,6 +153,22 @@ def test_rope_write_fp8_matches_oracle(T, H, Hkv, rope_dim, axis, interleaved, s
     assert (kc.cpu().numpy().reshape(-1, Hkv, 128)[left] == 0x55).all()
 
 
+def test_rope_write_fp8_rows_of_extreme_magnitude():
+    """Rows near the type's ends and subnormal rows: v's codes and scales are those of IEEE
+    fp32 divisions, bit for bit."""
+    c = Case(8, 2, 2, 128, 128, seed=21)
+    for t, e in enumerate((-126, -130, -133, -100, 0, 60, 120, 126)):
+        c.v[t] = (c.v[t].double() * 2.0 ** e).clamp(-3e38, 3e38).to(torch.bfloat16)
+    kc, vc = (torch.zeros((c.nb, BS, 2, 128), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((c.nb, 2, BS), device="cuda") for _ in range(2))
+    api.rope_kv_cache_write_fp8(kc, vc, ks, vs, c.q, c.k, c.v, c.table, c.pos, c.slots, **c.kwargs())
+    slots = c.slots.cpu().numpy()
+    codes, scales = fp8_ref.quantize_rows(synth.bf16_bits(c.v))
+    assert (scales[1:3] > 0).all() and (scales[1:3] < 2.0 ** -126).all()
+    assert np.array_equal(vs.cpu().numpy().transpose(0, 2, 1).reshape(-1, 2)[slots], scales)
+    assert np.array_equal(vc.cpu().numpy().reshape(-1, 2, 128)[slots], codes)
+
+
 def test_rope_write_in_place_on_a_projection_buffer():
     c = Case(200, 8, 2, 128, 128, seed=3, strided=True)
     kc, vc = (torch.zeros((c.nb, BS, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))

@@ -257,6 +257,9 @@ def test_selection_with_special_values():
     tiny = random_summaries(rng, nb, 2, 2.0 ** -132)  # subnormal bf16
     check_select(q, tiny, table, [n * BS], K)
     check_select((q * 2.0 ** -130).contiguous(), big, table, [n * BS], K)
+    # Subnormal queries against keys near the largest value: products of ordinary size.
+    q_tiny = torch.from_numpy(rng.standard_normal((1, 4, D)) * 2.0 ** -131).to(torch.bfloat16).cuda()
+    check_select(q_tiny, big, table, [n * BS], K)
     # A NaN query: every score is NaN.
     q[0, 0, 0] = float("nan")
     assert check_select(q, s, table, [n * BS], K, 0, 0)[0, 0, 0].tolist() == list(range(K))
