@@ -52,19 +52,45 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// E4M3 codes of 8 values over the row's scale (0: an all-zero row, zero codes).
-__device__ __forceinline__ uint2 codes8(const float* f, float scale) {
-  uint32_t u[2] = {0, 0};
-  if (__float_as_uint(scale)) {  // not a comparison, which would take a subnormal for zero
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// E4M3 codes of a lane's 16 values over their row's scale: the code of the fp32 quotient
+// x / scale (0: an all-zero row, zero codes). Rounding to E4M3 is monotonic, so where the codes
+// of two products that enclose the quotient agree, they are the quotient's: x times 1 / scale
+// less and more 2^-21 of it (the roundings of 1 / scale, of its multiple, of the product and of
+// the quotient are 2^-24 each). Lanes where they differ (a value that close to the middle of
+// two codes, less than one warp in a hundred) divide, and so do scales whose inverse could
+// overflow.
+__device__ __forceinline__ uint4 codes16(const float* f, float scale) {
+  uint32_t u[4] = {0, 0, 0, 0};
+  if (!__float_as_uint(scale)) return make_uint4(0, 0, 0, 0);  // (a comparison may flush it)
+  const float inv = div_ieee(1.f, scale);
+  const float below = mul_ieee(inv, 1.f - 0x1p-21f), above = mul_ieee(inv, 1.f + 0x1p-21f);
+  bool divide = scale < 0x1p-120f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(
-          make_float2(div_ieee(f[2 * i], scale), div_ieee(f[2 * i + 1], scale)), __NV_SATFINITE,
-          __NV_E4M3);
-      u[i >> 1] |= (uint32_t)c << (16 * (i & 1));
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t c = e4m3x2(mul_ieee(f[2 * i], below), mul_ieee(f[2 * i + 1], below));
+    divide |= c != e4m3x2(mul_ieee(f[2 * i], above), mul_ieee(f[2 * i + 1], above));
+    u[i >> 1] |= c << (16 * (i & 1));
+  }
+  if (divide) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = f[i];
+#pragma unroll 1
+    for (int n = 0; n < 8; ++n) {  // rolled (rare, and its code is small), the values moving past
+      const uint32_t c = e4m3x2(div_ieee(x[0], scale), div_ieee(x[1], scale));
+      u[0] = __funnelshift_r(u[0], u[1], 16);
+      u[1] = __funnelshift_r(u[1], u[2], 16);
+      u[2] = __funnelshift_r(u[2], u[3], 16);
+      u[3] = u[3] >> 16 | c << 16;
+#pragma unroll
+      for (int i = 0; i < 14; ++i) x[i] = x[i + 2];
     }
   }
-  return make_uint2(u[0], u[1]);
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // Rotates the lane's 8 pairs in place (f: the 16 values of its two vectors).
@@ -182,8 +208,9 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
       const float scale = div_ieee(amax, 448.f);
       const int g = is_v ? head0 - a.H - a.Hkv : head0 - a.H;
       uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + ((int64_t)slot * a.Hkv + g) * 128;
-      *reinterpret_cast<uint2*>(dst + lo) = codes8(f, scale);
-      *reinterpret_cast<uint2*>(dst + hi) = codes8(f + 8, scale);
+      const uint4 codes = codes16(f, scale);
+      *reinterpret_cast<uint2*>(dst + lo) = make_uint2(codes.x, codes.y);
+      *reinterpret_cast<uint2*>(dst + hi) = make_uint2(codes.z, codes.w);
       if (c == 0) {
         const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
         (is_v ? a.v_scale : a.k_scale)[(blk * a.Hkv + g) * a.block_size + off] = scale;
