@@ -31,9 +31,16 @@ __device__ __forceinline__ float div_ieee(float a, float b) {
   asm("div.rn.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// Sign operations by bits: the instructions may flush too.
-__device__ __forceinline__ float neg_ieee(float a) { return __uint_as_float(__float_as_uint(a) ^ 0x80000000u); }
-__device__ __forceinline__ float abs_ieee(float a) { return __uint_as_float(__float_as_uint(a) & 0x7fffffffu); }
+__device__ __forceinline__ float neg_ieee(float a) {
+  float r;
+  asm("neg.f32 %0, %1;\n" : "=f"(r) : "f"(a));
+  return r;
+}
+__device__ __forceinline__ float abs_ieee(float a) {
+  float r;
+  asm("abs.f32 %0, %1;\n" : "=f"(r) : "f"(a));
+  return r;
+}
 // Maximum and minimum; a NaN gives way to the other operand.
 __device__ __forceinline__ float max_ieee(float a, float b) {
   float r;

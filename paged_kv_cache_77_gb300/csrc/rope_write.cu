@@ -123,34 +123,43 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
   const bool active = sub < per_pass;      // head_dim not a power of two leaves lanes over
   const int nrot = a.rope_dim / 16;
   const bool rot = c < nrot;
-  const int lo = rot && !INTERLEAVED ? 8 * c : 16 * c;
-  const int hi = rot && !INTERLEAVED ? a.rope_dim / 2 + 8 * c : 16 * c + 8;
-  // A token's heads are q, then k, then v. Heads that stay bf16 go kUnroll passes to an item,
-  // heads that are quantised one pass.
-  const int heads = a.H + 2 * a.Hkv, plain = FP8 ? a.H : heads;
-  const int share = per_pass * kUnroll;
-  const int plain_parts = (plain + share - 1) / share;
-  const int parts = plain_parts + (heads - plain + per_pass - 1) / per_pass;
-  const int64_t items = a.num_tokens * parts;
-  for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items;
-       item += (int64_t)gridDim.x * 8) {
-    const int64_t t = item / parts;
-    const int part = (int)(item - t * parts);
-    const bool quantise = FP8 && part >= plain_parts;  // the same for the whole warp
-    const int head0 = (quantise ? plain + (part - plain_parts) * per_pass : part * share) + sub;
-    const int end = quantise ? heads : plain;
+  // The lane's two vectors, from the first head of a pass.
+  const int lo = sub * a.head_dim + (rot && !INTERLEAVED ? 8 * c : 16 * c);
+  const int hi = sub * a.head_dim + (rot && !INTERLEAVED ? a.rope_dim / 2 + 8 * c : 16 * c + 8);
+  // An item is up to kUnroll passes over the q, the k or the v heads of a token; one pass where
+  // the heads are quantised. All of an item's addresses are offsets from two uniform pointers.
+  const int q_share = per_pass * kUnroll, kv_share = FP8 ? per_pass : q_share;
+  const int q_parts = (a.H + q_share - 1) / q_share, kv_parts = (a.Hkv + kv_share - 1) / kv_share;
+  const int parts = q_parts + 2 * kv_parts;
+  const int pass_stride = per_pass * a.head_dim;
+  // A warp's items are one stride apart; the division is done once.
+  const int stride = (int)gridDim.x * 8, step_t = stride / parts, step_part = stride % parts;
+  const int warp0 = (int)blockIdx.x * 8 + __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+  int64_t t = warp0 / parts;
+  int part = warp0 % parts;
+  auto advance = [&]() {
+    t += step_t;
+    part += step_part;
+    if (part >= parts) {
+      part -= parts;
+      ++t;
+    }
+  };
+  for (; t < a.num_tokens; advance()) {
+    const bool is_q = part < q_parts, is_v = part >= q_parts + kv_parts;
+    const int head0 = is_q ? part * q_share : (part - q_parts - (is_v ? kv_parts : 0)) * kv_share;
+    const int left = (is_q ? a.H : a.Hkv) - head0 - sub;  // heads from the lane's first on
+    const uint16_t* src = (is_q    ? a.q + t * a.q_stride
+                           : is_v ? a.v + t * a.v_stride
+                                  : a.k + t * a.k_stride) +
+                          head0 * a.head_dim;
     uint4 w0[kUnroll], w1[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = head0 + u * per_pass;
       w0[u] = w1[u] = make_uint4(0, 0, 0, 0);
-      if (active && h < end && !(quantise && u)) {
-        const uint16_t* src = h < a.H ? a.q + t * a.q_stride + h * a.head_dim
-                              : h < a.H + a.Hkv
-                                  ? a.k + t * a.k_stride + (h - a.H) * a.head_dim
-                                  : a.v + t * a.v_stride + (h - a.H - a.Hkv) * a.head_dim;
-        w0[u] = *reinterpret_cast<const uint4*>(src + lo);
-        w1[u] = *reinterpret_cast<const uint4*>(src + hi);
+      if (active && u * per_pass < left && (!FP8 || is_q || u == 0)) {
+        w0[u] = *reinterpret_cast<const uint4*>(src + u * pass_stride + lo);
+        w1[u] = *reinterpret_cast<const uint4*>(src + u * pass_stride + hi);
       }
     }
     const int32_t slot = __ldg(a.slots + t);
@@ -169,7 +178,7 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
     if (bad_slot && lane == 0) flag_status(a.dev_status, PKV_DEV_BAD_SLOT);
     const bool store = slot >= 0 && !bad_slot;
     float cs[8], sn[8];
-    if (rot) {
+    if (rot && !is_v) {
       const int axis = a.chunk_axis[c];
       if (axis >= 0) {  // the 8 pairs share one axis: whole vectors of its table row
         const int p = axis == 0 ? pos[0] : axis == 1 ? pos[1] : axis == 2 ? pos[2] : pos[3];
@@ -192,8 +201,7 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
         }
       }
     }
-    if (quantise) {
-      const bool is_v = head0 >= a.H + a.Hkv;
+    if (FP8 && !is_q) {
       float f[16];
       unpack8(w0[0], f);
       unpack8(w1[0], f + 8);
@@ -204,24 +212,25 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
       for (int i = 0; i < 16; ++i) amax = max_ieee(amax, abs_ieee(f[i]));
 #pragma unroll
       for (int o = 4; o; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (head0 >= heads || !store) continue;
+      if (left <= 0 || !store) continue;
       const float scale = div_ieee(amax, 448.f);
-      const int g = is_v ? head0 - a.H - a.Hkv : head0 - a.H;
-      uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + ((int64_t)slot * a.Hkv + g) * 128;
+      uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + ((int64_t)slot * a.Hkv + head0) * 128;
       const uint4 codes = codes16(f, scale);
       *reinterpret_cast<uint2*>(dst + lo) = make_uint2(codes.x, codes.y);
       *reinterpret_cast<uint2*>(dst + hi) = make_uint2(codes.z, codes.w);
       if (c == 0) {
-        const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
-        (is_v ? a.v_scale : a.k_scale)[(blk * a.Hkv + g) * a.block_size + off] = scale;
+        const int blk = slot / a.block_size, off = slot - blk * a.block_size;
+        (is_v ? a.v_scale : a.k_scale)[((int64_t)blk * a.Hkv + head0 + sub) * a.block_size + off] = scale;
       }
       continue;
     }
+    if (!is_q && !store) continue;
+    uint16_t* dst = is_q ? a.q_out + t * a.q_out_stride + head0 * a.head_dim
+                         : reinterpret_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) +
+                               ((int64_t)slot * a.Hkv + head0) * a.head_dim;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = head0 + u * per_pass;
-      const bool is_q = h < a.H, is_v = h >= a.H + a.Hkv;
-      if (!active || h >= end) continue;
+      if (!active || u * per_pass >= left) continue;
       if (rot && !is_v) {
         float f[16];
         unpack8(w0[u], f);
@@ -230,26 +239,17 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
         w0[u] = pack8(f);
         w1[u] = pack8(f + 8);
       }
-      uint16_t* dst;
-      if (is_q) {
-        dst = a.q_out + t * a.q_out_stride + h * a.head_dim;
-      } else {
-        if (!store) continue;
-        const int g = is_v ? h - a.H - a.Hkv : h - a.H;
-        dst = reinterpret_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) +
-              ((int64_t)slot * a.Hkv + g) * a.head_dim;
-      }
-      *reinterpret_cast<uint4*>(dst + lo) = w0[u];
-      *reinterpret_cast<uint4*>(dst + hi) = w1[u];
+      *reinterpret_cast<uint4*>(dst + u * pass_stride + lo) = w0[u];
+      *reinterpret_cast<uint4*>(dst + u * pass_stride + hi) = w1[u];
     }
   }
 }
 
 template <bool FP8, bool INTERLEAVED>
 static cudaError_t launch_rope_n(const RopeArgs& a, cudaStream_t stream, int num_sms) {
-  const int per_pass = 32 / (a.head_dim / 16), share = per_pass * kUnroll;
-  const int heads = a.H + 2 * a.Hkv, plain = FP8 ? a.H : heads;
-  const int64_t items = a.num_tokens * ((plain + share - 1) / share + (heads - plain + per_pass - 1) / per_pass);
+  const int per_pass = 32 / (a.head_dim / 16), q_share = per_pass * kUnroll;
+  const int kv_share = FP8 ? per_pass : q_share;
+  const int64_t items = a.num_tokens * ((a.H + q_share - 1) / q_share + 2 * ((a.Hkv + kv_share - 1) / kv_share));
   int64_t blocks = (items + 7) / 8;
   const int64_t cap = (int64_t)num_sms * kCtasPerSm;
   if (blocks > cap) blocks = cap;
