@@ -169,6 +169,30 @@ def test_rope_write_fp8_rows_of_extreme_magnitude():
     assert np.array_equal(vc.cpu().numpy().reshape(-1, 2, 128)[slots], codes)
 
 
+def test_rope_write_fp8_codes_at_every_tie():
+    """Rows whose largest value has each of bf16's 128 significands, holding every significand
+    at exponents over E4M3's whole range: quotients at and next to the midpoints of codes. The
+    codes are those of correctly rounded fp32 quotients, bit for bit, at three magnitudes."""
+    rng = np.random.default_rng(23)
+    rows = np.empty((3 * 128, 9, 128))
+    for r in range(3 * 128):
+        top = (128 + r % 128) * 2.0 ** (-7 + (0, -60, 55)[r // 128])
+        for h in range(9):
+            rows[r, h] = rng.permutation(128 + np.arange(128)) * 2.0 ** (-8 - 2 * h) * 2.0 ** (
+                (0, -60, 55)[r // 128]) * rng.choice([-1, 1], 128)
+            rows[r, h, rng.integers(128)] = top
+    c = Case(3 * 128, 1, 9, 128, 16, seed=24)
+    c.v = torch.from_numpy(rows).to(torch.bfloat16).cuda()
+    assert np.array_equal(c.host(c.v), rows)  # all of them bf16 values
+    kc, vc = (torch.zeros((c.nb, BS, 9, 128), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((c.nb, 9, BS), device="cuda") for _ in range(2))
+    api.rope_kv_cache_write_fp8(kc, vc, ks, vs, c.q, c.k, c.v, c.table, c.pos, c.slots, **c.kwargs())
+    slots = c.slots.cpu().numpy()
+    codes, scales = fp8_ref.quantize_rows(synth.bf16_bits(c.v))
+    assert np.array_equal(vs.cpu().numpy().transpose(0, 2, 1).reshape(-1, 9)[slots], scales)
+    assert np.array_equal(vc.cpu().numpy().reshape(-1, 9, 128)[slots], codes)
+
+
 def test_rope_write_in_place_on_a_projection_buffer():
     c = Case(200, 8, 2, 128, 128, seed=3, strided=True)
     kc, vc = (torch.zeros((c.nb, BS, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
