@@ -111,8 +111,9 @@ __device__ __forceinline__ void rotate(float* f, const float* c, const float* s)
 }  // namespace
 
 // Measured on GB300 (16,001 tokens of 32 / 8 heads in bf16; 9,001 of 64 / 8 heads in FP8): 4
-// passes an item, 3 resident CTAs per SM and a grid of them 66.4 and 67.5 us; 2 passes and 4
-// CTAs 68.2 and 70.7; 8 CTAs per SM of grid 69 and 72; 2 resident CTAs 77 and 75.
+// passes an item, 3 resident CTAs per SM and a grid of them 64.3 and 56.3 us, 92 % of the copy
+// rate each; 2 passes and 4 CTAs 63.4 and 58.4; 8 passes and 2 CTAs 63.8 and 64.0; 4 passes and
+// 2 CTAs 74.8 and 70.2; 8 CTAs per SM of grid 66.0 and 59.3.
 constexpr int kUnroll = 4;
 constexpr int kCtasPerSm = 3;
 template <bool FP8, bool INTERLEAVED>
