@@ -863,7 +863,9 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_table, seq_lens, bl
     """Decode attention over the blocks that select_blocks chose (or any other list).
 
     q [B, H, d] with block_indices [B, H_kv, K], or q [B, q_len, H, d] with block_indices
-    [B, q_len, H_kv, K]; returns out in q's shape (and fills lse, the shape without d)."""
+    [B, q_len, H_kv, K]; returns out in q's shape (and fills lse, the shape without d). A list
+    may be in any order; negative entries are empty places. Of a row that sees n blocks, the
+    first min(K, n) entries are read."""
     B, Q, H, d = _query_rows(q)
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _dev_bf16(t, n)

@@ -238,6 +238,36 @@ def test_selection_decides_ties_and_near_ties_as_in_64_bits():
     assert check_select(q, s, table, [n * BS], K, 0, 1)[0, 0, 0].tolist() == [*range(K - 1), n - 1]
 
 
+@pytest.mark.parametrize("n,width,H", [(300, 300, 2), (600, 640, 1), (2000, 2000, 4), (1100, 8192, 1)])
+def test_selection_by_a_cluster_decides_ties_and_special_values(n, width, H):
+    """Rows of more blocks than one CTA selects: ties by the hundred across the border and the
+    CTAs, all blocks equal, near ties, NaN, infinities, zero queries, bad blocks."""
+    rng = np.random.default_rng(n)
+    lens = np.array([n * BS, n * BS - 200])
+    table, nb = make_table(rng, lens, width)
+    q = torch.ones((2, H, D), dtype=torch.bfloat16, device="cuda")
+    s = torch.ones((nb, 1, 2, D), dtype=torch.bfloat16, device="cuda")
+    assert check_select(q, s, table, lens, 50, 0, 0)[0, 0, 0].tolist() == list(range(50))
+    for K in (1, 33, n // 2, n - 4):
+        whole = torch.from_numpy(rng.integers(-1, 2, (nb, 1, 2, D)).astype(np.float64))
+        whole[..., 3:] = 0
+        check_select(q, whole.sort(dim=2).values.to(torch.bfloat16).cuda(), table, lens, K, 0, 1)
+    s[:, :, :, 0] = torch.from_numpy(rng.permutation(nb) % 200).to(torch.bfloat16).cuda()[:, None, None]
+    q[:, :, 0] = 2.0 ** -30  # differences that fp32 sums cannot see
+    check_select(q, s, table, lens, 70, 1, 2)
+    s = random_summaries(rng, nb, 1)
+    check_select(torch.zeros_like(q), s, table, lens, 40, 0, 1)
+    bad = table.copy()
+    bad[0, ::7], bad[1, 5] = -1, nb
+    check_select(q, s, bad, lens, n - 60, 2, 2, bit=2)
+    t = table[0]
+    s[int(t[n - 9]), 0, 1, 3] = float("inf")
+    s[int(t[9]), 0, 0, 4] = float("nan")
+    with np.errstate(invalid="ignore"):
+        want = check_select(q, s, table, lens, 20, 0, 0)
+    assert {9, n - 9} <= set(want[0, 0, 0])
+
+
 def test_selection_with_special_values():
     rng = np.random.default_rng(4)
     n, K = 30, 6

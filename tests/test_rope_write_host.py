@@ -92,3 +92,34 @@ def test_read_fp8_refusals():
     assert call(T=-1) == -1 and call(nb=0) == -1 and call(hkv=0) == -1
     assert call(k=None) == -1 and call(slots=None) == -1 and call(ks=None) == -1
     assert call(k=P + 8) == -1 and call(vs=P + 2) == -1 and b"aligned" in lib.pkv_last_error()
+
+
+def test_the_binding_refuses_host_tensors():
+    import torch
+
+    from paged_kv_cache_77_gb300 import api
+
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    rows = bf(3, 4, 128), bf(3, 2, 128), bf(3, 2, 128), torch.zeros((9, 128)), i32(3), i32(3)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.rope_kv_cache_write(bf(2, 128, 2, 128), bf(2, 128, 2, 128), *rows)
+    fp8 = u8(2, 128, 2, 128), u8(2, 128, 2, 128), torch.zeros((2, 2, 128)), torch.zeros((2, 2, 128))
+    with pytest.raises(ValueError, match="CUDA"):
+        api.rope_kv_cache_write_fp8(*fp8, *rows)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.kv_cache_read_fp8(*fp8, i32(3))
+
+
+def test_pair_axis_takes_any_sequence_of_the_right_length():
+    from paged_kv_cache_77_gb300 import api
+
+    for axis in ([0, 1, 2, 1], (0, 1, 2, 1), np.array([0, 1, 2, 1]), np.array([0, 1, 2, 1], dtype=np.uint8)):
+        arr, address = api._axis_array(axis, 8)
+        assert list(arr) == [0, 1, 2, 1] and address == (
+            arr.ctypes.data if isinstance(arr, np.ndarray) else arr.buffer_info()[0])
+    assert api._axis_array(None, 8) == (None, None)
+    for axis in ([0, 1, 2], np.zeros((2, 2)), np.zeros(5)):
+        with pytest.raises(ValueError, match="pair_axis"):
+            api._axis_array(axis, 8)

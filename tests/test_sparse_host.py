@@ -59,3 +59,19 @@ def test_workspace_is_that_of_a_batch_of_rows():
             lib.pkv_decode_workspace_size(B * Q, 64, 8, 128)
     assert lib.pkv_decode_sparse_workspace_size(4, 0, 64, 8, 128) == 0
     assert lib.pkv_decode_sparse_workspace_size(1 << 20, 1 << 20, 64, 8, 128) == 0
+
+
+def test_the_binding_refuses_host_tensors():
+    import torch
+
+    from paged_kv_cache_77_gb300 import api
+
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    cache, summaries, q, table, lens = bf(3, 128, 2, 128), bf(3, 2, 2, 128), bf(1, 4, 128), i32(1, 2), i32(1)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.update_block_summaries(summaries, cache, table, lens, i32(1), 1)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.select_blocks(q, summaries, table, lens, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.paged_attention_decode_sparse(q, cache, cache, table, lens, i32(1, 2, 2), 0.1)
