@@ -530,7 +530,7 @@ int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32
   a.max_blocks = max_blocks_per_seq;
   a.max_new = max_new;
   clear_error();
-  return launch_status(launch_block_summaries(a, (cudaStream_t)stream), what);
+  return launch_status(launch_block_summaries(a, (cudaStream_t)stream, current_num_sms()), what);
 }
 
 int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summaries,

@@ -53,18 +53,20 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
 
 // ------------------------------------------------------------------ summaries
 // One group of kWarps warps per (sequence, touched block, kv head). Half a warp holds a row of
-// 256 bytes (16 bytes a lane), so a warp takes two rows at a time; a lane has four in flight. The halves meet by a shuffle, the warps through shared
-// memory, and the old summary joins in where the block held rows before this step.
+// 256 bytes (16 bytes a lane), so a warp takes two rows at a time, and a lane has several loads
+// in flight. The halves meet by a shuffle, the warps through shared memory, and the old summary
+// joins in where the block held rows before this step.
 // Roofline: HBM; 256 B per new key and kv head read, 512 B per touched block and kv head
 // written, and read where the block was begun earlier.
 template <int kWarps>
 __global__ void __launch_bounds__(256, kWarps == 1 ? 4 : 8)
     block_summary_kernel(const __grid_constant__ SummaryArgs a) {
   constexpr int kGroups = 8 / kWarps;            // groups of a 256-thread CTA
-  // Rows a lane holds at a time: with 4 and eight resident CTAs per SM, prefill chunks of 16
-  // sequences take 22.0 us (GB300, 127 MB: 85 % of the copy rate); 4 and six CTAs 23.3, 8 and
-  // five 23.5, 8 and three 31.3, 2 and eight 23.7.
-  constexpr int kRowsAtOnce = 4;
+  // Rows a lane holds at a time. Prefill chunks of 16 sequences (127 MB), a warp per item: 8 rows
+  // and four resident CTAs per SM 20.2 us (GB300, 93 % of the copy rate), 8 and three 22.6, 4 and
+  // four 20.5, 4 and six 23.2. A CTA per item: 4 and eight 22.0, 4 and six 23.3, 8 and five 23.5,
+  // 2 and eight 23.7.
+  constexpr int kRowsAtOnce = kWarps == 1 ? 8 : 4;
   __shared__ uint4 part[8][32];
   pdl_wait_then_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,12 +144,15 @@ __global__ void __launch_bounds__(256, kWarps == 1 ? 4 : 8)
   *dst = acc;
 }
 
-cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream) {
+cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, int num_sms) {
   const int64_t items = (int64_t)a.B * a.span * a.Hkv;
   if (items == 0) return cudaSuccess;
-  // Few new rows per block: a warp per (block, head) reads them in one go. From 16 rows on a
-  // whole CTA shares a block's rows.
-  if (a.max_new <= 16)
+  // A warp per item, unless whole blocks come in fewer than 4 items per SM: then the eight warps
+  // of a CTA share one. Measured with 8 kv heads (us, warp and CTA): one sequence of 1,024 new
+  // rows (72 items) 4.1 and 2.9, of 8,192 (520 items) 4.3 and 3.9; 64 sequences of 64 (1,024
+  // items) 3.5 and 4.9, 512 of 64 11.0 and 19.3, 16 of 8,192 37.5 and 39.1; 16 sequences of 16,
+  // which leave most of a CTA's warps without a row, 2.6 and 3.0.
+  if (a.max_new <= 16 || items >= 4 * (int64_t)num_sms)
     return launch_dependent(block_summary_kernel<1>, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, stream, a);
   return launch_dependent(block_summary_kernel<8>, dim3((unsigned)items), dim3(256), 0, stream, a);
 }
@@ -178,6 +183,8 @@ namespace {
 constexpr int kSelWarps = 8;
 constexpr int kSelThreads = 32 * kSelWarps;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxChunk = 4096;           // blocks whose keys a CTA holds, 64 KB
+static_assert(kSelectMaxBlocks <= kMaxCluster * kMaxChunk, "a row's keys fit its cluster");
 constexpr int kDigitBits = 9;             // two digits of this size decide most 32-bit searches
 constexpr int kDigits = 1 << kDigitBits;  // two per thread
 constexpr int kWarpKeys = 8;              // keys of a lane where one warp selects
@@ -882,6 +889,11 @@ static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cud
   int chunk_cap = ((a.max_blocks + C - 1) / C + 7) & ~7;
   if (chunk_cap < alone) chunk_cap = alone;
   const size_t smem = (size_t)chunk_cap * 16;  // fp64 keys, fp32 keys, candidates
+  if (smem > 16 * 1024) {  // with the static part more than a kernel gets unasked
+    const cudaError_t e = cudaFuncSetAttribute(select_blocks_kernel<kRounds>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxChunk * 16);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * C));
   cfg.blockDim = dim3(kSelThreads);
@@ -902,17 +914,22 @@ static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cud
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int num_sms) {
   const int64_t segs = (int64_t)a.B * a.q_len * a.Hkv;
   if (segs == 0) return cudaSuccess;
-  // A cluster is as wide as it takes to give every SM two CTAs, as long as each of its CTAs
-  // has a round of 64 blocks to score, and wide enough that a CTA's keys stay within 16 KB.
+  // Cluster width. While the grid is at most one CTA per SM, wider as long as a CTA keeps 150
+  // blocks; up to two CTAs per SM where it keeps 500; and wide enough that a CTA's keys stay
+  // within 64 KB. Measured on GB300 (us for 1, 2, 4, 8 CTAs a row): 8 rows of 600 blocks 11.7,
+  // 10.7, 10.0, 11.3; 32 of 1,000 15.9, 12.6, 11.0, 15.0; 8 of 8,000 -, 51, 31, 22; 32 of 8,000
+  // -, 69, 43, 37; 128 of 600 17.2, 18.0, 26, 55; 128 of 2,000 41, 34, 41, 70; 512 of 1,000 59,
+  // 77, 103, 213.
   int C = 1;
-  while (C < kMaxCluster && (a.max_blocks > 1024 * C ||
-                             (segs * C < 2 * num_sms && a.max_blocks > C * kSelWarps * 8)))
-    C *= 2;
-  // Two groups of 8 blocks in flight where a warp has several to go (few CTAs per SM then, so
-  // loads in flight are what counts): 2 x 2 rows of 8 kv heads over a million tokens take 32 us
-  // with two on GB300, 42 us with one. One where the registers buy resident CTAs: 512 rows of up
-  // to 256 blocks, 15.2 us.
-  if (a.max_blocks > 4 * 64 * C) return launch_select_n<2>(a, C, segs, stream);
+  auto worth = [&](int64_t c) {
+    return segs * c <= num_sms ? a.max_blocks >= 150 * c : segs * c <= 2 * num_sms && a.max_blocks >= 500 * c;
+  };
+  while (C < kMaxCluster && (a.max_blocks > kMaxChunk * C || worth(2 * C))) C *= 2;
+  // Two groups of 8 blocks in flight where a warp has several to go: 512 rows of 600 blocks take
+  // 39.5 us, 45.8 with one, 2 x 2 rows of 8 kv heads over a million tokens 32 us and 42. One where
+  // a row is one CTA's and the registers buy resident CTAs: 512 rows of up to 256 blocks 15.2 us,
+  // 18.3 with two.
+  if (a.max_blocks > 32 * kWarpKeys) return launch_select_n<2>(a, C, segs, stream);
   return launch_select_n<1>(a, C, segs, stream);
 }
 

@@ -52,7 +52,7 @@ cudaError_t launch_kv_read_fp8(void* k, void* v, const void* k_cache, const void
                                int* dev_status, cudaStream_t stream, int num_sms);
 
 // Block summaries and block selection (block_select.cu).
-constexpr int kSelectMaxBlocks = 8192;  // table width that a selection's shared memory holds
+constexpr int kSelectMaxBlocks = 8192;  // widest table of a selection: a million tokens
 struct SummaryArgs {
   uint8_t* summaries;         // [nb, Hkv, 2, 128] bf16: minima, maxima
   const uint8_t* k_cache;     // [nb, 128, Hkv, 128] bf16
@@ -64,7 +64,7 @@ struct SummaryArgs {
   int B, Hkv, max_blocks, max_new;
   int span;                   // blocks that max_new new rows can touch
 };
-cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream);
+cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, int num_sms);
 struct SelectArgs {
   const uint16_t* q;          // [B, q_len, H, 128] bf16
   const uint8_t* summaries;

@@ -268,6 +268,78 @@ def test_selection_by_a_cluster_decides_ties_and_special_values(n, width, H):
     assert {9, n - 9} <= set(want[0, 0, 0])
 
 
+@pytest.mark.parametrize("B,Hkv,n,H", [(64, 8, 1500, 8), (16, 8, 2500, 32), (39, 8, 5000, 16),
+                                       (40, 8, 8192, 8), (4, 1, 8192, 2)])
+def test_selection_of_many_long_rows(B, Hkv, n, H):
+    """Runs of thousands of blocks per CTA, with as many rows as leave a row one CTA or a few.
+    The rows share their blocks; small whole numbers tie by the thousand."""
+    rng = np.random.default_rng(n)
+    nb = 9000
+    table = rng.integers(0, nb, (B, n)).astype(np.int32)
+    lens = rng.integers((n - 200) * BS, n * BS + 1, B)
+    lens[-1] = n * BS
+    t = ints(table)
+    q = torch.from_numpy(rng.standard_normal((B, H, D))).to(torch.bfloat16).cuda()
+    g = torch.Generator(device="cuda").manual_seed(n)
+    s = torch.randn((nb, Hkv, 2, D), generator=g, device="cuda").sort(dim=2).values.to(torch.bfloat16)
+    whole = torch.randint(-1, 2, (nb, Hkv, 2, D), generator=g, device="cuda").sort(dim=2).values
+    whole[..., 3:] = 0
+    for K in (1, 64, n // 2):
+        assert torch.equal(api.select_blocks(q, s, t, ints(lens), K), _torch_select(q, s, t, lens, K))
+        q1, w = torch.ones_like(q), whole.to(torch.bfloat16)
+        assert torch.equal(api.select_blocks(q1, w, t, ints(lens), K), _torch_select(q1, w, t, lens, K))
+
+
+def test_blocks_past_four_gigabytes():
+    """A cache whose last blocks lie beyond 2^32 bytes: summaries, selection, attention, the
+    rotary write and the FP8 read give what a small cache of the same blocks gives."""
+    nb, Hkv, H, n = 16500, 8, 16, 12
+    g = torch.Generator(device="cuda").manual_seed(3)
+    small = [torch.randn((n + 1, BS, Hkv, D), generator=g, device="cuda").to(torch.bfloat16)
+             for _ in range(2)]
+    big = [torch.empty((nb, BS, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    far = nb - n + torch.arange(n, device="cuda", dtype=torch.int32)
+    near = 1 + torch.arange(n, device="cuda", dtype=torch.int32)
+    for b, x in zip(big, small):
+        b[nb - n:] = x[1:]
+    # The rows of the first block are written through the rotary write.
+    q, k, v = (torch.randn((BS, h, D), generator=g, device="cuda").to(torch.bfloat16) for h in (H, Hkv, Hkv))
+    angle = torch.rand((BS, D // 2), generator=g, device="cuda")
+    rope = torch.cat([angle.cos(), angle.sin()], 1)
+    row = torch.arange(BS, device="cuda", dtype=torch.int32)
+    lens, new = ints([n * BS - 40]), ints([n * BS - 40])
+    results = []
+    for (kc, vc), t in ((small, near), (big, far)):
+        st = status()
+        rotated = api.rope_kv_cache_write(kc, vc, q, k, v, rope, row, int(t[0]) * BS + row, dev_status=st)
+        s = torch.zeros((kc.shape[0], Hkv, 2, D), dtype=torch.bfloat16, device="cuda")
+        api.update_block_summaries(s, kc, t.view(1, n), lens, new, int(new), dev_status=st)
+        idx = api.select_blocks(rotated[:1], s, t.view(1, n), lens, 5, dev_status=st)
+        out = api.paged_attention_decode_sparse(rotated[:1], kc, vc, t.view(1, n), lens, idx, D ** -0.5,
+                                                dev_status=st)
+        assert int(st.item()) == 0
+        results.append([rotated, s[t.long()], idx, out, kc[t.long()], vc[t.long()]])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    del big, kc, vc
+    nb = 33000  # blocks of half the bytes
+    codes = [torch.empty((nb, BS, Hkv, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.empty((nb, Hkv, BS), device="cuda") for _ in range(2)]
+    slots = (nb - 1) * BS + row
+    st = status()
+    api.rope_kv_cache_write_fp8(*codes, *scales, q, k, v, rope, row, slots, dev_status=st)
+    got = api.kv_cache_read_fp8(*codes, *scales, slots, dev_status=st)
+    last = [c[-1:].clone() for c in codes] + [c[-1:].clone() for c in scales]
+    want = api.kv_cache_read_fp8(*last, row, dev_status=st)
+    other = [torch.empty_like(x) for x in last]
+    api.rope_kv_cache_write_fp8(*other, q, k, v, rope, row, row, dev_status=st)
+    assert int(st.item()) == 0
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for a, b in zip(last, other):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_selection_with_special_values():
     rng = np.random.default_rng(4)
     n, K = 30, 6
