@@ -161,8 +161,9 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, in
 // One cluster of C CTAs per (query row, kv head). Each CTA scores one run of the row's blocks
 // and keeps their keys (order-preserving whole numbers) in its shared memory. A row of at most
 // 256 competing blocks is one CTA's, and is selected by one warp with the keys in registers;
-// for longer ones the CTAs select together, exchanging histograms and counts through
-// distributed shared memory.
+// of longer ones all keys go to the shared memory of the cluster's first CTA, which selects with
+// the keys in registers. Only where many blocks are at the border the CTAs select together,
+// exchanging histograms and counts through distributed shared memory.
 //
 // Scores are taken in fp32, 512 coalesced bytes per block (lanes 0-15 hold the minima and N,
 // lanes 16-31 the maxima and P, 8 channels each), 8 blocks per warp at a time whose sums are
@@ -174,8 +175,9 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, in
 // (one rounding in P and N, 5 in a lane's sum of products, 5 in the reduction, and room for
 // the bound's own), finds the K-th largest fp32 score tau to within a bin narrower
 // than eps, takes every block above the bin by more than 2 eps and none below it by more, and
-// scores the blocks between again in fp64 where they are more than the places left. The
-// result is that of fp64 scores, ties to the lower block, whatever the order of the fp32 sums.
+// scores the blocks between again where they are more than the places left: few of them in pairs
+// of fp32 numbers, and in fp64 where those do not tell them apart. The result is that of fp64
+// scores, ties to the lower block, whatever the order of the fp32 sums.
 //
 // A block whose score is NaN (a NaN key, or infinite keys that cancel) ranks above all others.
 namespace {
@@ -218,18 +220,31 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
-// Shared memory of one CTA. What other CTAs of the cluster read (hist, pub, the keys) is
+// What decides a row: keys above `sure` are in, keys below `maybe` are out, and of those between
+// the `need` best by more exact scores.
+struct Border {
+  uint32_t maybe, sure;
+  int need, settled;
+};
+
+// Digit counts: 4 passes over 32-bit keys, 8 over 64.
+using Hist = int[4 + 8][kDigits];
+
+// Shared memory of one CTA. What other CTAs of the cluster read (counts, pub, the keys) is
 // written once per kernel and place, so one cluster barrier between the writes and the reads
 // is enough.
 struct SelShared {
   float coef[2 * kDim], coef_low[2 * kDim];  // N, then P: their fp32 sums and what those left out
-  int hist[4 + 8][kDigits];              // digit counts: 4 passes over 32-bit keys, 8 over 64
-  unsigned long long pub[5][2];          // a pair of numbers per exchange
+  unsigned long long pub[4][2];          // a pair of numbers per exchange
   unsigned long long lo[kSelWarps], hi[kSelWarps];
   float size[kSelWarps];
   uint32_t any_q[kSelWarps], amax[kSelWarps];
   int warp_sum[kSelWarps], warp_sum2[kSelWarps];
-  int digit, above, inside, candidates;
+  int digit, above, inside, candidates, done;
+  uint32_t few[32], best;                // a single CTA's candidates, and which are taken
+  unsigned long long few64[32];          // their keys
+  Border border;
+  uint32_t range[kMaxCluster][3];        // smallest and largest key and largest |summary| of each CTA
 };
 
 struct Cluster {
@@ -300,6 +315,88 @@ __device__ void score64(const Row& row, const SelShared& sh, const uint32_t* can
   }
 }
 
+// The same in pairs of fp32 numbers: a sum and, beside it, what its roundings left out (Knuth's
+// two-sum, and a product's error by a fused multiply-add). With `reach` what bounds a score and
+// its partial sums, the second numbers of a level of the 13 additions are below 15 2^-24 reach in
+// all and rounded twice a level: the result is off by less than 2^-39 reach. In fp32 arithmetic
+// four candidates take a tenth of the time that they take in fp64.
+// A key is the order key of the rounded sum, then that of the rest.
+__device__ void score_pairs(const Row& row, const SelShared& sh, const uint32_t* cand,
+                            unsigned long long* keys, int n) {
+  // Eight lanes a candidate, 32 channels a lane. One loop of 8 channels: unrolled over all of
+  // them the code's fetch costs more than the loop.
+  const int lane = threadIdx.x & 31, r = lane >> 3, sub = lane & 7;
+  const int blk = r < n ? __ldg(row.table + cand[r]) : -1;
+  const bool good = blk >= 0 && (int64_t)blk < row.num_blocks;
+  const uint8_t* at = row.sum + (good ? blk : 0) * row.sum_stride + (sub - lane) * 16;
+  uint4 x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = ld_nc_v4(at + k * 128);
+  float s = 0.f, rest = 0.f;
+  auto add = [](float& s, float& rest, float p, float e) {
+    const float sum = add_ieee(s, p);
+    const float back = sub_ieee(sum, s);
+    const float lost = add_ieee(sub_ieee(s, sub_ieee(sum, back)), sub_ieee(p, back));
+    rest = add_ieee(rest, add_ieee(lost, e));
+    s = sum;
+  };
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const float* c = sh.coef + 8 * (sub + 8 * k);
+    const float* low = sh.coef_low + 8 * (sub + 8 * k);
+    const uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      const float p = mul_ieee(c[i], v);
+      add(s, rest, p, fma_ieee(low[i], v, fma_ieee(c[i], v, neg_ieee(p))));
+    }
+    x[0] = x[1], x[1] = x[2], x[2] = x[3];
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1)
+    add(s, rest, __shfl_xor_sync(0xffffffffu, s, o), __shfl_xor_sync(0xffffffffu, rest, o));
+  float low = 0.f;
+  add(s, low, rest, 0.f);
+  if (sub == 0 && r < n)
+    keys[r] = good ? (unsigned long long)order_key(s) << 32 | order_key(low) : 0ull;
+}
+
+// Keys that decide: exact zeros as they are, the others in fp64.
+__device__ __forceinline__ void exact_keys(const Row& row, const SelShared& sh, const uint32_t* key32,
+                                           const uint32_t* cand, unsigned long long* key64, int n) {
+  const int lane = threadIdx.x & 31;
+  if (!row.exact)
+    score64(row, sh, cand, key64, n);
+  else if (lane < n)
+    key64[lane] = key32[cand[lane]];
+}
+
+// Up to 32 candidates, those of lanes [0, n): the rank of a lane's, those above it and those equal
+// to it at lower places counted; 32 in the other lanes.
+__device__ int rank_in_warp(unsigned long long mine, uint32_t place, int n) {
+  int rank = (threadIdx.x & 31) < n ? 0 : 32;
+  for (int s = 0; s < n; ++s) {
+    const unsigned long long other = __shfl_sync(0xffffffffu, mine, s);
+    const uint32_t where = __shfl_sync(0xffffffffu, place, s);
+    rank += other > mine || (other == mine && where < place);
+  }
+  return rank;
+}
+
+// Whether the best `need` of the lanes' candidates are theirs by more than the pairs' errors.
+// (A bad block's key 0 is a NaN here, and decides nothing; nor do sums near the subnormals,
+// which order_key takes for zero.)
+__device__ bool decided(const Row& row, unsigned long long mine, int rank, int need) {
+  const unsigned last = __ballot_sync(0xffffffffu, rank == need - 1);
+  const unsigned next = __ballot_sync(0xffffffffu, rank == need);
+  const unsigned long long a = __shfl_sync(0xffffffffu, mine, __ffs(last) - 1);
+  const unsigned long long b = __shfl_sync(0xffffffffu, mine, __ffs(next) - 1);
+  const float gap = (key_score((uint32_t)(a >> 32)) - key_score((uint32_t)(b >> 32))) +
+                    (key_score((uint32_t)a) - key_score((uint32_t)b));
+  return gap > row.eps * 0x1p-13f + 1e-37f;  // eps is 14 2^-24 of the bound
+}
+
 // Low bits of the keys that need not be decided: a bin of 2^bits keys in [kmin, kmax] is
 // narrower than eps, for its scores are at most the largest magnitude's 2^-23 apart.
 __device__ __forceinline__ int spare_bits(const Row& row, uint32_t kmin, uint32_t kmax) {
@@ -309,8 +406,7 @@ __device__ __forceinline__ int spare_bits(const Row& row, uint32_t kmin, uint32_
   return min(max(bits, 0), 31);
 }
 
-// [maybe, sure] from the bin [lo, hi] that holds the K-th largest key: keys above `sure` are
-// in, keys below `maybe` are out.
+// [maybe, sure] from the bin [lo, hi] that holds the K-th largest key.
 __device__ __forceinline__ void border(const Row& row, uint32_t lo, uint32_t hi, uint32_t* maybe,
                                        uint32_t* sure) {
   *maybe = 0;
@@ -365,6 +461,15 @@ __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* ke
                              : (c & 1023u) >= (uint32_t)want         ? 1
                                                                      : 0;
       lo |= digit << bits;
+      if (digit && (c >> (10 * digit - 10) & 1023u) == (uint32_t)want) {
+        // The keys from lo on are as many as wanted: the least of them is the one looked for.
+        uint32_t least = 0xffffffffu;
+#pragma unroll
+        for (int u = 0; u < kWarpKeys; ++u) least = k[u] >= lo ? min(least, k[u]) : least;
+        lo = __reduce_min_sync(0xffffffffu, least);
+        bits = 0;
+        break;
+      }
     } while (bits > spare);
     hi = lo | ((1u << bits) - 1);
   }
@@ -389,26 +494,32 @@ __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* ke
       nc += __popc(mask);
     }
     __syncwarp();
-    for (int r = 0; r < nc; r += 4) {
-      if (row.exact) {
-        if (lane < 4 && r + lane < nc) key64[r + lane] = key32[cand[r + lane]];
-      } else {
-        score64(row, sh, cand + r, key64 + r, min(4, nc - r));
-      }
+    bool done = false;
+    if (nc <= 32 && row.bounded && !row.exact) {
+      for (int r = 0; r < nc; r += 4) score_pairs(row, sh, cand + r, key64 + r, min(4, nc - r));
+      __syncwarp();
+      const unsigned long long mine = lane < nc ? key64[lane] : 0;
+      const int rank = rank_in_warp(mine, lane, nc);
+      done = decided(row, mine, rank, need);
+      if (done && lane < nc) cand[lane] |= rank < need ? 0x80000000u : 0u;
+      __syncwarp();
     }
-    __syncwarp();
-    // A candidate's rank: those above it, and those equal to it in lower blocks.
+    if (!done) {
+      for (int r = 0; r < nc; r += 4) exact_keys(row, sh, key32, cand + r, key64 + r, min(4, nc - r));
+      __syncwarp();
+      // A candidate's rank: those above it, and those equal to it in lower blocks.
 #pragma unroll 1
-    for (int u = 0; u < kWarpKeys; ++u) {
-      if (32 * u >= nc) break;
-      const int r = lane + 32 * u;
-      const unsigned long long mine = r < nc ? key64[r] : 0;
-      int rank = 0;
-      for (int s = 0; s < nc; ++s) {
-        const unsigned long long other = key64[s];
-        rank += other > mine || (other == mine && s < r);
+      for (int u = 0; u < kWarpKeys; ++u) {
+        if (32 * u >= nc) break;
+        const int r = lane + 32 * u;
+        const unsigned long long mine = r < nc ? key64[r] : 0;
+        int rank = 0;
+        for (int s = 0; s < nc; ++s) {
+          const unsigned long long other = key64[s];
+          rank += other > mine || (other == mine && s < r);
+        }
+        if (r < nc) cand[r] |= rank < need ? 0x80000000u : 0u;
       }
-      if (r < nc) cand[r] |= rank < need ? 0x80000000u : 0u;
     }
     __syncwarp();
     // Back to the lanes that hold the keys; the r-th candidate in ascending order is cand[r].
@@ -440,12 +551,12 @@ struct Bin {
   int above, inside;
 };
 
-// The k-th largest of the cluster's keys (this CTA's are keys[0, n); all are in [kmin, kmax])
-// to within a bin of 2^spare values, or one that `done` accepts, by 9 bits at a time below the
-// bits they share. Every pass counts digits in its own histogram hist[pass], zero beforehand.
-template <typename Key, typename Done>
-__device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kmax, int spare,
-                                int (*hist)[kDigits], SelShared& sh, const Cluster& cl, Done done) {
+// The k-th largest of the cluster's keys (each(f) calls f for this thread's; all are in [kmin,
+// kmax]) to within a bin of 2^spare values, or one that `done` accepts, by 9 bits at a time below
+// the bits they share. Every pass counts digits in its own histogram hist[pass], zero beforehand.
+template <typename Key, typename Each, typename Done>
+__device__ Bin<Key> kth_largest(Each each, int k, Key kmin, Key kmax, int spare, int (*hist)[kDigits],
+                                SelShared& sh, const Cluster& cl, Done done) {
   Bin<Key> b = {kmin, kmax, 0, 0};
   if (kmin == kmax) return b;
   const int top = 8 * (int)sizeof(Key) - 1 -
@@ -454,10 +565,9 @@ __device__ Bin<Key> kth_largest(const Key* keys, int n, int k, Key kmin, Key kma
   for (int pass = 0, high = top;; ++pass) {
     const int shift = high >= kDigitBits ? high - kDigitBits + 1 : 0;  // digit: bits [shift, high]
     const Key mask = (Key)((1u << (high - shift + 1)) - 1);
-    for (int i = threadIdx.x; i < n; i += kSelThreads) {
-      const Key key = keys[i];
+    each([&](Key key) {
       if (key >= b.lo && key <= b.hi) atomicAdd(&hist[pass][(int)((key >> shift) & mask)], 1);
-    }
+    });
     cl.sync();
     // Thread t holds digits 511 - 2t and 510 - 2t, so that a prefix sum counts the larger ones.
     int upper = 0, lower = 0;
@@ -555,134 +665,194 @@ __device__ void compact(int n, SelShared& sh, Pick pick, Put put) {
   __syncthreads();
 }
 
-// Selection by the cluster: CTA `rank` holds the keys of m blocks from `first` on.
-__device__ void select_by_cluster(const Row& row, SelShared& sh, const Cluster& cl, uint32_t* key32,
-                                  unsigned long long* key64, uint32_t* cand, int m, int want,
-                                  int first, uint32_t kmin, uint32_t kmax, int32_t* out) {
+// Selection by one CTA of the `want` best of n blocks, to out in ascending order, where at most 32
+// blocks are at the border. Otherwise it writes nothing and returns what is known of the border.
+// Warp w has one run of the keys, in registers: elements 128 u + 4 lane + c of the run in k[4 u + c].
+__device__ Border select_few(const Row& row, SelShared& sh, Hist& hist, const uint32_t* keys, int n,
+                             int want, int first, uint32_t kmin, uint32_t kmax, int32_t* out) {
+  constexpr int kQuads = kSelectMaxBlocks / (4 * kSelThreads);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t lo = 0, hi = 0, maybe, sure;
+  const int quads = (n + 4 * kSelThreads - 1) / (4 * kSelThreads);
+  const int base = warp * quads * 128 + 4 * lane;
+  uint32_t k[4 * kQuads];  // 0 behind the row's end: no larger than any key
+#pragma unroll
+  for (int u = 0; u < kQuads; ++u) {
+    const int i = base + 128 * u;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (u < quads && i < n) x = *reinterpret_cast<const uint4*>(keys + i);
+    k[4 * u] = x.x;
+    k[4 * u + 1] = i + 1 < n ? x.y : 0;
+    k[4 * u + 2] = i + 2 < n ? x.z : 0;
+    k[4 * u + 3] = i + 3 < n ? x.w : 0;
+  }
+  const Cluster alone = {1, 0};
+  uint32_t lo = 0, hi = 0;
   if (row.bounded) {
     const Bin<uint32_t> bin = kth_largest<uint32_t>(
-        key32, m, want, kmin, kmax, spare_bits(row, kmin, kmax), sh.hist, sh, cl,
+        [&](auto f) {
+#pragma unroll
+          for (int j = 0; j < 4 * kQuads; ++j)
+            if (j < 4 * quads) f(k[j]);
+        },
+        want, kmin, kmax, spare_bits(row, kmin, kmax), hist, sh, alone,
         [](const Bin<uint32_t>&) { return false; });
     lo = bin.lo;
     hi = bin.hi;
   }
-  border(row, lo, hi, &maybe, &sure);
-  int in = 0, surely = 0;
-  for (int i = threadIdx.x; i < m; i += kSelThreads) {
-    in += key32[i] >= maybe;
-    surely += key32[i] > sure;
-  }
-  Counted t = count_cluster(in, surely, 1, sh, cl);
-  uint32_t pass = maybe;  // keys from here on are taken
-  if (t.all_a > want) {
-    // More blocks in reach of the border than places: score them in fp64.
-    const int need = want - t.all_c;
-    for (int i = threadIdx.x; i < 8 * kDigits; i += kSelThreads) (&sh.hist[4][0])[i] = 0;
-    for (int i = threadIdx.x; i < m; i += kSelThreads)
-      if (key32[i] >= maybe && key32[i] <= sure) cand[atomicAdd(&sh.candidates, 1)] = i;
-    __syncthreads();
-    const int nc = sh.candidates;
-    unsigned long long lo64 = ~0ull, hi64 = 0;
-    for (int r = warp * 4; r < nc; r += kSelWarps * 4) {
-      if (row.exact) {
-        if (lane < 4 && r + lane < nc) key64[r + lane] = key32[cand[r + lane]];
-      } else {
-        score64(row, sh, cand + r, key64 + r, min(4, nc - r));
-      }
-      __syncwarp();
-      for (int s = r; s < min(nc, r + 4); ++s) {
-        lo64 = min(lo64, key64[s]);
-        hi64 = max(hi64, key64[s]);
-      }
-    }
-    if (lane == 0) {
-      sh.lo[warp] = lo64;
-      sh.hi[warp] = hi64;
-    }
-    if (threadIdx.x == 0) sh.pub[2][0] = nc;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kSelWarps; ++w) {
-        sh.lo[0] = min(sh.lo[0], sh.lo[w]);
-        sh.hi[0] = max(sh.hi[0], sh.hi[w]);
-      }
-      sh.pub[3][0] = sh.lo[0];
-      sh.pub[3][1] = sh.hi[0];
-    }
-    cl.sync();
-    const int theirs = lane < cl.size ? (int)cl.read(&sh.pub[2][0], lane) : 0;
-    const int all = __reduce_add_sync(0xffffffffu, theirs);
-    if (all <= 32) {
-      // Few: lane l of the first warp of every CTA takes the l-th of them all and ranks it.
-      if (warp == 0) {
-        int owner = cl.size, at = lane;
+  Border b = {0, 0, want, 0};
+  border(row, lo, hi, &b.maybe, &b.sure);
+  if (lo == 0) return b;
+  uint32_t picks = 0, edge = 0;  // a bit per key
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-          const int have = __shfl_sync(0xffffffffu, theirs, r);
-          if (owner == cl.size && r < cl.size) {
-            if (at < have)
-              owner = r;
-            else
-              at -= have;
-          }
-        }
-        const bool have = owner < cl.size;
-        const unsigned long long mine = have ? cl.read(key64 + at, owner) : 0;
-        const uint32_t i = have ? cl.read(cand + at, owner) : 0;
-        const uint32_t place = (uint32_t)owner << 16 | i;  // ascending blocks over the cluster
-        int rank = 0;
-        for (int s = 0; s < all; ++s) {
-          const unsigned long long other = __shfl_sync(0xffffffffu, mine, s);
-          const uint32_t where = __shfl_sync(0xffffffffu, place, s);
-          rank += other > mine || (other == mine && where < place);
-        }
-        if (owner == cl.rank) key32[i] = rank < need ? kTaken : 0u;
+  for (int j = 0; j < 4 * kQuads; ++j) {
+    picks |= (uint32_t)(k[j] > b.sure) << j;
+    edge |= (uint32_t)(k[j] >= b.maybe && k[j] <= b.sure) << j;
+  }
+  const Counted t = count_cluster(__popc(picks), __popc(edge), 0, sh, alone);
+  b.need = want - t.all_a;
+  if (t.all_c > 32 && t.all_c > b.need) return b;
+  b.settled = 1;
+  if (t.all_c == b.need) {
+    picks |= edge;
+  } else {
+    // More blocks at the border than places: score them again, and rank them, one a lane.
+    const int nc = t.all_c;
+    for (uint32_t e = edge; e; e &= e - 1) {
+      const int j = __ffs(e) - 1;
+      sh.few[atomicAdd(&sh.candidates, 1)] = base + 32 * (j & ~3) + (j & 3);
+    }
+    __syncthreads();
+    for (bool pairs = !row.exact;; pairs = false) {
+      if (4 * warp < nc) {
+        if (pairs)
+          score_pairs(row, sh, sh.few + 4 * warp, sh.few64 + 4 * warp, min(4, nc - 4 * warp));
+        else
+          exact_keys(row, sh, keys, sh.few + 4 * warp, sh.few64 + 4 * warp, min(4, nc - 4 * warp));
       }
       __syncthreads();
-    } else {
-      for (int r = 0; r < cl.size; ++r) {
-        lo64 = min(lo64, cl.read(&sh.pub[3][0], r));
-        hi64 = max(hi64, cl.read(&sh.pub[3][1], r));
+      if (warp == 0) {
+        const unsigned long long mine = lane < nc ? sh.few64[lane] : 0;
+        const int rank = rank_in_warp(mine, lane < nc ? sh.few[lane] : 0, nc);
+        const bool done = !pairs || decided(row, mine, rank, b.need);
+        const unsigned best = __ballot_sync(0xffffffffu, rank < b.need);
+        if (lane == 0) {
+          sh.done = done;
+          sh.best = best;
+        }
       }
-      // All keys of the bin are taken, or (one value) as many of the lowest blocks as it takes.
-      const Bin<unsigned long long> bin = kth_largest<unsigned long long>(
-          key64, nc, need, lo64, hi64, 0, sh.hist + 4, sh, cl,
-          [&](const Bin<unsigned long long>& x) { return x.above + x.inside == need; });
-      int at_edge = 0;
-      for (int r = threadIdx.x; r < nc; r += kSelThreads) {
-        const bool edge = key64[r] >= bin.lo && key64[r] <= bin.hi;
-        at_edge += edge;
-        key32[cand[r]] = key64[r] > bin.hi ? kTaken : edge ? kEdge : 0u;
-      }
-      const int rest = need - bin.above - count_cluster(at_edge, 0, 4, sh, cl).before_a;
-      compact(
-          m, sh, [&](int i) { return key32[i] == kEdge; },
-          [&](int k, int i) { key32[i] = k < rest ? kTaken : 0u; });
+      __syncthreads();
+      if (sh.done) break;
     }
-    pass = sure + 1;
-    in = 0;
-    for (int i = threadIdx.x; i < m; i += kSelThreads) in += key32[i] >= pass;
-    // The first exchange's place is free again: every CTA has read it and passed a barrier since.
-    t = count_cluster(in, 0, 1, sh, cl);
+    for (uint32_t e = edge; e; e &= e - 1) {
+      const int j = __ffs(e) - 1;
+      const uint32_t i = base + 32 * (j & ~3) + (j & 3);
+      for (uint32_t x = sh.best; x; x &= x - 1)
+        if (sh.few[__ffs(x) - 1] == i) picks |= 1u << j;
+    }
   }
+  const int mine = (int)__reduce_add_sync(0xffffffffu, __popc(picks));
+  if (lane == 0) sh.warp_sum[warp] = mine;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) out += sh.warp_sum[w];
+#pragma unroll 1
+  for (int u = 0; u < quads; ++u, picks >>= 4) {
+    const uint32_t own = picks & 15u;
+    if (!__any_sync(0xffffffffu, own)) continue;
+    int before = 0, all = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const unsigned mask = __ballot_sync(0xffffffffu, own >> c & 1);
+      before += __popc(mask & ((1u << lane) - 1));
+      all += __popc(mask);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (own >> c & 1) out[before++] = first + base + 128 * u + c;
+    out += all;
+  }
+  return b;
+}
+
+// Selection by a cluster, whose CTA `rank` holds the keys of m blocks from `first` on, with more
+// than 32 blocks at the border: those are scored in fp64.
+__device__ void select_many(const Row& row, SelShared& sh, Hist& hist, const Cluster& cl, uint32_t* key32,
+                            unsigned long long* key64, uint32_t* cand, int m, int first, const Border& b,
+                            int32_t* out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 8 * kDigits; i += kSelThreads) (&hist[4][0])[i] = 0;
+  for (int i = threadIdx.x; i < m; i += kSelThreads)
+    if (key32[i] >= b.maybe && key32[i] <= b.sure) cand[atomicAdd(&sh.candidates, 1)] = i;
+  __syncthreads();
+  const int nc = sh.candidates;
+  unsigned long long lo64 = ~0ull, hi64 = 0;
+  for (int r = warp * 4; r < nc; r += kSelWarps * 4) {
+    exact_keys(row, sh, key32, cand + r, key64 + r, min(4, nc - r));
+    __syncwarp();
+    for (int s = r; s < min(nc, r + 4); ++s) {
+      lo64 = min(lo64, key64[s]);
+      hi64 = max(hi64, key64[s]);
+    }
+  }
+  if (lane == 0) {
+    sh.lo[warp] = lo64;
+    sh.hi[warp] = hi64;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kSelWarps; ++w) {
+      sh.lo[0] = min(sh.lo[0], sh.lo[w]);
+      sh.hi[0] = max(sh.hi[0], sh.hi[w]);
+    }
+    sh.pub[1][0] = sh.lo[0];
+    sh.pub[1][1] = sh.hi[0];
+  }
+  cl.sync();
+  for (int r = 0; r < cl.size; ++r) {
+    lo64 = min(lo64, cl.read(&sh.pub[1][0], r));
+    hi64 = max(hi64, cl.read(&sh.pub[1][1], r));
+  }
+  // All keys of the bin are taken, or (one value) as many of the lowest blocks as it takes.
+  const Bin<unsigned long long> bin = kth_largest<unsigned long long>(
+      [&](auto f) {
+        for (int i = threadIdx.x; i < nc; i += kSelThreads) f(key64[i]);
+      },
+      b.need, lo64, hi64, 0, hist + 4, sh, cl,
+      [&](const Bin<unsigned long long>& x) { return x.above + x.inside == b.need; });
+  int at_edge = 0;
+  for (int r = threadIdx.x; r < nc; r += kSelThreads) {
+    const bool edge = key64[r] >= bin.lo && key64[r] <= bin.hi;
+    at_edge += edge;
+    key32[cand[r]] = key64[r] > bin.hi ? kTaken : edge ? kEdge : 0u;
+  }
+  const int rest = b.need - bin.above - count_cluster(at_edge, 0, 2, sh, cl).before_a;
   compact(
-      m, sh, [&](int i) { return key32[i] >= pass; },
-      [&](int r, int i) { out[t.before_a + r] = first + i; });
+      m, sh, [&](int i) { return key32[i] == kEdge; },
+      [&](int k, int i) { key32[i] = k < rest ? kTaken : 0u; });
+  int in = 0;
+  for (int i = threadIdx.x; i < m; i += kSelThreads) in += key32[i] > b.sure;
+  const int before = count_cluster(in, 0, 3, sh, cl).before_a;
+  compact(
+      m, sh, [&](int i) { return key32[i] > b.sure; },
+      [&](int r, int i) { out[before + r] = first + i; });
   if (cl.size > 1) cl.sync();  // the others may still be reading this CTA's shared memory
 }
 
 }  // namespace
 
-// kRounds: groups of 8 blocks whose summaries a warp has in flight at a time.
-template <int kRounds>
-__global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
+// kWide: for tables of more blocks than one warp selects, or (to be narrow) a CTA. A warp has two
+// groups of 8 blocks' summaries in flight, which takes 512 rows of 600 blocks 39.5 us, 45.8 with
+// one. Narrow, the registers of a second group buy resident CTAs: 512 rows of 256 blocks take 14.0
+// us with one group and four CTAs per SM, 17.2 with three, 19.5 with five (whose registers spill);
+// two groups took 18.3 where one took 15.2.
+template <bool kWide>
+__global__ void __launch_bounds__(kSelThreads, kWide ? 2 : 4)
     select_blocks_kernel(const __grid_constant__ SelectArgs a, int chunk_cap) {
-  extern __shared__ unsigned long long sel_smem[];
+  extern __shared__ __align__(16) unsigned long long sel_smem[];
   __shared__ SelShared sh;
+  __shared__ int hist[kWide ? 12 : 1][kDigits];
   pdl_wait_then_launch();
-  const Cluster cl = {(int)cg::this_cluster().num_blocks(), (int)cg::this_cluster().block_rank()};
+  const Cluster cl = {kWide ? (int)cg::this_cluster().num_blocks() : 1,
+                      kWide ? (int)cg::this_cluster().block_rank() : 0};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t seg = blockIdx.x / cl.size;  // (query row, kv head)
   const int g = (int)(seg % a.Hkv);
@@ -690,6 +860,54 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
   const int b = (int)(qrow / a.q_len), qi = (int)(qrow % a.q_len);
   const int cap = a.max_blocks * kBs;
   const int raw = __ldg(a.seq_lens + b);
+
+  const int len = clamp_len(raw, cap);
+  if (len != raw && g == 0 && qi == 0 && cl.rank == 0 && threadIdx.x == 0)
+    flag_status(a.dev_status, PKV_DEV_BAD_LENGTH);
+  const int row_len = len - a.q_len + 1 + qi;
+  const int n = row_len > 0 ? (row_len + kBs - 1) / kBs : 0;
+  const int K = a.num_selected;
+  int32_t* out = a.out + seg * K;
+  // Blocks [0, e0) and [e1, n) are always taken; the others compete for `want` places.
+  const int e0 = a.num_sink, e1 = n - a.num_recent;
+  const int want = K - a.num_sink - a.num_recent;
+  if (cl.rank == 0) {
+    if (n <= K) {
+      for (int i = threadIdx.x; i < K; i += kSelThreads) out[i] = i < n ? i : -1;
+    } else {
+      for (int i = threadIdx.x; i < e0; i += kSelThreads) out[i] = i;
+      for (int i = threadIdx.x; i < a.num_recent; i += kSelThreads) out[e0 + want + i] = e1 + i;
+    }
+  }
+  if (n <= K || want == 0) return;  // the whole cluster takes this way
+  out += e0;
+  const int total = e1 - e0;  // > want
+  // Few blocks are one CTA's work, however wide the table and with it the cluster.
+  const bool by_warp = !kWide || total <= 32 * kWarpKeys;
+  if (by_warp && cl.rank) return;
+  // This CTA's run of competing blocks: [first, first + m).
+  const int chunk = by_warp ? total : ((total + cl.size - 1) / cl.size + 7) & ~7;
+  const int first = e0 + cl.rank * chunk;
+  const int m = max(0, min(chunk, e1 - first));
+  // [chunk_cap], and [max_blocks] in the same place: the keys of the whole row, which the first
+  // CTA of a cluster has for as long as it selects by itself.
+  unsigned long long* key64 = sel_smem;
+  uint32_t* gathered = reinterpret_cast<uint32_t*>(sel_smem);
+  const bool many = kWide && !by_warp && cl.size > 1;
+  uint32_t* key32 = gathered + (kWide && cl.size > 1 ? max(2 * chunk_cap, a.max_blocks) : 2 * chunk_cap);
+  uint32_t* cand = key32 + chunk_cap;  // [chunk_cap] each
+  Row row;
+  row.table = a.block_table + (int64_t)b * a.max_blocks + first;
+  row.sum = a.summaries + (int64_t)g * kSumBytes + lane * 16;
+  row.sum_stride = (int64_t)a.Hkv * kSumBytes;
+  row.num_blocks = a.num_blocks;
+  constexpr int kGroup = kWide ? 16 : 8;
+  // Table entries of a group, one per lane; a group that ends the run repeats its last block,
+  // so that every load below is unconditional and all of them are in flight together.
+  auto entry = [&](int j) { return j < m ? __ldg(row.table + min(j + (lane & (kGroup - 1)), m - 1)) : 0; };
+  int next = entry(warp * kGroup);
+
+  if (many) cg::this_cluster().barrier_arrive();
 
   // ---- coefficients: thread d sums N (d < 128) or P of its channel over the heads, and what
   // the fp32 sums leave out (the error of each addition, found exactly)
@@ -729,58 +947,21 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
     }
     if (threadIdx.x == 0) sh.candidates = 0;
   }
-
-  const int len = clamp_len(raw, cap);
-  if (len != raw && g == 0 && qi == 0 && cl.rank == 0 && threadIdx.x == 0)
-    flag_status(a.dev_status, PKV_DEV_BAD_LENGTH);
-  const int row_len = len - a.q_len + 1 + qi;
-  const int n = row_len > 0 ? (row_len + kBs - 1) / kBs : 0;
-  const int K = a.num_selected;
-  int32_t* out = a.out + seg * K;
-  // Blocks [0, e0) and [e1, n) are always taken; the others compete for `want` places.
-  const int e0 = a.num_sink, e1 = n - a.num_recent;
-  const int want = K - a.num_sink - a.num_recent;
-  if (cl.rank == 0) {
-    if (n <= K) {
-      for (int i = threadIdx.x; i < K; i += kSelThreads) out[i] = i < n ? i : -1;
-    } else {
-      for (int i = threadIdx.x; i < e0; i += kSelThreads) out[i] = i;
-      for (int i = threadIdx.x; i < a.num_recent; i += kSelThreads) out[e0 + want + i] = e1 + i;
-    }
-  }
-  if (n <= K || want == 0) return;  // the whole cluster takes this way
-  out += e0;
-  const int total = e1 - e0;  // > want
-  // Few blocks are one CTA's work, however wide the table and with it the cluster.
-  const bool by_warp = total <= 32 * kWarpKeys;
-  if (by_warp && cl.rank) return;
-  // This CTA's run of competing blocks: [first, first + m).
-  const int chunk = by_warp ? total : ((total + cl.size - 1) / cl.size + 7) & ~7;
-  const int first = e0 + cl.rank * chunk;
-  const int m = max(0, min(chunk, e1 - first));
-  unsigned long long* key64 = sel_smem;                                 // [chunk_cap]
-  uint32_t* key32 = reinterpret_cast<uint32_t*>(sel_smem + chunk_cap);  // [chunk_cap]
-  uint32_t* cand = key32 + chunk_cap;                                   // [chunk_cap]
   if (!by_warp)
-    for (int i = threadIdx.x; i < 4 * kDigits; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < 4 * kDigits; i += kSelThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
 
   // ---- fp32 scores
-  Row row;
-  row.table = a.block_table + (int64_t)b * a.max_blocks + first;
-  row.sum = a.summaries + (int64_t)g * kSumBytes + lane * 16;
-  row.sum_stride = (int64_t)a.Hkv * kSumBytes;
-  row.num_blocks = a.num_blocks;
   uint64_t coef[4];  // of channels 2i and 2i + 1
 #pragma unroll
   for (int i = 0; i < 4; ++i) coef[i] = f2pack(sh.coef[8 * lane + 2 * i], sh.coef[8 * lane + 2 * i + 1]);
-  constexpr int kGroup = 8 * kRounds;
+  uint32_t* far = nullptr;
+  if (many) {
+    cg::this_cluster().barrier_wait();  // every CTA runs: its shared memory can be written
+    far = cg::this_cluster().map_shared_rank(gathered, 0) + (first - e0);
+  }
   uint32_t vmax = 0;  // the largest |summary| of the even and the odd channels (NaN: the largest bits)
   uint32_t kmin = 0xffffffffu, kmax = 0;
-  // Table entries of a group, one per lane; a group that ends the run repeats its last block,
-  // so that every load below is unconditional and all of them are in flight together.
-  auto entry = [&](int j) { return j < m ? __ldg(row.table + min(j + (lane & (kGroup - 1)), m - 1)) : 0; };
-  int next = entry(warp * kGroup);
   for (int j0 = warp * kGroup; j0 < m; j0 += kSelWarps * kGroup) {
     const int blk = next;
     next = entry(j0 + kSelWarps * kGroup);
@@ -830,6 +1011,7 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
       if ((lane & 3) == 0 && j0 + u < m) {
         const uint32_t key = bad_mask >> u & 1 ? 0u : order_key(v[0]);
         key32[j0 + u] = key;
+        if (many) far[j0 + u] = key;
         kmin = min(kmin, key);
         kmax = max(kmax, key);
       }
@@ -849,21 +1031,23 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
   if (by_warp && warp) return;
   top = __reduce_max_sync(0xffffffffu, sh.amax[lane & 7]);
   if (!by_warp) {
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < cl.size) {  // thread r tells CTA r
       uint32_t lo = 0xffffffffu, hi = 0;
       for (int w = 0; w < kSelWarps; ++w) {
         lo = min(lo, (uint32_t)sh.lo[w]);
         hi = max(hi, (uint32_t)sh.hi[w]);
       }
-      sh.pub[0][0] = ((unsigned long long)lo << 32) | hi;
-      sh.pub[0][1] = top;
+      uint32_t* to = sh.range[cl.rank];
+      if (cl.size > 1) to = cg::this_cluster().map_shared_rank(to, threadIdx.x);
+      to[0] = lo;
+      to[1] = hi;
+      to[2] = top;
     }
     cl.sync();
-    const int r = lane < cl.size ? lane : 0;  // lane r reads CTA r's numbers
-    const unsigned long long both = cl.read(&sh.pub[0][0], r);
-    kmin = __reduce_min_sync(0xffffffffu, (uint32_t)(both >> 32));
-    kmax = __reduce_max_sync(0xffffffffu, (uint32_t)both);
-    top = __reduce_max_sync(0xffffffffu, (uint32_t)cl.read(&sh.pub[0][1], r));
+    const int r = lane < cl.size ? lane : 0;
+    kmin = __reduce_min_sync(0xffffffffu, sh.range[r][0]);
+    kmax = __reduce_max_sync(0xffffffffu, sh.range[r][1]);
+    top = __reduce_max_sync(0xffffffffu, sh.range[r][2]);
   }
   float size = 0.f;
   uint32_t any = 0;
@@ -877,20 +1061,35 @@ __global__ void __launch_bounds__(kSelThreads, kRounds == 1 ? 3 : 2)
   row.bounded = reach < 1e37f;
   row.exact = row.bounded && (any == 0 || top == 0);
   row.eps = row.exact ? 0.f : reach * (14.f * 0x1p-24f) + 1e-35f;
-  if (by_warp)
-    select_by_warp(row, sh, key32, key64, cand, m, want, first, out);
-  else
-    select_by_cluster(row, sh, cl, key32, key64, cand, m, want, first, kmin, kmax, out);
+  if constexpr (kWide) {
+    if (!by_warp) {
+      // One CTA selects where few blocks are at the border: a barrier of the cluster with a read of
+      // another CTA's shared memory takes about a microsecond, and a selection by all CTAs six.
+      Border b;
+      if (cl.rank == 0) b = select_few(row, sh, hist, many ? gathered : key32, total, want, e0, kmin, kmax, out);
+      if (many) {
+        if (cl.rank == 0 && threadIdx.x < cl.size)
+          *cg::this_cluster().map_shared_rank(&sh.border, threadIdx.x) = b;
+        cl.sync();
+        b = sh.border;
+      }
+      if (!b.settled) select_many(row, sh, hist, cl, key32, key64, cand, m, first, b, out);
+      return;
+    }
+  }
+  select_by_warp(row, sh, key32, key64, cand, m, want, first, out);
 }
 
-template <int kRounds>
+template <bool kWide>
 static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cudaStream_t stream) {
   const int alone = a.max_blocks < 32 * kWarpKeys ? a.max_blocks : 32 * kWarpKeys;
   int chunk_cap = ((a.max_blocks + C - 1) / C + 7) & ~7;
   if (chunk_cap < alone) chunk_cap = alone;
-  const size_t smem = (size_t)chunk_cap * 16;  // fp64 keys, fp32 keys, candidates
+  // fp64 keys (or all fp32 keys of a cluster's row), fp32 keys, candidates
+  const size_t shared = C > 1 && a.max_blocks > 2 * chunk_cap ? a.max_blocks : 2 * chunk_cap;
+  const size_t smem = (shared + 2 * chunk_cap) * 4;
   if (smem > 16 * 1024) {  // with the static part more than a kernel gets unasked
-    const cudaError_t e = cudaFuncSetAttribute(select_blocks_kernel<kRounds>,
+    const cudaError_t e = cudaFuncSetAttribute(select_blocks_kernel<kWide>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxChunk * 16);
     if (e != cudaSuccess) return e;
   }
@@ -908,29 +1107,22 @@ static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cud
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_blocks_kernel<kRounds>, a, chunk_cap);
+  return cudaLaunchKernelEx(&cfg, select_blocks_kernel<kWide>, a, chunk_cap);
 }
 
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int num_sms) {
   const int64_t segs = (int64_t)a.B * a.q_len * a.Hkv;
   if (segs == 0) return cudaSuccess;
-  // Cluster width. While the grid is at most one CTA per SM, wider as long as a CTA keeps 150
-  // blocks; up to two CTAs per SM where it keeps 500; and wide enough that a CTA's keys stay
-  // within 64 KB. Measured on GB300 (us for 1, 2, 4, 8 CTAs a row): 8 rows of 600 blocks 11.7,
-  // 10.7, 10.0, 11.3; 32 of 1,000 15.9, 12.6, 11.0, 15.0; 8 of 8,000 -, 51, 31, 22; 32 of 8,000
-  // -, 69, 43, 37; 128 of 600 17.2, 18.0, 26, 55; 128 of 2,000 41, 34, 41, 70; 512 of 1,000 59,
-  // 77, 103, 213.
+  // Cluster width: as wide as a grid of one CTA per SM allows, or two where the rows are long, and
+  // enough that a CTA's keys stay within 64 KB. Measured on GB300 (us for 1, 2, 4, 8 CTAs a row): 8
+  // rows of 600 blocks 11.6, 10.2, 8.7, 7.7; 32 of 280 9.1, 9.2, 8.3, 8.7; 32 of 1,000 15.4, 11.8,
+  // 9.5, 9.4; 32 of 8,000 -, 67, 41, 32; 128 of 600 13.9, 14.5, 21, 33; 128 of 1,000 16.8, 15.9,
+  // 22, 34; 128 of 8,000 -, 90, 103, 119; 512 of 1,000 56, 71, 89, 137.
   int C = 1;
-  auto worth = [&](int64_t c) {
-    return segs * c <= num_sms ? a.max_blocks >= 150 * c : segs * c <= 2 * num_sms && a.max_blocks >= 500 * c;
-  };
-  while (C < kMaxCluster && (a.max_blocks > kMaxChunk * C || worth(2 * C))) C *= 2;
-  // Two groups of 8 blocks in flight where a warp has several to go: 512 rows of 600 blocks take
-  // 39.5 us, 45.8 with one, 2 x 2 rows of 8 kv heads over a million tokens 32 us and 42. One where
-  // a row is one CTA's and the registers buy resident CTAs: 512 rows of up to 256 blocks 15.2 us,
-  // 18.3 with two.
-  if (a.max_blocks > 32 * kWarpKeys) return launch_select_n<2>(a, C, segs, stream);
-  return launch_select_n<1>(a, C, segs, stream);
+  const int64_t most = (a.max_blocks >= 800 ? 2 : 1) * (int64_t)num_sms;
+  while (C < kMaxCluster && (a.max_blocks > kMaxChunk * C || segs * 2 * C <= most)) C *= 2;
+  if (a.max_blocks > 32 * kWarpKeys) return launch_select_n<true>(a, C, segs, stream);
+  return launch_select_n<false>(a, 1, segs, stream);
 }
 
 }  // namespace pkv

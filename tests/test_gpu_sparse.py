@@ -290,6 +290,29 @@ def test_selection_of_many_long_rows(B, Hkv, n, H):
         assert torch.equal(api.select_blocks(q1, w, t, ints(lens), K), _torch_select(q1, w, t, lens, K))
 
 
+@pytest.mark.parametrize("n", [40, 256, 700, 3000])
+@pytest.mark.parametrize("power", [-8, -13, -20, -28, -36, -42])
+def test_selection_at_borders_of_every_closeness(n, power):
+    """Scores that differ from their neighbours by steps between fp32's reach and that of 64 bits
+    (whole sums below 2^9 and steps of 2^-41 are exact in 53 bits; random scores of bf16 values are
+    rounded by less than 2^-42 in any order): in twos, so that borders between equals occur too."""
+    rng = np.random.default_rng(n - power)
+    table, nb = make_table(rng, [n * BS])
+    q = torch.ones((1, 2, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 2.0 ** power
+    base = torch.randint(-1, 2, (nb, 1, 1, D), generator=torch.Generator().manual_seed(n))
+    base[..., 4:] = 1
+    s = base.expand(nb, 1, 2, D).to(torch.bfloat16).cuda().contiguous()
+    s[..., 0] = torch.from_numpy(rng.permutation(nb) // 2 % 100).to(torch.bfloat16).cuda()[:, None, None]
+    for K in (1, 7, 20, n // 3, n // 2):
+        check_select(q, s, table, [n * BS], K, 0, 0)
+    for K in (5, n // 4):  # and among random scores
+        s = random_summaries(rng, nb, 1)
+        s[nb // 2:] = s[:nb - nb // 2].clone()
+        s[nb // 2:, :, :, 0] += 2.0
+        check_select(q, s, table, [n * BS], K, 0, 1)
+
+
 def test_blocks_past_four_gigabytes():
     """A cache whose last blocks lie beyond 2^32 bytes: summaries, selection, attention, the
     rotary write and the FP8 read give what a small cache of the same blocks gives."""
