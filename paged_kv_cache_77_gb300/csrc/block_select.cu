@@ -49,6 +49,17 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// d = A B with A of 16 rows and 16 columns, B of 8 columns. Lane 4 i + c holds of A the columns
+// 2c, 2c + 1 of rows i and i + 8, then 2c + 8, 2c + 9 of both; of B those rows of column i; of d
+// columns 2c, 2c + 1 of row i, then of row i + 8.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ summaries
@@ -165,15 +176,19 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, in
 // the keys in registers. Only where many blocks are at the border the CTAs select together,
 // exchanging histograms and counts through distributed shared memory.
 //
-// Scores are taken in fp32, 512 coalesced bytes per block (lanes 0-15 hold the minima and N,
-// lanes 16-31 the maxima and P, 8 channels each), 8 blocks per warp at a time whose sums are
-// reduced across the lanes together. Selection needs exact order only at the border, so the
-// kernel bounds the fp32 error,
+// Scores are matrix products of bf16 numbers with fp32 sums: a fp32 coefficient is the sum of three
+// bf16 numbers, so a row's coefficients are three columns of 256, and 16 summaries, as they lie in
+// memory, the rows of the other factor. A warp multiplies them 16 channels at a time (mma.sync: the
+// operands come straight from global memory to registers, once, and there are 3 or 6 columns), in
+// an order of the channels that lets a lane load 16 bytes. Products with fused multiply-adds and
+// sums over the lanes took 50 cycles a block and half the kernel's time: 8 rows of 8,000 blocks 18.6
+// us, 14.7 so. Selection needs exact order only at the border, so the kernel bounds the error,
 //
-//   |score32 - score| <= eps = 14 2^-24 (sum_d P_d + |N_d|) max |summary|
+//   |score32 - score| <= eps = 56 2^-24 (sum_d P_d + |N_d|) max |summary|
 //
-// (one rounding in P and N, 5 in a lane's sum of products, 5 in the reduction, and room for
-// the bound's own), finds the K-th largest fp32 score tau to within a bin narrower
+// (the 16 sums of a product, each at least as good as a truncation to 24 bits: 32; the 16 products'
+// sum 16; the columns' 3; the coefficients 1; room for the bound's own), and finds the K-th largest
+// fp32 score tau to within a bin narrower
 // than eps, takes every block above the bin by more than 2 eps and none below it by more, and
 // scores the blocks between again where they are more than the places left: few of them in pairs
 // of fp32 numbers, and in fp64 where those do not tell them apart. The result is that of fp64
@@ -185,13 +200,15 @@ namespace {
 constexpr int kSelWarps = 8;
 constexpr int kSelThreads = 32 * kSelWarps;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxChunk = 4096;           // blocks whose keys a CTA holds, 64 KB
+constexpr int kMaxChunk = 2048;           // blocks whose keys a CTA holds
+constexpr int kMaxKeys = kSelectMaxBlocks > 2 * kMaxChunk ? kSelectMaxBlocks : 2 * kMaxChunk;
 static_assert(kSelectMaxBlocks <= kMaxCluster * kMaxChunk, "a row's keys fit its cluster");
 constexpr int kDigitBits = 9;             // two digits of this size decide most 32-bit searches
 constexpr int kDigits = 1 << kDigitBits;  // two per thread
 constexpr int kWarpKeys = 8;              // keys of a lane where one warp selects
 constexpr uint32_t kNanKey = 0xfffffffeu;
 constexpr uint32_t kTaken = 0xffffffffu;  // above every score's key
+constexpr uint32_t kBad = 0xffffffffu;    // half a score of a bad block: no sum's NaN has these bits
 constexpr uint32_t kEdge = kNanKey;       // candidates at the border, once no key is a NaN's
 
 // Order-preserving whole numbers for scores; -0 and +0 are equal, NaN is the largest. Key 0
@@ -234,17 +251,23 @@ using Hist = int[4 + 8][kDigits];
 // written once per kernel and place, so one cluster barrier between the writes and the reads
 // is enough.
 struct SelShared {
-  float coef[2 * kDim], coef_low[2 * kDim];  // N, then P: their fp32 sums and what those left out
   unsigned long long pub[4][2];          // a pair of numbers per exchange
   unsigned long long lo[kSelWarps], hi[kSelWarps];
-  float size[kSelWarps];
-  uint32_t any_q[kSelWarps], amax[kSelWarps];
   int warp_sum[kSelWarps], warp_sum2[kSelWarps];
   int digit, above, inside, candidates, done;
   uint32_t few[32], best;                // a single CTA's candidates, and which are taken
   unsigned long long few64[32];          // their keys
+  uint32_t top[kSelWarps], tops[kMaxCluster];  // largest |summary| of each warp and each CTA
+};
+
+// The same for a query row.
+struct RowShared {
+  float coef[2 * kDim], coef_low[2 * kDim];  // N, then P: their fp32 sums and what those left out
+  float size[kSelWarps];
+  uint32_t any_q[kSelWarps];
+  uint32_t lo[kSelWarps], hi[kSelWarps];     // smallest and largest key of each warp
+  uint32_t los[kMaxCluster], his[kMaxCluster];  // and of each CTA
   Border border;
-  uint32_t range[kMaxCluster][3];        // smallest and largest key and largest |summary| of each CTA
 };
 
 struct Cluster {
@@ -261,8 +284,9 @@ struct Cluster {
   }
 };
 
-// Where a row's blocks lie and what bounds their scores.
+// A row's coefficients, where its blocks lie and what bounds their scores.
 struct Row {
+  const float *coef, *coef_low;
   const int32_t* table;  // of the CTA's first block
   const uint8_t* sum;    // the lane's 16 bytes of block 0's summary
   int64_t sum_stride, num_blocks;
@@ -284,7 +308,7 @@ __device__ __forceinline__ double widen_bits(uint32_t bits) {
 // operation of a warp costs some 70 to 90 cycles here, so there are few: 8 additions for the
 // coefficients and 16 operations a candidate, no conversions (a smaller version with
 // conversions, always four candidates, took 9.7k cycles instead of 6k).
-__device__ void score64(const Row& row, const SelShared& sh, const uint32_t* cand,
+__device__ void score64(const Row& row, const uint32_t* cand,
                         unsigned long long* key64, int n) {
   const int lane = threadIdx.x & 31;
   uint4 x[4];
@@ -298,8 +322,8 @@ __device__ void score64(const Row& row, const SelShared& sh, const uint32_t* can
   double k[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    k[i] = widen_bits(__float_as_uint(sh.coef[8 * lane + i])) +
-           widen_bits(__float_as_uint(sh.coef_low[8 * lane + i]));
+    k[i] = widen_bits(__float_as_uint(row.coef[8 * lane + i])) +
+           widen_bits(__float_as_uint(row.coef_low[8 * lane + i]));
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (r >= n) break;
@@ -321,7 +345,7 @@ __device__ void score64(const Row& row, const SelShared& sh, const uint32_t* can
 // all and rounded twice a level: the result is off by less than 2^-39 reach. In fp32 arithmetic
 // four candidates take a tenth of the time that they take in fp64.
 // A key is the order key of the rounded sum, then that of the rest.
-__device__ void score_pairs(const Row& row, const SelShared& sh, const uint32_t* cand,
+__device__ void score_pairs(const Row& row, const uint32_t* cand,
                             unsigned long long* keys, int n) {
   // Eight lanes a candidate, 32 channels a lane. One loop of 8 channels: unrolled over all of
   // them the code's fetch costs more than the loop.
@@ -342,8 +366,8 @@ __device__ void score_pairs(const Row& row, const SelShared& sh, const uint32_t*
   };
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
-    const float* c = sh.coef + 8 * (sub + 8 * k);
-    const float* low = sh.coef_low + 8 * (sub + 8 * k);
+    const float* c = row.coef + 8 * (sub + 8 * k);
+    const float* low = row.coef_low + 8 * (sub + 8 * k);
     const uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -363,11 +387,11 @@ __device__ void score_pairs(const Row& row, const SelShared& sh, const uint32_t*
 }
 
 // Keys that decide: exact zeros as they are, the others in fp64.
-__device__ __forceinline__ void exact_keys(const Row& row, const SelShared& sh, const uint32_t* key32,
+__device__ __forceinline__ void exact_keys(const Row& row, const uint32_t* key32,
                                            const uint32_t* cand, unsigned long long* key64, int n) {
   const int lane = threadIdx.x & 31;
   if (!row.exact)
-    score64(row, sh, cand, key64, n);
+    score64(row, cand, key64, n);
   else if (lane < n)
     key64[lane] = key32[cand[lane]];
 }
@@ -394,7 +418,7 @@ __device__ bool decided(const Row& row, unsigned long long mine, int rank, int n
   const unsigned long long b = __shfl_sync(0xffffffffu, mine, __ffs(next) - 1);
   const float gap = (key_score((uint32_t)(a >> 32)) - key_score((uint32_t)(b >> 32))) +
                     (key_score((uint32_t)a) - key_score((uint32_t)b));
-  return gap > row.eps * 0x1p-13f + 1e-37f;  // eps is 14 2^-24 of the bound
+  return gap > row.eps * 0x1p-15f + 1e-37f;  // eps is at least 56 2^-24 of the bound
 }
 
 // Low bits of the keys that need not be decided: a bin of 2^bits keys in [kmin, kmax] is
@@ -425,7 +449,7 @@ __device__ __forceinline__ void border(const Row& row, uint32_t lo, uint32_t hi,
 // ascending order, to out[i] = first + block. Lane l holds blocks l, l + 32, ...: counting the
 // keys from a threshold on takes 8 comparisons and a warp sum, so the K-th largest is found two
 // bits at a time, from the highest in which the keys differ down to a bin narrower than eps.
-__device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* key32,
+__device__ void select_by_warp(const Row& row, const uint32_t* key32,
                                unsigned long long* key64, uint32_t* cand, int m, int want, int first,
                                int32_t* out) {
   const int lane = threadIdx.x & 31;
@@ -496,7 +520,7 @@ __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* ke
     __syncwarp();
     bool done = false;
     if (nc <= 32 && row.bounded && !row.exact) {
-      for (int r = 0; r < nc; r += 4) score_pairs(row, sh, cand + r, key64 + r, min(4, nc - r));
+      for (int r = 0; r < nc; r += 4) score_pairs(row, cand + r, key64 + r, min(4, nc - r));
       __syncwarp();
       const unsigned long long mine = lane < nc ? key64[lane] : 0;
       const int rank = rank_in_warp(mine, lane, nc);
@@ -505,7 +529,7 @@ __device__ void select_by_warp(const Row& row, SelShared& sh, const uint32_t* ke
       __syncwarp();
     }
     if (!done) {
-      for (int r = 0; r < nc; r += 4) exact_keys(row, sh, key32, cand + r, key64 + r, min(4, nc - r));
+      for (int r = 0; r < nc; r += 4) exact_keys(row, key32, cand + r, key64 + r, min(4, nc - r));
       __syncwarp();
       // A candidate's rank: those above it, and those equal to it in lower blocks.
 #pragma unroll 1
@@ -672,6 +696,9 @@ __device__ Border select_few(const Row& row, SelShared& sh, Hist& hist, const ui
                              int want, int first, uint32_t kmin, uint32_t kmax, int32_t* out) {
   constexpr int kQuads = kSelectMaxBlocks / (4 * kSelThreads);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 4 * kDigits; i += kSelThreads) (&hist[0][0])[i] = 0;
+  if (threadIdx.x == 0) sh.candidates = 0;
+  __syncthreads();
   const int quads = (n + 4 * kSelThreads - 1) / (4 * kSelThreads);
   const int base = warp * quads * 128 + 4 * lane;
   uint32_t k[4 * kQuads];  // 0 behind the row's end: no larger than any key
@@ -725,9 +752,9 @@ __device__ Border select_few(const Row& row, SelShared& sh, Hist& hist, const ui
     for (bool pairs = !row.exact;; pairs = false) {
       if (4 * warp < nc) {
         if (pairs)
-          score_pairs(row, sh, sh.few + 4 * warp, sh.few64 + 4 * warp, min(4, nc - 4 * warp));
+          score_pairs(row, sh.few + 4 * warp, sh.few64 + 4 * warp, min(4, nc - 4 * warp));
         else
-          exact_keys(row, sh, keys, sh.few + 4 * warp, sh.few64 + 4 * warp, min(4, nc - 4 * warp));
+          exact_keys(row, keys, sh.few + 4 * warp, sh.few64 + 4 * warp, min(4, nc - 4 * warp));
       }
       __syncthreads();
       if (warp == 0) {
@@ -780,13 +807,15 @@ __device__ void select_many(const Row& row, SelShared& sh, Hist& hist, const Clu
                             int32_t* out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 8 * kDigits; i += kSelThreads) (&hist[4][0])[i] = 0;
+  if (threadIdx.x == 0) sh.candidates = 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < m; i += kSelThreads)
     if (key32[i] >= b.maybe && key32[i] <= b.sure) cand[atomicAdd(&sh.candidates, 1)] = i;
   __syncthreads();
   const int nc = sh.candidates;
   unsigned long long lo64 = ~0ull, hi64 = 0;
   for (int r = warp * 4; r < nc; r += kSelWarps * 4) {
-    exact_keys(row, sh, key32, cand + r, key64 + r, min(4, nc - r));
+    exact_keys(row, key32, cand + r, key64 + r, min(4, nc - r));
     __syncwarp();
     for (int s = r; s < min(nc, r + 4); ++s) {
       lo64 = min(lo64, key64[s]);
@@ -839,81 +868,99 @@ __device__ void select_many(const Row& row, SelShared& sh, Hist& hist, const Clu
 
 }  // namespace
 
-// kWide: for tables of more blocks than one warp selects, or (to be narrow) a CTA. A warp has two
-// groups of 8 blocks' summaries in flight, which takes 512 rows of 600 blocks 39.5 us, 45.8 with
-// one. Narrow, the registers of a second group buy resident CTAs: 512 rows of 256 blocks take 14.0
-// us with one group and four CTAs per SM, 17.2 with three, 19.5 with five (whose registers spill);
-// two groups took 18.3 where one took 15.2.
-template <bool kWide>
+// kWide: for tables of more blocks than one warp selects, or (to be narrow) a CTA; kRows: query rows
+// of a sequence that a cluster selects for. A wide kernel's warp has 16 whole summaries in flight;
+// narrow, two warps share them, so that rows of 64 blocks keep all of them busy and 64 registers do,
+// for four CTAs per SM: 512 rows of 256 blocks take 14.0 us (three CTAs 17.1, five, whose registers
+// spill, 23.8), of 128 10.3 (12.7, 15.7), of random lengths up to 256 13.5 (12.5, 21).
+template <bool kWide, int kRows>
 __global__ void __launch_bounds__(kSelThreads, kWide ? 2 : 4)
     select_blocks_kernel(const __grid_constant__ SelectArgs a, int chunk_cap) {
   extern __shared__ __align__(16) unsigned long long sel_smem[];
   __shared__ SelShared sh;
+  __shared__ RowShared rows[kRows];
+  // Columns 0 to 2 (and 4 to 6 of a second row) hold a row's coefficients; what is in the others
+  // does not count. The stride keeps two columns' 64 bytes in different banks.
+  __shared__ __align__(16) uint16_t split[8][2 * kDim + 32];
   __shared__ int hist[kWide ? 12 : 1][kDigits];
   pdl_wait_then_launch();
   const Cluster cl = {kWide ? (int)cg::this_cluster().num_blocks() : 1,
                       kWide ? (int)cg::this_cluster().block_rank() : 0};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t seg = blockIdx.x / cl.size;  // (query row, kv head)
+  const int64_t seg = blockIdx.x / cl.size;  // (kRows query rows, kv head)
   const int g = (int)(seg % a.Hkv);
-  const int64_t qrow = seg / a.Hkv;
-  const int b = (int)(qrow / a.q_len), qi = (int)(qrow % a.q_len);
+  const int64_t group = seg / a.Hkv;
+  const int groups = (a.q_len + kRows - 1) / kRows;
+  const int b = (int)(group / groups), q0 = (int)(group % groups) * kRows;
   const int cap = a.max_blocks * kBs;
   const int raw = __ldg(a.seq_lens + b);
-
   const int len = clamp_len(raw, cap);
-  if (len != raw && g == 0 && qi == 0 && cl.rank == 0 && threadIdx.x == 0)
+  if (len != raw && g == 0 && q0 == 0 && cl.rank == 0 && threadIdx.x == 0)
     flag_status(a.dev_status, PKV_DEV_BAD_LENGTH);
-  const int row_len = len - a.q_len + 1 + qi;
-  const int n = row_len > 0 ? (row_len + kBs - 1) / kBs : 0;
   const int K = a.num_selected;
-  int32_t* out = a.out + seg * K;
-  // Blocks [0, e0) and [e1, n) are always taken; the others compete for `want` places.
-  const int e0 = a.num_sink, e1 = n - a.num_recent;
-  const int want = K - a.num_sink - a.num_recent;
-  if (cl.rank == 0) {
-    if (n <= K) {
-      for (int i = threadIdx.x; i < K; i += kSelThreads) out[i] = i < n ? i : -1;
-    } else {
-      for (int i = threadIdx.x; i < e0; i += kSelThreads) out[i] = i;
-      for (int i = threadIdx.x; i < a.num_recent; i += kSelThreads) out[e0 + want + i] = e1 + i;
+  // Blocks [0, e0) and the last num_recent are always taken; the others compete for `want` places.
+  const int e0 = a.num_sink, want = K - a.num_sink - a.num_recent;
+  int32_t* first_out = a.out + (((int64_t)b * a.q_len + q0) * a.Hkv + g) * K;
+  auto out = [&](int r) { return first_out + (kRows == 1 ? 0 : r * (int64_t)a.Hkv * K); };
+  int total[kRows];  // competing blocks (of the later row at least as many), 0: none to choose
+  int most = 0;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    total[r] = 0;
+    if (q0 + r >= a.q_len) continue;
+    const int row_len = len - a.q_len + 1 + q0 + r;
+    const int n = row_len > 0 ? (row_len + kBs - 1) / kBs : 0;
+    if (cl.rank == 0) {
+      if (n <= K) {
+        for (int i = threadIdx.x; i < K; i += kSelThreads) out(r)[i] = i < n ? i : -1;
+      } else {
+        for (int i = threadIdx.x; i < e0; i += kSelThreads) out(r)[i] = i;
+        for (int i = threadIdx.x; i < a.num_recent; i += kSelThreads)
+          out(r)[e0 + want + i] = n - a.num_recent + i;
+      }
     }
+    if (n > K && want > 0) total[r] = n - a.num_recent - e0;  // > want
+    most = max(most, total[r]);
   }
-  if (n <= K || want == 0) return;  // the whole cluster takes this way
-  out += e0;
-  const int total = e1 - e0;  // > want
+  if (most == 0) return;  // the whole cluster takes this way
   // Few blocks are one CTA's work, however wide the table and with it the cluster.
-  const bool by_warp = !kWide || total <= 32 * kWarpKeys;
+  const bool by_warp = !kWide || most <= 32 * kWarpKeys;
   if (by_warp && cl.rank) return;
-  // This CTA's run of competing blocks: [first, first + m).
-  const int chunk = by_warp ? total : ((total + cl.size - 1) / cl.size + 7) & ~7;
-  const int first = e0 + cl.rank * chunk;
-  const int m = max(0, min(chunk, e1 - first));
-  // [chunk_cap], and [max_blocks] in the same place: the keys of the whole row, which the first
-  // CTA of a cluster has for as long as it selects by itself.
+  const bool many = kWide && !by_warp && cl.size > 1;
+  if (many) cg::this_cluster().barrier_arrive();
+  // This CTA's run of competing blocks: [start, start + m), of a row as many of them as it has.
+  const int chunk = by_warp ? most : ((most + cl.size - 1) / cl.size + 7) & ~7;
+  const int start = cl.rank * chunk;
+  const int m = max(0, min(chunk, most - start));
+  // [chunk_cap], and [max_blocks] in the same place: the keys of a whole row, in the CTA of a
+  // cluster that selects for it, until it has.
   unsigned long long* key64 = sel_smem;
   uint32_t* gathered = reinterpret_cast<uint32_t*>(sel_smem);
-  const bool many = kWide && !by_warp && cl.size > 1;
   uint32_t* key32 = gathered + (kWide && cl.size > 1 ? max(2 * chunk_cap, a.max_blocks) : 2 * chunk_cap);
-  uint32_t* cand = key32 + chunk_cap;  // [chunk_cap] each
+  uint32_t* cand = key32 + kRows * chunk_cap;  // [chunk_cap] per row; [chunk_cap]
   Row row;
-  row.table = a.block_table + (int64_t)b * a.max_blocks + first;
+  row.table = a.block_table + (int64_t)b * a.max_blocks + e0 + start;
   row.sum = a.summaries + (int64_t)g * kSumBytes + lane * 16;
   row.sum_stride = (int64_t)a.Hkv * kSumBytes;
   row.num_blocks = a.num_blocks;
-  constexpr int kGroup = kWide ? 16 : 8;
+  constexpr int kGroup = 16;  // blocks of a matrix product
   // Table entries of a group, one per lane; a group that ends the run repeats its last block,
   // so that every load below is unconditional and all of them are in flight together.
   auto entry = [&](int j) { return j < m ? __ldg(row.table + min(j + (lane & (kGroup - 1)), m - 1)) : 0; };
-  int next = entry(warp * kGroup);
-
-  if (many) cg::this_cluster().barrier_arrive();
+  // Narrow, two warps share a group, one on the minima and one on the maxima.
+  constexpr int kShare = kWide ? 1 : 2;
+  constexpr int kSweep = kSelWarps / kShare * kGroup;
+  const int j00 = warp / kShare * kGroup;
+  int next = entry(j00);
 
   // ---- coefficients: thread d sums N (d < 128) or P of its channel over the heads, and what
   // the fp32 sums leave out (the error of each addition, found exactly)
-  {
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (total[r] == 0) continue;
     const int d = threadIdx.x;
-    const uint16_t* q = a.q + (qrow * a.H + (int64_t)g * a.n_rep) * kDim + d % kDim;
+    const uint16_t* q =
+        a.q + (((int64_t)b * a.q_len + q0 + r) * a.H + (int64_t)g * a.n_rep) * kDim + d % kDim;
     float sum = 0.f, low = 0.f;
     uint32_t any = 0;
     for (int h0 = 0; h0 < a.n_rep; h0 += 8) {
@@ -935,162 +982,210 @@ __global__ void __launch_bounds__(kSelThreads, kWide ? 2 : 4)
     const bool finite = abs_ieee(all) < INFINITY;
     low = finite ? add_ieee(low, sub_ieee(sum, all)) : 0.f;
     sum = finite ? all : sum;
-    sh.coef[d] = sum;
-    sh.coef_low[d] = low;
+    // Three bf16 numbers whose sum it is, one each 8 of its 24 bits.
+    const float high = __bfloat162float(__float2bfloat16_rn(sum));
+    const float rest = sub_ieee(sum, high);
+    const float mid = __bfloat162float(__float2bfloat16_rn(rest));
+    split[4 * r][d] = __float_as_uint(high) >> 16;
+    split[4 * r + 1][d] = __float_as_uint(mid) >> 16;
+    split[4 * r + 2][d] = __bfloat16_as_ushort(__float2bfloat16_rn(sub_ieee(rest, mid)));
+    rows[r].coef[d] = sum;
+    rows[r].coef_low[d] = low;
     float size = abs_ieee(sum);
 #pragma unroll
     for (int o = 16; o; o >>= 1) size = add_ieee(size, __shfl_xor_sync(0xffffffffu, size, o));
     any = __reduce_or_sync(0xffffffffu, any);
     if (lane == 0) {
-      sh.size[warp] = size;
-      sh.any_q[warp] = any;
+      rows[r].size[warp] = size;
+      rows[r].any_q[warp] = any;
     }
-    if (threadIdx.x == 0) sh.candidates = 0;
   }
-  if (!by_warp)
-    for (int i = threadIdx.x; i < 4 * kDigits; i += kSelThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
 
   // ---- fp32 scores
-  uint64_t coef[4];  // of channels 2i and 2i + 1
-#pragma unroll
-  for (int i = 0; i < 4; ++i) coef[i] = f2pack(sh.coef[8 * lane + 2 * i], sh.coef[8 * lane + 2 * i + 1]);
+  uint32_t kmin = 0xffffffffu, kmax = 0;  // of the row that the lane writes
   uint32_t* far = nullptr;
+  const int at = lane >> 2, c = lane & 3;  // place in the fragments
+  const int r = kRows == 1 ? 0 : c >> 1;
   if (many) {
     cg::this_cluster().barrier_wait();  // every CTA runs: its shared memory can be written
-    far = cg::this_cluster().map_shared_rank(gathered, 0) + (first - e0);
+    far = cg::this_cluster().map_shared_rank(gathered, r) + start;
   }
+  const int mine = c < 2 * kRows ? min(m, (kRows == 1 || r == 0 ? total[0] : total[kRows - 1]) - start) : 0;
   uint32_t vmax = 0;  // the largest |summary| of the even and the odd channels (NaN: the largest bits)
-  uint32_t kmin = 0xffffffffu, kmax = 0;
-  for (int j0 = warp * kGroup; j0 < m; j0 += kSelWarps * kGroup) {
+  constexpr int kPieces = 8 / kShare;  // 64-byte pieces of a summary
+  const int t0 = kPieces * (warp % kShare);
+  const uint8_t* sums = row.sum + (c - lane) * 16 + t0 * 64;
+  for (int j0 = j00; j0 < m; j0 += kSweep) {
     const int blk = next;
-    next = entry(j0 + kSelWarps * kGroup);
+    next = entry(j0 + kSweep);
     const bool bad = blk < 0 || (int64_t)blk >= a.num_blocks;
     const int from = bad ? 0 : blk;
-    uint4 x[kGroup];
-#pragma unroll
-    for (int u = 0; u < kGroup; ++u)
-      x[u] = ld_nc_v4(row.sum + __shfl_sync(0xffffffffu, from, u) * row.sum_stride);
+    const uint8_t* p = sums + __shfl_sync(0xffffffffu, from, at) * row.sum_stride;
+    const uint8_t* p8 = sums + __shfl_sync(0xffffffffu, from, at + 8) * row.sum_stride;
     const unsigned bad_mask = __ballot_sync(0xffffffffu, bad);
-    if (bad_mask) {  // block 0 stood in for them: it must not count in vmax
-      if (bad) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+    if (bad) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    uint4 x[kPieces], y[kPieces];
 #pragma unroll
-      for (int u = 0; u < kGroup; ++u)
-        if (bad_mask >> u & 1) x[u] = make_uint4(0, 0, 0, 0);
+    for (int t = 0; t < kPieces; ++t) {
+      x[t] = ld_nc_v4(p + t * 64);
+      y[t] = ld_nc_v4(p8 + t * 64);
+    }
+    if (bad_mask) {  // block 0 stood in for them: it must not count in vmax
+#pragma unroll
+      for (int t = 0; t < kPieces; ++t) {
+        if (bad_mask >> at & 1) x[t] = make_uint4(0, 0, 0, 0);
+        if (bad_mask >> (at + 8) & 1) y[t] = make_uint4(0, 0, 0, 0);
+      }
     }
 #pragma unroll
-    for (int u0 = 0; u0 < kGroup; u0 += 8) {
-      float v[8];
+    for (int t = 0; t < kPieces; ++t) {
+      const uint4 k = *reinterpret_cast<const uint4*>(&split[at][32 * (t0 + t) + 8 * c]);
+      float d[4];
+      mma16816(d, x[t].x, y[t].x, x[t].y, y[t].y, k.x, k.y);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t w[4] = {x[u0 + u].x, x[u0 + u].y, x[u0 + u].z, x[u0 + u].w};
-        uint64_t s = 0;  // two sums of four products
+      for (int i = 0; i < 4; ++i) acc[i] += d[i];
+      mma16816(d, x[t].z, y[t].z, x[t].w, y[t].w, k.z, k.w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s = ffma2(coef[i], f2pack(bf16lo(w[i]), bf16hi(w[i])), s);
-          vmax = max_abs2(vmax, w[i]);
-        }
-        const float2 both = f2unpack(s);
-        v[u] = both.x + both.y;
-      }
-      // Sums over the 32 lanes of all 8 at once: each step halves the blocks a lane holds.
-#pragma unroll
-      for (int o = 16, k = 4; o >= 4; o >>= 1, k >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i >= k) continue;
-          const float send = up ? v[i] : v[i + k];
-          const float keep = up ? v[i + k] : v[i];
-          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
-      }
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-      const int u = u0 + ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-      if ((lane & 3) == 0 && j0 + u < m) {
-        const uint32_t key = bad_mask >> u & 1 ? 0u : order_key(v[0]);
-        key32[j0 + u] = key;
-        if (many) far[j0 + u] = key;
-        kmin = min(kmin, key);
-        kmax = max(kmax, key);
-      }
+      for (int i = 0; i < 4; ++i) acc[i] += d[i];
+      vmax = max_abs2(max_abs2(max_abs2(vmax, x[t].x), x[t].y), max_abs2(x[t].z, x[t].w));
+      vmax = max_abs2(max_abs2(max_abs2(vmax, y[t].x), y[t].y), max_abs2(y[t].z, y[t].w));
+    }
+    // A row's three columns are in two lanes: both sum them, and one takes block `at`, one at + 8.
+    float v = c & 1 ? acc[0] : acc[0] + acc[1], v8 = c & 1 ? acc[2] : acc[2] + acc[3];
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    v8 += __shfl_xor_sync(0xffffffffu, v8, 1);
+    const int u = at + 8 * (c & 1);
+    const float score = c & 1 ? v8 : v;
+    if (!kWide) {
+      if (j0 + u < mine) (t0 ? cand : key32)[j0 + u] = bad_mask >> u & 1 ? kBad : __float_as_uint(score);
+    } else if (j0 + u < mine) {
+      const uint32_t key = bad_mask >> u & 1 ? 0u : order_key(score);
+      key32[r * chunk_cap + j0 + u] = key;
+      if (many) far[j0 + u] = key;
+      kmin = min(kmin, key);
+      kmax = max(kmax, key);
     }
   }
 
-  // ---- range of the keys and of the summaries, over the cluster
-  kmin = __reduce_min_sync(0xffffffffu, kmin);
-  kmax = __reduce_max_sync(0xffffffffu, kmax);
+  // ---- range of the keys and of the summaries
   uint32_t top = __reduce_max_sync(0xffffffffu, max(vmax & 0x7fffu, vmax >> 16 & 0x7fffu));
-  if (lane == 0) {
-    sh.lo[warp] = kmin;
-    sh.hi[warp] = kmax;
-    sh.amax[warp] = top;
+  if (lane == 0) sh.top[warp] = top;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const uint32_t lo = __reduce_min_sync(0xffffffffu, i == r ? kmin : 0xffffffffu);
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, i == r ? kmax : 0);
+    if (lane == 0) {
+      rows[i].lo[warp] = lo;
+      rows[i].hi[warp] = hi;
+    }
   }
   __syncthreads();
-  if (by_warp && warp) return;
-  top = __reduce_max_sync(0xffffffffu, sh.amax[lane & 7]);
-  if (!by_warp) {
-    if (threadIdx.x < cl.size) {  // thread r tells CTA r
-      uint32_t lo = 0xffffffffu, hi = 0;
-      for (int w = 0; w < kSelWarps; ++w) {
-        lo = min(lo, (uint32_t)sh.lo[w]);
-        hi = max(hi, (uint32_t)sh.hi[w]);
+  if (!kWide) {  // the two halves of the scores; a row has at most as many blocks as the CTA threads
+    static_assert(32 * kWarpKeys <= kSelThreads, "one step");
+    if (threadIdx.x < most) {
+      const uint32_t low = key32[threadIdx.x];
+      key32[threadIdx.x] =
+          low == kBad ? 0u : order_key(__uint_as_float(low) + __uint_as_float(cand[threadIdx.x]));
+    }
+    __syncthreads();
+  }
+  top = __reduce_max_sync(0xffffffffu, sh.top[lane & 7]);
+  if (!by_warp) {  // over the cluster
+    if (threadIdx.x < cl.size) {  // thread c tells CTA c
+      auto tell = [&](uint32_t* place, uint32_t x) {
+        *(cl.size > 1 ? cg::this_cluster().map_shared_rank(place, threadIdx.x) : place) = x;
+      };
+      tell(&sh.tops[cl.rank], top);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        uint32_t lo = 0xffffffffu, hi = 0;
+        for (int w = 0; w < kSelWarps; ++w) {
+          lo = min(lo, rows[r].lo[w]);
+          hi = max(hi, rows[r].hi[w]);
+        }
+        tell(&rows[r].los[cl.rank], lo);
+        tell(&rows[r].his[cl.rank], hi);
       }
-      uint32_t* to = sh.range[cl.rank];
-      if (cl.size > 1) to = cg::this_cluster().map_shared_rank(to, threadIdx.x);
-      to[0] = lo;
-      to[1] = hi;
-      to[2] = top;
     }
     cl.sync();
-    const int r = lane < cl.size ? lane : 0;
-    kmin = __reduce_min_sync(0xffffffffu, sh.range[r][0]);
-    kmax = __reduce_max_sync(0xffffffffu, sh.range[r][1]);
-    top = __reduce_max_sync(0xffffffffu, sh.range[r][2]);
+    top = __reduce_max_sync(0xffffffffu, sh.tops[lane < cl.size ? lane : 0]);
   }
-  float size = 0.f;
-  uint32_t any = 0;
+  auto bound = [&](const RowShared& x) {
+    row.coef = x.coef;
+    row.coef_low = x.coef_low;
+    float size = 0.f;
+    uint32_t any = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    size = add_ieee(size, sh.size[w]);
-    any |= sh.any_q[w];
-  }
-  const float reach = mul_ieee(size, __uint_as_float(top << 16));  // bounds |score|, partial sums
-  // A reach that is not finite bounds nothing. The added constant covers sums flushed to zero.
-  row.bounded = reach < 1e37f;
-  row.exact = row.bounded && (any == 0 || top == 0);
-  row.eps = row.exact ? 0.f : reach * (14.f * 0x1p-24f) + 1e-35f;
+    for (int w = 0; w < kSelWarps; ++w) {
+      size = add_ieee(size, x.size[w]);
+      any |= x.any_q[w];
+    }
+    const float reach = mul_ieee(size, __uint_as_float(top << 16));  // bounds |score|, partial sums
+    // A reach that is not finite bounds nothing.
+    row.bounded = reach < 1e37f;
+    row.exact = row.bounded && (any == 0 || top == 0);
+    // Numbers that the products may take for zero are below 2^-126.
+    row.eps = row.exact ? 0.f
+                        : reach * (56.f * 0x1p-24f) + size * 0x1p-125f +
+                              __uint_as_float(top << 16) * 0x1p-115f + 1e-35f;
+  };
+  auto count = [&](int r) { return kRows == 1 || r == 0 ? total[0] : total[kRows - 1]; };
   if constexpr (kWide) {
     if (!by_warp) {
-      // One CTA selects where few blocks are at the border: a barrier of the cluster with a read of
-      // another CTA's shared memory takes about a microsecond, and a selection by all CTAs six.
-      Border b;
-      if (cl.rank == 0) b = select_few(row, sh, hist, many ? gathered : key32, total, want, e0, kmin, kmax, out);
-      if (many) {
-        if (cl.rank == 0 && threadIdx.x < cl.size)
-          *cg::this_cluster().map_shared_rank(&sh.border, threadIdx.x) = b;
-        cl.sync();
-        b = sh.border;
+      // One CTA selects where few blocks are at the border, another for the other row: a barrier of
+      // the cluster with a read of another CTA's shared memory takes about a microsecond, and a
+      // selection by all CTAs six.
+#pragma unroll 1
+      for (int r = 0; r < kRows; ++r) {
+        if (count(r) == 0 || cl.rank != r % cl.size) continue;
+        bound(rows[r]);
+        const int c = lane < cl.size ? lane : 0;
+        const uint32_t lo = __reduce_min_sync(0xffffffffu, rows[r].los[c]);
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, rows[r].his[c]);
+        Row whole = row;
+        whole.table -= start;
+        const Border found = select_few(whole, sh, hist, many ? gathered : key32 + r * chunk_cap, count(r),
+                                        want, e0, lo, hi, out(r) + e0);
+        if (many && threadIdx.x < cl.size)
+          *cg::this_cluster().map_shared_rank(&rows[r].border, threadIdx.x) = found;
+        else if (!many && threadIdx.x == 0)
+          rows[r].border = found;
       }
-      if (!b.settled) select_many(row, sh, hist, cl, key32, key64, cand, m, first, b, out);
+      cl.sync();
+#pragma unroll 1
+      for (int r = 0; r < kRows; ++r) {
+        if (count(r) == 0 || rows[r].border.settled) continue;
+        bound(rows[r]);
+        select_many(row, sh, hist, cl, key32 + r * chunk_cap, key64, cand, max(0, min(m, count(r) - start)),
+                    e0 + start, rows[r].border, out(r) + e0);
+      }
       return;
     }
   }
-  select_by_warp(row, sh, key32, key64, cand, m, want, first, out);
+  // In a narrow kernel any one of the warps, so that those of an SM's CTAs are not all on one of
+  // its four schedulers (by the hash 13.5 us for a decode step, always the first warp 13.6).
+  const int turn = kWide ? warp : (warp + (int)(blockIdx.x * 2654435761u >> 29)) & (kSelWarps - 1);
+  if (turn >= kRows || count(turn) == 0) return;
+  bound(rows[turn]);
+  select_by_warp(row, key32 + turn * chunk_cap, key64 + turn * 32 * kWarpKeys, cand + turn * 32 * kWarpKeys,
+                 count(turn), want, e0, out(turn) + e0);
 }
 
-template <bool kWide>
+template <bool kWide, int kRows>
 static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cudaStream_t stream) {
-  const int alone = a.max_blocks < 32 * kWarpKeys ? a.max_blocks : 32 * kWarpKeys;
+  // Rows of one warp each have 256 places in a CTA, whatever the cluster.
+  const int alone = kRows == 1 && a.max_blocks < 32 * kWarpKeys ? a.max_blocks : kRows * 32 * kWarpKeys;
   int chunk_cap = ((a.max_blocks + C - 1) / C + 7) & ~7;
   if (chunk_cap < alone) chunk_cap = alone;
   // fp64 keys (or all fp32 keys of a cluster's row), fp32 keys, candidates
   const size_t shared = C > 1 && a.max_blocks > 2 * chunk_cap ? a.max_blocks : 2 * chunk_cap;
-  const size_t smem = (shared + 2 * chunk_cap) * 4;
-  if (smem > 16 * 1024) {  // with the static part more than a kernel gets unasked
-    const cudaError_t e = cudaFuncSetAttribute(select_blocks_kernel<kWide>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxChunk * 16);
+  const size_t smem = (shared + (kRows + 1) * chunk_cap) * 4;
+  if (smem > 8 * 1024) {  // with the static part it may be more than a kernel gets unasked
+    const cudaError_t e = cudaFuncSetAttribute(select_blocks_kernel<kWide, kRows>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               4 * (kMaxKeys + (kRows + 1) * kMaxChunk));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -1107,22 +1202,32 @@ static cudaError_t launch_select_n(const SelectArgs& a, int C, int64_t segs, cud
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_blocks_kernel<kWide>, a, chunk_cap);
+  return cudaLaunchKernelEx(&cfg, select_blocks_kernel<kWide, kRows>, a, chunk_cap);
 }
 
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int num_sms) {
-  const int64_t segs = (int64_t)a.B * a.q_len * a.Hkv;
-  if (segs == 0) return cudaSuccess;
+  const bool wide = a.max_blocks > 32 * kWarpKeys;
+  const int64_t single = (int64_t)a.B * a.q_len * a.Hkv;
+  if (single == 0) return cudaSuccess;
+  // Query rows of a sequence go by twos, which read the summaries once, where the rows alone are too
+  // many for the widest clusters. Measured with 8 kv heads (us, by twos and one by one): 2 rows of
+  // each of 8 sequences, 1,000 blocks 13.2 and 15.2, 4,000 26.6 and 35.4, 280 10.5 and 9.5; of 32
+  // sequences, 280 blocks 17.0 and 21.3, 1,000 29.3 and 39.5; 4 rows of one sequence, 4,000 blocks
+  // 14.4 and 14.8.
+  const bool pairs = wide && a.q_len > 1 && single * kMaxCluster > 2 * (int64_t)num_sms;
+  const int64_t segs = pairs ? (int64_t)a.B * ((a.q_len + 1) / 2) * a.Hkv : single;
   // Cluster width: as wide as a grid of one CTA per SM allows, or two where the rows are long, and
-  // enough that a CTA's keys stay within 64 KB. Measured on GB300 (us for 1, 2, 4, 8 CTAs a row): 8
-  // rows of 600 blocks 11.6, 10.2, 8.7, 7.7; 32 of 280 9.1, 9.2, 8.3, 8.7; 32 of 1,000 15.4, 11.8,
-  // 9.5, 9.4; 32 of 8,000 -, 67, 41, 32; 128 of 600 13.9, 14.5, 21, 33; 128 of 1,000 16.8, 15.9,
-  // 22, 34; 128 of 8,000 -, 90, 103, 119; 512 of 1,000 56, 71, 89, 137.
+  // enough that a CTA's keys leave room for two CTAs per SM. Measured on GB300 (us for 1, 2, 4, 8
+  // CTAs a row): 8 rows of 600 blocks 10.3, 9.7, 8.7, 7.9; 32 of 280 8.7, 8.8, 8.1, 8.5; 32 of 1,000
+  // 12.9, 11.6, 10.0, 9.7; 32 of 8,000 -, -, 32, 30; 64 of 2,000 19.9, 15.0, 14.5, 21; 128 of 600
+  // 12.7, 13.1, 20, 32; 128 of 2,000 28.8, 25.5, 32, 45; 128 of 8,000 -, -, 102, 118; 512 of 1,000
+  // 53, 68, 83, 132.
   int C = 1;
   const int64_t most = (a.max_blocks >= 800 ? 2 : 1) * (int64_t)num_sms;
   while (C < kMaxCluster && (a.max_blocks > kMaxChunk * C || segs * 2 * C <= most)) C *= 2;
-  if (a.max_blocks > 32 * kWarpKeys) return launch_select_n<true>(a, C, segs, stream);
-  return launch_select_n<false>(a, 1, segs, stream);
+  if (pairs) return launch_select_n<true, 2>(a, C, segs, stream);
+  if (wide) return launch_select_n<true, 1>(a, C, segs, stream);
+  return launch_select_n<false, 1>(a, 1, segs, stream);
 }
 
 }  // namespace pkv

@@ -313,6 +313,49 @@ def test_selection_at_borders_of_every_closeness(n, power):
         check_select(q, s, table, [n * BS], K, 0, 1)
 
 
+def check_rows(q, s, table, lens, K, sink=0, recent=1, bit=0):
+    """Every query row as it is selected by itself (with the sequence's length up to that row)."""
+    st, Q = status(), q.shape[1]
+    got = api.select_blocks(q, s, ints(table), ints(lens), K, sink, recent, dev_status=st)
+    assert int(st.item()) == bit
+    for i in range(Q):
+        alone = api.select_blocks(q[:, i].contiguous(), s, ints(table), ints(np.maximum(lens - Q + 1 + i, 0)),
+                                  K, sink, recent)
+        assert torch.equal(got[:, i], alone), i
+
+
+@pytest.mark.parametrize("q_len,H,Hkv,n,check", [
+    (2, 2, 1, 263, check_select), (3, 2, 1, 261, check_select), (2, 8, 8, 1300, check_rows),
+    (5, 4, 1, 2100, check_rows), (4, 32, 8, 5000, check_rows), (2, 16, 8, 8192, check_rows)])
+def test_selection_of_several_query_rows_over_long_tables(q_len, H, Hkv, n, check):
+    """Neighbouring query rows that see the same blocks, or one block more, up to the limits where
+    a row has nothing to choose and where one warp selects it; ties, bad blocks, infinities."""
+    rng = np.random.default_rng(n)
+    K = 9
+    lens = np.array([n * BS, (n - 1) * BS + 1, (n - 1) * BS, 258 * BS + 1, 257 * BS + 1, K * BS + 1, K * BS, 3, 0])
+    width = 5000 if n == 261 else n
+    nb = 4000
+    table = rng.integers(0, nb, (len(lens), width)).astype(np.int32)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    q = torch.randn((len(lens), q_len, H, D), generator=g, device="cuda").to(torch.bfloat16)
+    s = torch.randn((nb, Hkv, 2, D), generator=g, device="cuda").sort(dim=2).values.to(torch.bfloat16)
+    check(q, s, table, lens, K)
+    check(q, s, table, lens, 140, 2, 3)
+    for sink, recent in ((0, 0), (4, 5)):  # (the last leaves no place to choose)
+        check(q, s, table, lens, K, sink, recent)
+    q[:, q_len - 1] = 0  # all of one row's scores are equal
+    check(q, s, table, lens, K)
+    q[:, 1] = 1
+    whole = torch.randint(-1, 2, (nb, Hkv, 2, D), generator=g, device="cuda").sort(dim=2).values
+    whole[..., 2:] = 0
+    check(q, whole.to(torch.bfloat16), table, lens, 60, 1, 1)
+    s[7, 0, 1, 3], s[8, 0, 0, 9] = float("inf"), float("nan")
+    bad = table.copy()
+    bad[:, 1::9] = nb
+    with np.errstate(invalid="ignore"):
+        check(q, s, bad, lens, 40, bit=2)
+
+
 def test_blocks_past_four_gigabytes():
     """A cache whose last blocks lie beyond 2^32 bytes: summaries, selection, attention, the
     rotary write and the FP8 read give what a small cache of the same blocks gives."""
