@@ -248,8 +248,8 @@ struct Border {
 using Hist = int[4 + 8][kDigits];
 
 // Shared memory of one CTA. What other CTAs of the cluster read (counts, pub, the keys) is
-// written once per kernel and place, so one cluster barrier between the writes and the reads
-// is enough.
+// written once per row and place, so one cluster barrier between the writes and the reads is
+// enough; another ends a row.
 struct SelShared {
   unsigned long long pub[4][2];          // a pair of numbers per exchange
   unsigned long long lo[kSelWarps], hi[kSelWarps];
