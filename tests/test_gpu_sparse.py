@@ -356,6 +356,45 @@ def test_selection_of_several_query_rows_over_long_tables(q_len, H, Hkv, n, chec
         check(q, s, bad, lens, 40, bit=2)
 
 
+def test_selections_over_long_tables_at_once_and_in_a_graph():
+    """Clusters of different widths and shared memory on two streams at a time; replays follow the
+    lengths and queries in their buffers."""
+    rng = np.random.default_rng(12)
+    nb = 3000
+    g = torch.Generator(device="cuda").manual_seed(12)
+    s = torch.randn((nb, 2, 2, D), generator=g, device="cuda").sort(dim=2).values.to(torch.bfloat16)
+    cases = []
+    for B, n, K in ((1, 8192, 100), (120, 2100, 20), (3, 300, 7)):
+        q = torch.randn((B, 4, D), generator=g, device="cuda").to(torch.bfloat16)
+        t = ints(rng.integers(0, nb, (B, n)))
+        lens = ints(rng.integers(1, n * BS + 1, B))
+        out = torch.empty((B, 2, K), dtype=torch.int32, device="cuda")
+        cases.append((q, t, lens, K, out))
+
+    def check():
+        for q, t, lens, K, out in cases:
+            assert torch.equal(out, _torch_select(q, s, t, lens, K))
+            out.zero_()
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, (q, t, lens, K, out) in enumerate(cases):
+            api.select_blocks(q, s, t, lens, K, out=out, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for q, t, lens, K, out in cases:
+            api.select_blocks(q, s, t, lens, K, out=out)
+    for _ in range(2):
+        graph.replay()
+        check()
+        for q, t, lens, K, out in cases:
+            q.copy_(torch.randn(q.shape, generator=g, device="cuda"))
+            lens.copy_(ints(rng.integers(1, t.shape[1] * BS + 1, len(lens))))
+
+
 def test_blocks_past_four_gigabytes():
     """A cache whose last blocks lie beyond 2^32 bytes: summaries, selection, attention, the
     rotary write and the FP8 read give what a small cache of the same blocks gives."""
