@@ -186,8 +186,8 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, in
 //
 //   |score32 - score| <= eps = 56 2^-24 (sum_d P_d + |N_d|) max |summary|
 //
-// (the 16 sums of a product, each at least as good as a truncation to 24 bits: 32; the 16 products'
-// sum 16; the columns' 3; the coefficients 1; room for the bound's own), and finds the K-th largest
+// (the 16 sums of a product, each at least as good as a truncation to 24 bits: 32, of which 20,000
+// products of random numbers with exponents up to 40 apart reached 4; the 16 products' sum 16; the columns' 3; the coefficients 1; room for the bound's own), and finds the K-th largest
 // fp32 score tau to within a bin narrower
 // than eps, takes every block above the bin by more than 2 eps and none below it by more, and
 // scores the blocks between again where they are more than the places left: few of them in pairs
