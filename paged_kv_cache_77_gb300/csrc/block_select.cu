@@ -430,14 +430,17 @@ __device__ __forceinline__ int spare_bits(const Row& row, uint32_t kmin, uint32_
   return min(max(bits, 0), 31);
 }
 
-// [maybe, sure] from the bin [lo, hi] that holds the K-th largest key.
+// [maybe, sure] from the bin [lo, hi] that holds the K-th largest key. With lo = 0 (bad blocks at
+// the border, or no bound) every key is between them, whatever the scores: no block is in before
+// the choice, so all of the row's places are the choice's.
 __device__ __forceinline__ void border(const Row& row, uint32_t lo, uint32_t hi, uint32_t* maybe,
                                        uint32_t* sure) {
   *maybe = 0;
   *sure = kNanKey;
+  if (lo == 0) return;
   if (row.exact) {
     *maybe = *sure = lo;
-  } else if (row.bounded && lo != 0) {  // lo = 0: bad blocks are at the border
+  } else if (row.bounded) {
     const float a = key_score(lo), b = key_score(hi);
     // Rounded outward: a few units of 2^-24 of the operands.
     *maybe = order_key(a - (2.f * row.eps + (fabsf(a) + row.eps) * 0x1p-22f));

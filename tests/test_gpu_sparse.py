@@ -789,3 +789,40 @@ def test_entry_points_reject_bad_buffers_before_launch():
             api.update_block_summaries(**{**dict(summaries=s, k_cache=kc, block_table=t, seq_lens=n,
                                                  num_new=ints([1, 1]), max_new=1), **kw})
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("B,q_len,n,width", [
+    (2, 1, 300, 300), (90, 1, 300, 300), (1, 2, 600, 640), (160, 2, 600, 600), (1, 1, 2000, 2000),
+    (40, 3, 2000, 2000), (1, 1, 700, 8192), (3, 1, 200, 200), (3, 2, 255, 300)])
+def test_selection_with_fewer_good_blocks_than_places(B, q_len, n, width):
+    """Table entries outside the cache rank last whatever the scores: with fewer good blocks than
+    places every good one is in, then the lowest bad ones. With zero queries or zero summaries all
+    scores are equal, and the lowest good blocks come first however many there are. Memory around
+    the lists keeps its values."""
+    rng = np.random.default_rng(n + B)
+    K, sink, recent, nb = 40, 1, 2, 500
+    want = K - sink - recent
+    lens = np.full(B, n * BS)
+    q = torch.from_numpy(rng.standard_normal((B, q_len, 2, D))).to(torch.bfloat16).cuda()
+    s = random_summaries(rng, nb, 1)
+    places, pad = B * q_len * K, 64
+    buf = torch.empty(places + 2 * pad, dtype=torch.int32, device="cuda")
+    for good in (0, 1, want - 1, want, want + 9):
+        table = rng.integers(0, nb, (B, width)).astype(np.int32)
+        expect = np.empty((B, q_len, 1, K), dtype=np.int32)
+        for b in range(B):
+            rivals = np.arange(sink, n - recent)
+            keep = np.sort(rng.permutation(rivals)[:good])
+            lost = np.setdiff1d(rivals, keep)
+            table[b, lost] = rng.choice([-1, nb, -(1 << 31), (1 << 31) - 1], len(lost))
+            take = np.sort(np.concatenate([keep, lost])[:want])
+            expect[b] = np.concatenate([np.arange(sink), take, np.arange(n - recent, n)])
+        kinds = [(torch.zeros_like(q), s), (q, torch.zeros_like(s))] + [(q, s)] * (good < want)
+        for qk, sk in kinds:
+            buf.fill_(-77)
+            st = status()
+            out = buf[pad:pad + places].view(B, q_len, 1, K)
+            api.select_blocks(qk, sk, ints(table), ints(lens), K, sink, recent, out=out, dev_status=st)
+            assert int(st.item()) == 2
+            assert (buf[:pad] == -77).all() and (buf[pad + places:] == -77).all(), good
+            assert np.array_equal(out.cpu().numpy(), expect), good
