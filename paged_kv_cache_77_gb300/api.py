@@ -101,18 +101,39 @@ def _launch_stream(index, stream=None):
     return _raw_stream(current) if _raw_stream is not None else _stream()
 
 
+def _empty(shape, dtype, device, stream=None, returned=True):
+    """An uninitialised tensor for a launch on `stream` (None: the current one).
+
+    Its memory is the launch stream's: the allocator hands it out again only behind the work
+    of that stream, and no earlier work of another stream still uses it. A `returned` tensor
+    is the caller's, whose current stream counts as a user of it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
 def check_shape(t, shape, name) -> None:
     if t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {_shape_str(t.shape)}, expected {_shape_str(shape)}")
 
 
-def out_buffer(out, shape, out_dtype, device, name="out"):
-    """The output tensor: a new one when `out` is None, else `out` after checking that
-    it is a contiguous bf16 or fp32 tensor of exactly `shape` on `device`."""
+def out_buffer(out, shape, out_dtype, device, name="out", stream=None):
+    """The output tensor of a launch on `stream`: a new one when `out` is None, else `out`
+    after checking that it is a contiguous bf16 or fp32 tensor of exactly `shape` on
+    `device`."""
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
-        return torch.empty(tuple(shape), dtype=out_dtype, device=device)
+        return _empty(tuple(shape), out_dtype, device, stream)
     if not isinstance(out, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     if out.dtype not in (torch.float32, torch.bfloat16):
@@ -137,11 +158,12 @@ def lse_buffer(lse, shape, device, name="lse"):
     return lse
 
 
-def workspace_buffer(ws, need: int, device, name="workspace"):
-    """The scratch buffer and its size in bytes: a new uint8 tensor when `ws` is None,
-    else `ws` after checking that it is contiguous, on `device` and holds `need` bytes."""
+def workspace_buffer(ws, need: int, device, name="workspace", stream=None):
+    """The scratch buffer of a launch on `stream` and its size in bytes: a new uint8 tensor
+    when `ws` is None, else `ws` after checking that it is contiguous, on `device` and holds
+    `need` bytes."""
     if ws is None:
-        ws = torch.empty(max(int(need), 256), dtype=torch.uint8, device=device)
+        ws = _empty(max(int(need), 256), torch.uint8, device, stream, returned=False)
     if not isinstance(ws, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
     _on_device(ws, device, name)
@@ -573,7 +595,7 @@ def _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions, slot_mapping,
     if shape != ((T,) if len(shape) == 1 else (axes, T)):
         raise ValueError(f"positions must be [T={T}] or [axes, T={T}], got {_shape_str(shape)}")
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        q_out = _empty((T, H, d), torch.bfloat16, q.device, stream)
         qos = H * d
     else:
         heads, qos = _rope_rows(q_out, T, d, "q_out")
@@ -648,9 +670,9 @@ def kv_cache_read_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=No
     check_shape(v_scale, (nb, hkv, bs), "v_scale")
     T = slot_mapping.numel()
     if k_out is None:
-        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+        k_out = _empty((T, hkv, d), torch.bfloat16, k_cache.device, stream)
     if v_out is None:
-        v_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+        v_out = _empty((T, hkv, d), torch.bfloat16, k_cache.device, stream)
     for t, n in ((k_out, "k_out"), (v_out, "v_out")):
         _dev_bf16(t, n)
         check_shape(t, (T, hkv, d), n)
@@ -689,11 +711,12 @@ def paged_attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     check_same_device(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
                       block_table=block_table, seq_lens=seq_lens)
     check_current_device(dev)
-    out = out_buffer(out, (B, H, d), out_dtype, dev)
+    out = out_buffer(out, (B, H, d), out_dtype, dev, stream=stream)
     lse_buffer(lse, (B, H), dev)
     status_buffer(dev_status, dev)
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
-    workspace, ws_bytes = workspace_buffer(workspace, decode_workspace_size(B, H, hkv, d), dev)
+    workspace, ws_bytes = workspace_buffer(workspace, decode_workspace_size(B, H, hkv, d), dev,
+                                           stream=stream)
     check(load().pkv_paged_attention_decode_fp8(
         _ptr(out), code, _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
         _ptr(v_scale), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B, H, hkv, d, bs, nb,
@@ -740,11 +763,12 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, seq_lens, scale: fl
     """Decode attention over the paged cache; returns out [B, H, d] (and fills lse [B, H])."""
     (B, H, d), (nb, bs, hkv) = _decode_inputs(q, k_cache, v_cache, block_table, seq_lens, 3)
     dev = q.device
-    out = out_buffer(out, (B, H, d), out_dtype, dev)
+    out = out_buffer(out, (B, H, d), out_dtype, dev, stream=stream)
     lse_buffer(lse, (B, H), dev)
     status_buffer(dev_status, dev)
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
-    workspace, ws_bytes = workspace_buffer(workspace, decode_workspace_size(B, H, hkv, d), dev)
+    workspace, ws_bytes = workspace_buffer(workspace, decode_workspace_size(B, H, hkv, d), dev,
+                                           stream=stream)
     check(load().pkv_paged_attention_decode(
         _ptr(out), code, _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), B, H, hkv, d, bs, nb, float(scale), int(window),
@@ -765,12 +789,12 @@ def paged_attention_decode_spec(q, k_cache, v_cache, block_table, seq_lens, scal
     lse [B, q_len, H])."""
     (B, Q, H, d), (nb, bs, hkv) = _decode_inputs(q, k_cache, v_cache, block_table, seq_lens, 4)
     dev = q.device
-    out = out_buffer(out, (B, Q, H, d), out_dtype, dev)
+    out = out_buffer(out, (B, Q, H, d), out_dtype, dev, stream=stream)
     lse_buffer(lse, (B, Q, H), dev)
     status_buffer(dev_status, dev)
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
     workspace, ws_bytes = workspace_buffer(workspace, decode_spec_workspace_size(B, Q, H, hkv, d),
-                                           dev)
+                                           dev, stream=stream)
     check(load().pkv_paged_attention_decode_spec(
         _ptr(out), code, _ptr(lse), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
         block_table.shape[1], _ptr(seq_lens), B, Q, H, hkv, d, bs, nb, float(scale), int(window),
@@ -835,7 +859,7 @@ def select_blocks(q, summaries, block_table, seq_lens, num_selected: int, num_si
         raise ValueError("num_selected must be positive")
     shape = (B, hkv, num_selected) if q.dim() == 3 else (B, Q, hkv, num_selected)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+        out = _empty(shape, torch.int32, q.device, stream)
     else:
         _dev_i32(out, "out")
         check_shape(out, shape, "out")
@@ -883,14 +907,15 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_table, seq_lens, bl
                block_indices=block_indices)
     raw = _launch_stream(index, stream)
     dev = q.device
-    out = out_buffer(out, q.shape, out_dtype, dev)
+    out = out_buffer(out, q.shape, out_dtype, dev, stream=stream)
     lse_buffer(lse, lead + (H,), dev)
     status_buffer(dev_status, dev)
     if Q == 0:
         return out
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
     workspace, ws_bytes = workspace_buffer(workspace,
-                                           decode_sparse_workspace_size(B, Q, H, hkv, d), dev)
+                                           decode_sparse_workspace_size(B, Q, H, hkv, d), dev,
+                                           stream=stream)
     check(load().pkv_paged_attention_decode_sparse(
         out.data_ptr(), code, _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), block_indices.data_ptr(),
@@ -924,11 +949,11 @@ def paged_attention_prefill(q, cu_seqlens_q, k_cache, v_cache, block_table, seq_
     check_same_device(dev, cu_seqlens_q=cu_seqlens_q, k_cache=k_cache, v_cache=v_cache,
                       block_table=block_table, seq_lens_kv=seq_lens_kv)
     check_current_device(dev)
-    out = out_buffer(out, (T, H, d), out_dtype, dev)
+    out = out_buffer(out, (T, H, d), out_dtype, dev, stream=stream)
     lse_buffer(lse, (T, H), dev)
     status_buffer(dev_status, dev)
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
-    workspace, ws_bytes = workspace_buffer(workspace, prefill_workspace_size(), dev)
+    workspace, ws_bytes = workspace_buffer(workspace, prefill_workspace_size(), dev, stream=stream)
     check(load().pkv_paged_attention_prefill(
         _ptr(out), code, _ptr(lse), _ptr(q), _ptr(cu_seqlens_q), T, _ptr(k_cache), _ptr(v_cache),
         _ptr(block_table), block_table.shape[1], _ptr(seq_lens_kv), B, H, hkv, d, bs, nb,
@@ -969,11 +994,12 @@ def mla_paged_decode(q_nope, q_rope, cache_nope, cache_rope, block_table, seq_le
     (B, H), dc, dr, nb, bs = _mla_inputs(q_nope, q_rope, cache_nope, cache_rope, block_table,
                                          seq_lens, 3)
     dev = q_nope.device
-    out = out_buffer(out, (B, H, dc), out_dtype, dev)
+    out = out_buffer(out, (B, H, dc), out_dtype, dev, stream=stream)
     lse_buffer(lse, (B, H), dev)
     status_buffer(dev_status, dev)
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
-    workspace, ws_bytes = workspace_buffer(workspace, mla_decode_workspace_size(B, H), dev)
+    workspace, ws_bytes = workspace_buffer(workspace, mla_decode_workspace_size(B, H), dev,
+                                           stream=stream)
     check(load().pkv_mla_paged_decode(
         _ptr(out), code, _ptr(lse), _ptr(q_nope), _ptr(q_rope), _ptr(cache_nope), _ptr(cache_rope),
         _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B, H, dc, dr, bs, nb, float(scale),
@@ -995,11 +1021,12 @@ def mla_paged_decode_spec(q_nope, q_rope, cache_nope, cache_rope, block_table, s
     (B, Q, H), dc, dr, nb, bs = _mla_inputs(q_nope, q_rope, cache_nope, cache_rope, block_table,
                                             seq_lens, 4)
     dev = q_nope.device
-    out = out_buffer(out, (B, Q, H, dc), out_dtype, dev)
+    out = out_buffer(out, (B, Q, H, dc), out_dtype, dev, stream=stream)
     lse_buffer(lse, (B, Q, H), dev)
     status_buffer(dev_status, dev)
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
-    workspace, ws_bytes = workspace_buffer(workspace, mla_decode_spec_workspace_size(B, Q, H), dev)
+    workspace, ws_bytes = workspace_buffer(workspace, mla_decode_spec_workspace_size(B, Q, H), dev,
+                                           stream=stream)
     check(load().pkv_mla_paged_decode_spec(
         _ptr(out), code, _ptr(lse), _ptr(q_nope), _ptr(q_rope), _ptr(cache_nope), _ptr(cache_rope),
         _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B, Q, H, dc, dr, bs, nb,
@@ -1022,7 +1049,7 @@ def paged_attention_decode_static(q, k_cache, v_cache, block_table, seq_lens, sc
     of the array the call uses, and `stream` must belong to that device."""
     (B, H, d), (nb, bs, hkv) = _decode_inputs(q, k_cache, v_cache, block_table, seq_lens, 3)
     dev = q.device
-    out = out_buffer(out, (B, H, d), out_dtype, dev)
+    out = out_buffer(out, (B, H, d), out_dtype, dev, stream=stream)
     lse_buffer(lse, (B, H), dev)
     status_buffer(dev_status, dev)
     code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
