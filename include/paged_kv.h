@@ -519,7 +519,8 @@ int pkv_mla_paged_decode_spec(void* out, int32_t out_dtype, float* lse, const vo
  * Format: one fp32 scale per (token, kv head) row of head_dim values,
  * scale = amax / 448 (IEEE fp32 division), code = E4M3(x / scale) rounded to nearest
  * even with saturation to +-448 (the "fn" variant: no infinities, S.1111.111 =
- * NaN); an all-zero row has scale 0 and zero codes. value = code * scale.
+ * NaN); an all-zero row has scale 0 and zero codes. value = code * scale. A row with an
+ * infinite value has an infinite scale, and every value of it reads back as NaN.
  *   k_cache, v_cache [num_blocks, block_size, H_kv, head_dim] uint8 codes
  *   k_scale, v_scale [num_blocks, H_kv, block_size] fp32 (a block's scales of one
  *                    kv head are contiguous)
@@ -527,13 +528,16 @@ int pkv_mla_paged_decode_spec(void* out, int32_t out_dtype, float* lse, const vo
 
 /* Quantise new rows k, v [num_tokens, H_kv, head_dim] bf16 and write codes and
  * scales through slot_mapping (negative slot: skipped; slot >= num_blocks *
- * block_size: skipped and PKV_DEV_BAD_SLOT). Caches 16-byte aligned, scales 4. */
+ * block_size: skipped and PKV_DEV_BAD_SLOT). Caches 16-byte aligned, scales 4. NaN values
+ * do not count in amax: they keep NaN codes under the scale of the row's other values, and
+ * a row of nothing but NaN and zeros is written as zeros. */
 int pkv_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                            const void* k, const void* v, const int32_t* slot_mapping,
                            int64_t num_tokens, int64_t num_blocks, int32_t block_size,
                            int32_t num_kv_heads, int32_t head_dim, int* dev_status, void* stream);
 /* pkv_rope_kv_cache_write into an FP8 cache: the rotated k row (fp32, not rounded to
- * bf16 first) and the v row are quantised as above. head_dim must be 128
+ * bf16 first) and the v row are quantised as above, but for NaN: a row with a NaN has the
+ * scale NaN and NaN codes, so that all of it reads back as NaN. head_dim must be 128
  * (PKV_ERR_UNSUPPORTED); scales 4-byte aligned. */
 int pkv_rope_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                                 void* q_out, int64_t q_out_stride, const void* q,

@@ -226,16 +226,6 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   const unsigned long long u = x == 0.0 ? 0ull : (unsigned long long)__double_as_longlong(x);
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // What decides a row: keys above `sure` are in, keys below `maybe` are out, and of those between
 // the `need` best by more exact scores.

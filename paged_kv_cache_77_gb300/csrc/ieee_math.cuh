@@ -41,15 +41,15 @@ __device__ __forceinline__ float abs_ieee(float a) {
   asm("abs.f32 %0, %1;\n" : "=f"(r) : "f"(a));
   return r;
 }
-// Maximum and minimum; a NaN gives way to the other operand.
-__device__ __forceinline__ float max_ieee(float a, float b) {
+// Maximum and minimum; NaN if either operand is.
+__device__ __forceinline__ float max_nan(float a, float b) {
   float r;
-  asm("max.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float min_ieee(float a, float b) {
+__device__ __forceinline__ float min_nan(float a, float b) {
   float r;
-  asm("min.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ double widen_ieee(float a) {

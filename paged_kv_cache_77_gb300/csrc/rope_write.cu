@@ -209,12 +209,13 @@ __global__ void __launch_bounds__(256, kCtasPerSm) rope_write_kernel(const __gri
       unpack8(w0[0], f);
       unpack8(w1[0], f + 8);
       if (rot && !is_v) rotate<INTERLEAVED>(f, cs, sn);
-      // Largest magnitude of the row, over its 8 lanes (head_dim is 128).
+      // Largest magnitude of the row, over its 8 lanes (head_dim is 128); NaN if any value is,
+      // so that the row's scale and codes are.
       float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = max_ieee(amax, abs_ieee(f[i]));
+      for (int i = 0; i < 16; ++i) amax = max_nan(amax, abs_ieee(f[i]));
 #pragma unroll
-      for (int o = 4; o; o >>= 1) amax = max_ieee(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int o = 4; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (left <= 0 || !store) continue;
       const float scale = div_ieee(amax, 448.f);
       uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + ((int64_t)slot * a.Hkv + head0) * 128;

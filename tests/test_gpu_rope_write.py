@@ -193,6 +193,42 @@ def test_rope_write_fp8_codes_at_every_tie():
     assert np.array_equal(vc.cpu().numpy().reshape(-1, 9, 128)[slots], codes)
 
 
+def test_rope_write_fp8_rows_with_nan_and_infinities():
+    """A row's scale is its largest magnitude over 448: NaN if a value is NaN, whatever the others
+    are, infinite if one is infinite; either way no value of the row can be told, and all of them
+    read back as NaN. Other rows of the token, and other tokens, do not change."""
+    nan, inf = float("nan"), float("inf")
+    c = Case(9, 4, 3, 128, 64, seed=21)
+    clean = [t.clone() for t in (c.k, c.v)]
+    for t in (c.k, c.v):
+        t[0, 0] = nan                       # nothing but NaN
+        t[1, 1] = 0
+        t[1, 1, 100] = nan                  # NaN and zeros
+        t[2, 2, 5] = nan                    # some NaN, in the rotated part
+        t[3, 0, 127] = nan                  # and behind it
+        t[4, 1, 70], t[4, 1, 71] = inf, 2.0
+        t[5, 2, 90], t[5, 2, 64] = -inf, nan
+    lost = torch.zeros((9, 3), dtype=torch.bool, device="cuda")
+    lost[range(6), [0, 1, 2, 0, 1, 2]] = True
+    got = []
+    for k, v in ((c.k, c.v), clean):
+        caches = [torch.full((c.nb, BS, 3, 128), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.full((c.nb, 3, BS), 7.0, device="cuda") for _ in range(2)]
+        api.rope_kv_cache_write_fp8(*caches, *scales, c.q, k, v, c.table, c.pos, c.slots, **c.kwargs())
+        read = api.kv_cache_read_fp8(*caches, *scales, c.slots)
+        slots = c.slots.long()
+        got.append([(codes.view(-1, 3, 128)[slots], s.transpose(1, 2).reshape(-1, 3)[slots], r)
+                    for codes, s, r in zip(caches, scales, read)])
+    assert int(c.status.item()) == 0
+    for special, plain in zip(*got):
+        codes, scale, rows = special
+        assert torch.isnan(rows[lost]).all() and torch.isnan(scale[:4][lost[:4]]).all()
+        assert torch.isinf(scale[4, 1]) and torch.isnan(scale[5, 2])
+        assert ((codes[:4][lost[:4]] & 0x7F) == 0x7F).all()
+        for a, b in zip(special, plain):
+            assert torch.equal(a[~lost], b[~lost]) and torch.isfinite(b.float()).all()
+
+
 def test_rope_write_in_place_on_a_projection_buffer():
     c = Case(200, 8, 2, 128, 128, seed=3, strided=True)
     kc, vc = (torch.zeros((c.nb, BS, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
