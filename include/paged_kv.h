@@ -386,6 +386,7 @@ int pkv_paged_attention_decode_spec(void* out, int32_t out_dtype, float* lse, co
  * or seq_lens[b] > max_blocks_per_seq * block_size, skips the sequence and sets
  * PKV_DEV_BAD_LENGTH; a table entry outside [0, num_blocks) skips the block
  * (PKV_DEV_BAD_BLOCK). A block that two sequences of one call both update must not be.
+ * summaries may not overlap anything the call reads (PKV_ERR_INVALID_ARG).
  * Supported: head_dim 128, block_size 128 (PKV_ERR_UNSUPPORTED otherwise). */
 int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32_t* block_table,
                                int32_t max_blocks_per_seq, const int32_t* seq_lens,
@@ -410,6 +411,7 @@ int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32
  * PKV_DEV_BAD_BLOCK; a length past the table is clamped (PKV_DEV_BAD_LENGTH). Every block
  * that a row sees competes: a table whose expired entries hold the null block (a sliding
  * window's) does not go with it.
+ * block_indices may not overlap anything the call reads (PKV_ERR_INVALID_ARG).
  * Supported: head_dim 128, block_size 128, H % H_kv == 0, H / H_kv <= 16,
  * num_sink + num_recent <= num_selected, max_blocks_per_seq <= 8192 (1,048,576 tokens).
  * No workspace. */
@@ -553,7 +555,8 @@ int pkv_rope_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, fl
  * prefix reaches pkv_paged_attention_prefill, which reads bf16 caches. A negative slot
  * gives a row of zeros, a slot >= num_blocks * block_size too and sets
  * PKV_DEV_BAD_SLOT. k, v [num_tokens, H_kv, head_dim] bf16; head_dim must be 128
- * (PKV_ERR_UNSUPPORTED). Rows and caches 16-byte aligned, scales 4. */
+ * (PKV_ERR_UNSUPPORTED). Rows and caches 16-byte aligned, scales 4. k and v may overlap
+ * neither each other nor anything the call reads (PKV_ERR_INVALID_ARG). */
 int pkv_kv_cache_read_fp8(void* k, void* v, const void* k_cache, const void* v_cache,
                           const float* k_scale, const float* v_scale, const int32_t* slot_mapping,
                           int64_t num_tokens, int64_t num_blocks, int32_t block_size,

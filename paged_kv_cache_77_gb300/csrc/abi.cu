@@ -271,6 +271,12 @@ int pkv_kv_cache_write_fp8(void* k_cache, void* v_cache, float* k_scale, float* 
 
 namespace {
 
+// Whether [a, a + a_bytes) and [b, b + b_bytes) share a byte.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+  return a_bytes > 0 && b_bytes > 0 && pa < pb + (uint64_t)b_bytes && pb < pa + (uint64_t)a_bytes;
+}
+
 // Whether rows of `width` elements at a + t * a_stride and b + t * b_stride (t < tokens, 2-byte
 // elements) can share an element. Rows that run through one buffer at a common stride, as
 // slices of a projection's output do, are apart when their columns are.
@@ -427,6 +433,16 @@ int pkv_kv_cache_read_fp8(void* k, void* v, const void* k_cache, const void* v_c
   PKV_REQUIRE(aligned16(k_cache) && aligned16(v_cache) && aligned16(k) && aligned16(v) &&
                   (((uintptr_t)k_scale) & 3) == 0 && (((uintptr_t)v_scale) & 3) == 0,
               PKV_ERR_INVALID_ARG, "pkv_kv_cache_read_fp8: misaligned pointer");
+  const int64_t rows = num_tokens * num_kv_heads, cached = num_blocks * block_size * num_kv_heads;
+  auto reads = [&](const void* out) {  // whether an output lies in what the call reads
+    return overlap(out, rows * 256, k_cache, cached * 128) ||
+           overlap(out, rows * 256, v_cache, cached * 128) ||
+           overlap(out, rows * 256, k_scale, cached * 4) ||
+           overlap(out, rows * 256, v_scale, cached * 4) ||
+           overlap(out, rows * 256, slot_mapping, num_tokens * 4);
+  };
+  PKV_REQUIRE(!overlap(k, rows * 256, v, rows * 256) && !reads(k) && !reads(v), PKV_ERR_INVALID_ARG,
+              "pkv_kv_cache_read_fp8: k or v overlaps the other or an input");
   clear_error();
   return launch_status(launch_kv_read_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping,
                                           num_tokens, num_blocks, block_size, num_kv_heads,
@@ -518,6 +534,13 @@ int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32
   if (a.span > max_blocks_per_seq) a.span = max_blocks_per_seq;
   PKV_REQUIRE((int64_t)B * a.span <= INT32_MAX / H_kv, PKV_ERR_UNSUPPORTED,
               "%s: B * blocks of max_new * H_kv must fit in int32", what);
+  const int64_t summary_bytes = num_blocks * H_kv * (4 * (int64_t)head_dim);
+  PKV_REQUIRE(!overlap(summaries, summary_bytes, k_cache,
+                       num_blocks * block_size * H_kv * (2 * (int64_t)head_dim)) &&
+                  !overlap(summaries, summary_bytes, block_table, (int64_t)B * max_blocks_per_seq * 4) &&
+                  !overlap(summaries, summary_bytes, seq_lens, (int64_t)B * 4) &&
+                  !overlap(summaries, summary_bytes, num_new, (int64_t)B * 4),
+              PKV_ERR_INVALID_ARG, "%s: summaries overlaps an input", what);
   a.summaries = (uint8_t*)summaries;
   a.k_cache = (const uint8_t*)k_cache;
   a.block_table = block_table;
@@ -560,6 +583,12 @@ int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summari
               "%s: null pointer", what);
   PKV_REQUIRE(aligned16(q) && aligned16(summaries), PKV_ERR_INVALID_ARG,
               "%s: pointers must be 16-byte aligned", what);
+  const int64_t rows = (int64_t)B * q_len, out_bytes = rows * H_kv * num_selected * 4;
+  PKV_REQUIRE(!overlap(block_indices, out_bytes, q, rows * H * head_dim * 2) &&
+                  !overlap(block_indices, out_bytes, summaries, num_blocks * H_kv * (4 * (int64_t)head_dim)) &&
+                  !overlap(block_indices, out_bytes, block_table, (int64_t)B * max_blocks_per_seq * 4) &&
+                  !overlap(block_indices, out_bytes, seq_lens, (int64_t)B * 4),
+              PKV_ERR_INVALID_ARG, "%s: block_indices overlaps an input", what);
   SelectArgs a = {};
   a.q = (const uint16_t*)q;
   a.summaries = (const uint8_t*)summaries;

@@ -94,6 +94,22 @@ def test_read_fp8_refusals():
     assert call(k=P + 8) == -1 and call(vs=P + 2) == -1 and b"aligned" in lib.pkv_last_error()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(v=P),                                # k and v the same rows
+    dict(v=P + 2032), dict(k=21 * P - 2032),  # or sharing 16 bytes
+    dict(k=30 * P + 16), dict(k=40 * P + 16), dict(v=50 * P + 16), dict(v=60 * P + 16), dict(v=70 * P),
+    dict(k=30 * P - 2048 + 16), dict(k=30 * P + 2 * 128 * 2 * 128 - 16),
+    dict(k=70 * P - 2048 + 16), dict(v=60 * P + 2 * 128 * 2 * 4 - 16),
+])
+def test_read_fp8_refuses_outputs_that_overlap(kw):
+    """4 rows of 2 heads are 2,048 bytes; 2 blocks are 65,536 bytes of codes and 2,048 of scales."""
+    lib = load()
+    a = dict(k=P, v=21 * P, kc=30 * P, vc=40 * P, ks=50 * P, vs=60 * P, slots=70 * P)
+    a.update(kw)
+    assert lib.pkv_kv_cache_read_fp8(*a.values(), 4, 2, 128, 2, 128, None, None) == -1
+    assert b"overlaps" in lib.pkv_last_error()
+
+
 def test_the_binding_refuses_host_tensors():
     import torch
 

@@ -52,6 +52,22 @@ def test_sparse_decode_refusals(kw, code):
     assert _call("pkv_paged_attention_decode_sparse", SPARSE, kw) == code
 
 
+@pytest.mark.parametrize("fn,defaults,out,size,inputs", [
+    # 9 blocks of 2 heads: summaries of 512 bytes each, keys of 32,768.
+    ("pkv_update_block_summaries", SUMMARIES, "summaries", 9216,
+     dict(k_cache=9 * 2 * 32768, table=32, lens=8, num_new=8)),
+    # 2 rows, 8 query heads, 4 of 4 blocks for 2 kv heads.
+    ("pkv_select_blocks", SELECT, "out", 64, dict(q=4096, summaries=9216, table=32, lens=8)),
+])
+def test_outputs_that_overlap_what_the_call_reads_are_refused(fn, defaults, out, size, inputs):
+    lib = load()
+    apart = {name: (i + 2) * P for i, name in enumerate(inputs)}
+    for name, nbytes in inputs.items():
+        for at in (apart[name], apart[name] - size + 16, apart[name] + max(nbytes - 16, 0)):
+            assert _call(fn, defaults, {**apart, out: at}) == -1
+            assert b"overlaps" in lib.pkv_last_error(), (name, at)
+
+
 def test_workspace_is_that_of_a_batch_of_rows():
     lib = load()
     for B, Q in ((4, 1), (4, 3), (0, 2)):
