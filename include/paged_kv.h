@@ -428,7 +428,8 @@ int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summari
  * block_indices[b][i][g] (in any order). A negative entry is an empty place. Only the first
  * min(num_selected, n) entries are read, n being the number of blocks that the row sees;
  * an entry of n or more is skipped and sets PKV_DEV_BAD_BLOCK. A block listed twice counts
- * twice. A row without a single position to attend to returns o = 0, lse = -inf.
+ * twice. A row without a single position to attend to returns o = 0, lse = -inf; a head
+ * with a NaN score (a NaN in its query or in a key that it attends to) o = lse = NaN.
  *   out, q, lse, caches, block_table, seq_lens as for pkv_paged_attention_decode_spec
  *   block_indices [B, q_len, H_kv, num_selected] int32 (device)
  * Supported: head_dim 128, block_size 128, H / H_kv in {1, 2, 4, 8, 16}.

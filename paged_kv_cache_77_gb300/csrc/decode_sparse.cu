@@ -82,10 +82,10 @@ __global__ void __launch_bounds__(512) sparse_merge_kernel(const __grid_constant
       sum += w;
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;  // (a NaN piece makes the row NaN)
   put((int64_t)c.b * a.H + (int64_t)c.g * a.n_rep + h,
       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv),
-      sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY);
+      sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY);
 }
 
 static cudaError_t launch_attention(const DecodeArgs& a, cudaStream_t stream) {

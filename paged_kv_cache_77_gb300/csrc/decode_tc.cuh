@@ -452,8 +452,10 @@ __global__ void __launch_bounds__(tcd::Shape<NREP, QL>::NTHREADS, 1)
         const int h = qbase + i;  // column: query token h / NREP, head h % NREP
         if (NCH > 1 && h >= NR) continue;
         const float l = l_part[i], le = le_part[i];
-        const float ov = l > 0.f ? o_reg[i] / l : 0.f;
-        const float lse2 = le > 0.f ? m_run[i] + log2f(le) : -INFINITY;
+        // Sums of zero: a column without a token. Of a NaN score the dense forms make one
+        // too; a sparse row is NaN then.
+        const float ov = (SPARSE ? l != 0.f : l > 0.f) ? o_reg[i] / l : 0.f;
+        const float lse2 = (SPARSE ? le != 0.f : le > 0.f) ? m_run[i] + log2f(le) : -INFINITY;
         if (p_whole) {
           const int64_t row = ((int64_t)pb * QL + h / NREP) * a.H + (int64_t)pg * NREP + h % NREP;
           if (a.out_f32)

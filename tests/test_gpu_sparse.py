@@ -596,6 +596,45 @@ def test_sparse_decode_flags_bad_entries_and_skips_them():
     assert int(st.item()) & 4
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_sparse_decode_of_nan_scores_is_nan(out_dtype):
+    """A NaN in a query, or in a key that is attended to, makes the heads that score it NaN, in rows
+    that one CTA holds and in rows that the split cuts into many pieces; other heads and rows keep
+    every bit."""
+    rng = np.random.default_rng(25)
+    lens = np.array([300, 200 * BS - 7, 90])
+    table, nb = make_table(rng, lens)
+    kc, vc = caches(nb, 2)
+    idx = random_lists(rng, lens, 2, 2, 190)
+    q = torch.from_numpy(rng.standard_normal((3, 2, 8, D))).to(torch.bfloat16).cuda()
+
+    def run():
+        st, lse = status(), torch.empty((3, 2, 8), device="cuda")
+        out = api.paged_attention_decode_sparse(q, kc, vc, ints(table), ints(lens), ints(idx), D ** -0.5,
+                                                lse=lse, out_dtype=out_dtype, dev_status=st)
+        assert int(st.item()) == 0
+        return out, lse
+
+    out, lse = run()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    lost = torch.zeros((3, 2, 8), dtype=torch.bool, device="cuda")
+    q[2, 1, 6, 17] = float("nan")
+    lost[2, 1, 6] = True
+    q[1, 0, 1, 0] = float("nan")
+    lost[1, 0, 1] = True
+    kc[int(table[0, 1]), 5, 0, 100] = float("nan")  # both rows of sequence 0, the heads of kv head 0
+    lost[0, :, :4] = True
+    block = int(idx[1, 1, 1, 77])                   # a block in the middle of a cut list
+    kc[int(table[1, block]), 64, 1, 3] = float("nan")
+    for i in range(2):
+        if block in idx[1, i, 1]:
+            lost[1, i, 4:] = True
+    kc[int(table[2, 0]), 90:, :] = float("nan")     # behind the sequence: nothing attends to it
+    out_nan, lse_nan = run()
+    assert torch.isnan(out_nan[lost]).all() and torch.isnan(lse_nan[lost]).all()
+    assert torch.equal(out_nan[~lost], out[~lost]) and torch.equal(lse_nan[~lost], lse[~lost])
+
+
 def test_sparse_decode_over_every_block_is_the_dense_decode():
     """With room for every block the lists are whole, the tiles and their split are those of
     the dense kernel, and so is every bit of the result."""
