@@ -591,8 +591,8 @@ def _rope_inputs(k_cache, v_cache, q, k, v, rope_table, positions, slot_mapping,
     max_pos, rope_dim = rope_table.shape
     _dev_i32(positions, "positions")
     shape = positions.shape
-    axes = 1 if len(shape) == 1 else shape[0]
-    if shape != ((T,) if len(shape) == 1 else (axes, T)):
+    axes = shape[0] if len(shape) == 2 else 1
+    if shape != ((axes, T) if len(shape) == 2 else (T,)):
         raise ValueError(f"positions must be [T={T}] or [axes, T={T}], got {_shape_str(shape)}")
     if q_out is None:
         q_out = _empty((T, H, d), torch.bfloat16, q.device, stream)

@@ -416,3 +416,14 @@ def test_entry_points_reject_bad_buffers_before_launch():
     with pytest.raises(ValueError):
         api.kv_cache_read_fp8(codes, codes, sc, sc, c.slots, k_out=torch.empty((6, 2, 128), device="cuda"))
     torch.cuda.synchronize()
+
+
+def test_positions_need_a_token_axis():
+    c = Case(1, 4, 2, 128, 128, seed=15)
+    kc, vc = (torch.zeros((c.nb, BS, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for pos in (c.pos[0, 0], c.pos[None]):
+        with pytest.raises(ValueError, match="positions"):
+            api.rope_kv_cache_write(kc, vc, c.q, c.k, c.v, c.table, pos, c.slots)
+    for pos in (c.pos, c.pos[0]):
+        api.rope_kv_cache_write(kc, vc, c.q, c.k, c.v, c.table, pos, c.slots)
+    torch.cuda.synchronize()
