@@ -52,6 +52,14 @@ def _dev_i32(t, name):
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
 
 
+def _int32(x, name) -> int:
+    """`x` as the library's int32 argument; ctypes would drop the bits above it."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name} = {x} does not fit in int32")
+    return x
+
+
 # ---- caller-provided buffers ------------------------------------------------
 # The C ABI receives bare pointers and cannot see a tensor's size, so a wrong-shaped
 # output would be written out of bounds on the GPU. Every buffer the caller passes
@@ -826,8 +834,8 @@ def update_block_summaries(summaries, k_cache, block_table, seq_lens, num_new, m
         status_buffer(dev_status, k_cache.device)
     check(load().pkv_update_block_summaries(
         summaries.data_ptr(), k_cache.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), num_new.data_ptr(), int(max_new), B, hkv, d, bs, nb, _ptr(dev_status),
-        raw), "pkv_update_block_summaries")
+        seq_lens.data_ptr(), num_new.data_ptr(), _int32(max_new, "max_new"), B, hkv, d, bs, nb,
+        _ptr(dev_status), raw), "pkv_update_block_summaries")
 
 
 def _query_rows(q):
@@ -854,7 +862,8 @@ def select_blocks(q, summaries, block_table, seq_lens, num_selected: int, num_si
     if sd != d:
         raise ValueError(f"summaries head_dim {sd} differs from q's {d}")
     _table_and_lens(block_table, seq_lens, B)
-    num_selected = int(num_selected)
+    num_selected = _int32(num_selected, "num_selected")
+    num_sink, num_recent = _int32(num_sink, "num_sink"), _int32(num_recent, "num_recent")
     if num_selected < 1:
         raise ValueError("num_selected must be positive")
     shape = (B, hkv, num_selected) if q.dim() == 3 else (B, Q, hkv, num_selected)
@@ -873,7 +882,7 @@ def select_blocks(q, summaries, block_table, seq_lens, num_selected: int, num_si
     check(load().pkv_select_blocks(
         out.data_ptr(), q.data_ptr(), summaries.data_ptr(), block_table.data_ptr(),
         block_table.shape[1], seq_lens.data_ptr(), B, Q, H, hkv, d, 128, nb, num_selected,
-        int(num_sink), int(num_recent), _ptr(dev_status), raw), "pkv_select_blocks")
+        num_sink, num_recent, _ptr(dev_status), raw), "pkv_select_blocks")
     return out
 
 

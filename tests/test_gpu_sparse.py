@@ -865,3 +865,18 @@ def test_selection_with_fewer_good_blocks_than_places(B, q_len, n, width):
             assert int(st.item()) == 2
             assert (buf[:pad] == -77).all() and (buf[pad + places:] == -77).all(), good
             assert np.array_equal(out.cpu().numpy(), expect), good
+
+
+def test_sizes_past_int32_are_refused():
+    """A count whose low 32 bits would pass for another one (2^32 + 1 rows for one)."""
+    kc, _ = caches(4, 2)
+    s = torch.zeros((4, 2, 2, D), dtype=torch.bfloat16, device="cuda")
+    q, t, n = torch.zeros((1, 8, D), dtype=torch.bfloat16, device="cuda"), ints([[1, 2]]), ints([200])
+    with pytest.raises(ValueError, match="max_new"):
+        api.update_block_summaries(s, kc, t, n, ints([1]), 2 ** 32 + 1)
+    for name in ("num_selected", "num_sink", "num_recent"):
+        for x in (2 ** 32 + 1, 2 ** 31, -2 ** 32 + 1):
+            with pytest.raises(ValueError, match=name):
+                api.select_blocks(q, s, t, n, **{"num_selected": 3, name: x})
+    api.update_block_summaries(s, kc, t, n, ints([1]), 2 ** 31 - 1)
+    torch.cuda.synchronize()
