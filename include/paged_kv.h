@@ -606,7 +606,8 @@ int pkv_paged_attention_decode_static(void* out, int32_t out_dtype, float* lse, 
                                       float scale, int32_t window, int* dev_status, void* stream);
 
 /* ==========================================================================
- * Self-test (no counterpart in the pages: a check of the kernels' failure path)
+ * Self-tests (no counterpart in the pages: checks of the kernels' failure path and
+ * of what the block selection takes its products to be)
  * ========================================================================== */
 
 /* Launches one small kernel that waits, with the bounded wait routines every
@@ -617,6 +618,12 @@ int pkv_paged_attention_decode_static(void* out, int32_t out_dtype, float* lse, 
  * `stream`. Errors: PKV_ERR_INVALID_ARG for a null dev_status; PKV_ERR_LAUNCH if
  * the launch fails. */
 int pkv_selftest_bounded_wait(int* dev_status, void* stream);
+
+/* n products d = a b of 16 x 16 and 16 x 8 bf16 matrices with fp32 sums, by the matrix
+ * instruction that scores blocks: a [n, 16, 16] by rows, b [n, 8, 16] by columns,
+ * d [n, 16, 8] by rows, device memory, 16-byte aligned. The selection is exact as long
+ * as a product is off by at most 32 2^-24 of the sum of its terms' magnitudes. */
+int pkv_selftest_bf16_products(float* d, const void* a, const void* b, int32_t n, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1083,3 +1083,19 @@ def selftest_bounded_wait(dev_status, stream=None) -> None:
     check_current_device(dev_status.device)
     check(load().pkv_selftest_bounded_wait(_ptr(dev_status), _stream(stream)),
           "pkv_selftest_bounded_wait")
+
+
+def selftest_bf16_products(a, b, stream=None):
+    """Products of bf16 matrices a [n, 16, 16] and b [n, 8, 16] (by columns), fp32 [n, 16, 8],
+    by the matrix instruction that scores blocks."""
+    _dev_bf16(a, "a")
+    _dev_bf16(b, "b")
+    n = a.shape[0] if a.dim() else 0
+    check_shape(a, (n, 16, 16), "a")
+    check_shape(b, (n, 8, 16), "b")
+    check_same_device(a.device, b=b)
+    check_current_device(a.device)
+    d = _empty((n, 16, 8), torch.float32, a.device, stream)
+    check(load().pkv_selftest_bf16_products(_ptr(d), _ptr(a), _ptr(b), n, _stream(stream)),
+          "pkv_selftest_bf16_products")
+    return d

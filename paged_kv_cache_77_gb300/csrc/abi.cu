@@ -738,4 +738,12 @@ int pkv_selftest_bounded_wait(int* dev_status, void* stream) {
                        "pkv_selftest_bounded_wait");
 }
 
+int pkv_selftest_bf16_products(float* d, const void* a, const void* b, int32_t n, void* stream) {
+  PKV_REQUIRE(n >= 0 && (n == 0 || (d && a && b)) && aligned16(d) && aligned16(a) && aligned16(b),
+              PKV_ERR_INVALID_ARG, "pkv_selftest_bf16_products: bad size or pointer");
+  clear_error();
+  return launch_status(launch_bf16_products(d, a, b, n, static_cast<cudaStream_t>(stream)),
+                       "pkv_selftest_bf16_products");
+}
+
 }  // extern "C"

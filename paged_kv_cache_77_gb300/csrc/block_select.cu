@@ -18,6 +18,7 @@
 #include "device_common.cuh"
 #include "ieee_math.cuh"
 #include "launch.h"
+#include "mma_bf16.cuh"
 #include "pdl.cuh"
 
 namespace pkv {
@@ -47,17 +48,6 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-// d = A B with A of 16 rows and 16 columns, B of 8 columns. Lane 4 i + c holds of A the columns
-// 2c, 2c + 1 of rows i and i + 8, then 2c + 8, 2c + 9 of both; of B those rows of column i; of d
-// columns 2c, 2c + 1 of row i, then of row i + 8.
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};\n"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 }  // namespace
@@ -187,11 +177,12 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, in
 //   |score32 - score| <= eps = 56 2^-24 (sum_d P_d + |N_d|) max |summary|
 //
 // (the 16 sums of a product, each at least as good as a truncation to 24 bits: 32, of which 20,000
-// products of random numbers with exponents up to 40 apart reached 4; the 16 products' sum 16; the columns' 3; the coefficients 1; room for the bound's own), and finds the K-th largest
-// fp32 score tau to within a bin narrower
-// than eps, takes every block above the bin by more than 2 eps and none below it by more, and
-// scores the blocks between again where they are more than the places left: few of them in pairs
-// of fp32 numbers, and in fp64 where those do not tell them apart. The result is that of fp64
+// products of random numbers with exponents up to 40 apart reached 4; pkv_selftest_bf16_products
+// hands the products out, and a test holds them to this; the 16 products' sum 16; the columns' 3;
+// the coefficients 1; room for the bound's own), and finds the K-th largest fp32 score tau to within
+// a bin narrower than eps, takes every block above the bin by more than 2 eps and none below it by
+// more, and scores the blocks between again where they are more than the places left: few of them in
+// pairs of fp32 numbers, and in fp64 where those do not tell them apart. The result is that of fp64
 // scores, ties to the lower block, whatever the order of the fp32 sums.
 //
 // A block whose score is NaN (a NaN key, or infinite keys that cancel) ranks above all others.

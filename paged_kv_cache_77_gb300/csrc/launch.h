@@ -138,5 +138,7 @@ cudaError_t launch_prefill(const void* q, const int32_t* cu_q, const void* k_cac
 
 // Self-test: a bounded wait that runs out (selftest.cu).
 cudaError_t launch_bounded_wait(int* dev_status, cudaStream_t stream);
+// And the selection's bf16 matrix products, n of them.
+cudaError_t launch_bf16_products(float* d, const void* a, const void* b, int n, cudaStream_t stream);
 
 }  // namespace pkv

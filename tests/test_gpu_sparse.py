@@ -880,3 +880,31 @@ def test_sizes_past_int32_are_refused():
                 api.select_blocks(q, s, t, n, **{"num_selected": 3, name: x})
     api.update_block_summaries(s, kc, t, n, ints([1]), 2 ** 31 - 1)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("spread", [0, 1, 3, 8, 16, 40, 100])
+@pytest.mark.parametrize("signs", [False, True])
+def test_matrix_products_are_as_exact_as_the_selection_takes_them_to_be(spread, signs):
+    """A sum of 16 products of bf16 numbers (exact in fp32 each), added one by one and truncated to
+    24 bits each time, is off by at most 16 2^-23 of the sum of their magnitudes, and the order or a
+    better rounding only helps. The selection's bound counts 32 2^-24 for it; below 2^-126 it counts
+    on nothing. In 64 bits the 16 products and their sum are off by 2^-49 of that sum at most."""
+    n = 20000
+    g = torch.Generator(device="cuda").manual_seed(spread)
+
+    def numbers(shape):
+        e = 127 - torch.randint(0, spread + 1, shape, generator=g, device="cuda", dtype=torch.int32)
+        bits = (e << 7) | torch.randint(0, 128, shape, generator=g, device="cuda", dtype=torch.int32)
+        x = bits.to(torch.int16).view(torch.bfloat16)
+        return torch.where(torch.rand(shape, generator=g, device="cuda") < 0.5, -x, x) if signs else x
+
+    a, b = numbers((n, 16, 16)), numbers((n, 8, 16))
+    if signs and spread:  # sums that cancel: half the terms against the other half, but for one
+        a[: n // 2, :, 8:15] = -a[: n // 2, :, :7]
+        b[: n // 2, :, 8:15] = b[: n // 2, :, :7]
+    d = api.selftest_bf16_products(a, b)
+    x, y = a.double(), b.double().transpose(1, 2)
+    err, size = (d.double() - x @ y).abs(), x.abs() @ y.abs()
+    floor = 2.0 ** -126 * (x.abs().sum(2)[:, :, None] + y.abs().sum(1)[:, None] + 16)
+    bound = (32 * 2.0 ** -24 + 2.0 ** -49) * size + floor
+    assert (err <= bound).all(), float((err / size).max() * 2 ** 24)

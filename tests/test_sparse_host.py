@@ -77,6 +77,12 @@ def test_workspace_is_that_of_a_batch_of_rows():
     assert lib.pkv_decode_sparse_workspace_size(1 << 20, 1 << 20, 64, 8, 128) == 0
 
 
+def test_selftest_of_the_products_refuses_bad_arguments():
+    lib = load()
+    for args in ((P, P, P, -1), (None, P, P, 2), (P, P, None, 2), (P, P + 8, P, 2)):
+        assert lib.pkv_selftest_bf16_products(*args, None) == -1
+
+
 def test_the_binding_refuses_host_tensors():
     import torch
 
