@@ -157,3 +157,33 @@ def test_two_calls_at_once_on_two_streams_with_tensors_of_their_own():
     torch.cuda.synchronize()
     for i, out in got:
         assert torch.equal(out, want[i])
+
+
+@pytest.mark.gpu
+def test_calls_on_a_forked_stream_inside_a_capture_make_their_tensors_in_the_graph():
+    """Selection and sparse attention on a side stream of a captured graph, no buffer given: the
+    replays follow their inputs while other graphs and eager calls use the allocator."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rows = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    kc, vc, s, q = rows(9, 128, 2, 128), rows(9, 128, 2, 128), rows(9, 2, 2, 128), rows(1, 16, 128)
+    t = torch.arange(9, dtype=torch.int32, device="cuda").view(1, 9)
+    lens = torch.tensor([1100], dtype=torch.int32, device="cuda")
+
+    def step(stream=None):
+        idx = api.select_blocks(q, s, t, lens, 4, stream=stream)
+        return api.paged_attention_decode_sparse(q, kc, vc, t, lens, idx, 0.1, stream=stream)
+
+    side = torch.cuda.Stream()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = step(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(4):
+        q.copy_(torch.randn(q.shape, generator=g, device="cuda"))
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
