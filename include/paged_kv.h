@@ -412,7 +412,8 @@ int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32
  * that a row sees competes: a table whose expired entries hold the null block (a sliding
  * window's) does not go with it.
  * block_indices may not overlap anything the call reads (PKV_ERR_INVALID_ARG).
- * Supported: head_dim 128, block_size 128, H % H_kv == 0, H / H_kv <= 16,
+ * Supported: head_dim 128, block_size 128, H % H_kv == 0, H / H_kv <= 16 (lists of groups
+ * that pkv_paged_attention_decode_sparse does not take are for the caller's own attention),
  * num_sink + num_recent <= num_selected, max_blocks_per_seq <= 8192 (1,048,576 tokens).
  * No workspace. */
 int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summaries,
@@ -432,6 +433,8 @@ int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summari
  * with a NaN score (a NaN in its query or in a key that it attends to) o = lse = NaN.
  *   out, q, lse, caches, block_table, seq_lens as for pkv_paged_attention_decode_spec
  *   block_indices [B, q_len, H_kv, num_selected] int32 (device)
+ * Always the tensor-core kernel, whatever pkv_set_decode_kernel chose: the weights enter the
+ * value product rounded to bf16, and the same rounded weights divide it.
  * Supported: head_dim 128, block_size 128, H / H_kv in {1, 2, 4, 8, 16}.
  * Workspace: pkv_decode_sparse_workspace_size() bytes, 256-byte aligned. */
 size_t pkv_decode_sparse_workspace_size(int32_t B, int32_t q_len, int32_t H, int32_t H_kv,

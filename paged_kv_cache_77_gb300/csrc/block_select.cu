@@ -159,8 +159,8 @@ cudaError_t launch_block_summaries(const SummaryArgs& a, cudaStream_t stream, in
 }
 
 // ------------------------------------------------------------------ selection
-// One cluster of C CTAs per (query row, kv head). Each CTA scores one run of the row's blocks
-// and keeps their keys (order-preserving whole numbers) in its shared memory. A row of at most
+// One cluster of C CTAs per kv head and query row, or two neighbouring query rows of a sequence
+// (kRows). Each CTA scores one run of the rows' blocks and keeps their keys (order-preserving whole numbers) in its shared memory. A row of at most
 // 256 competing blocks is one CTA's, and is selected by one warp with the keys in registers;
 // of longer ones all keys go to the shared memory of the cluster's first CTA, which selects with
 // the keys in registers. Only where many blocks are at the border the CTAs select together,

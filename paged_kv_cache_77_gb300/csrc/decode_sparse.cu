@@ -5,7 +5,7 @@
 // one does: it starts from the cuts instead.
 //
 // Bound by HBM, as the dense kernel: 64 KB per listed (block, kv head). Measured on GB300: 512
-// rows x 32 blocks of 64 long sequences (0.99 GB) 159.5 us, 92 % of the copy rate; 64 rows x 4
+// rows x 32 blocks of 64 long sequences (0.99 GB) 159.7 us, 92 % of the copy rate; 64 rows x 4
 // blocks (17 MB) 16 us a call, host time and latency; 8,192 query rows x 8 kv heads x 2 blocks
 // 1.5 ms (6.5 ms with the dense merge and a seek by one thread).
 #include "decode_tc.cuh"

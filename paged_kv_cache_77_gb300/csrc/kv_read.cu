@@ -64,7 +64,7 @@ cudaError_t launch_kv_read_fp8(void* k, void* v, const void* k_cache, const void
   if (rows == 0) return cudaSuccess;
   int64_t blocks = (rows + 31) / 32;
   // Many small CTAs, so that an SM's loads and stores overlap across them: 131,071 tokens of 8
-  // heads in random order take 131.8 us on GB300 with up to 64 CTAs per SM of grid (91 % of
+  // heads in random order take 129.4 us on GB300 with up to 64 CTAs per SM of grid (93 % of
   // the copy rate, 98 % with the 32-byte sectors that the scattered 4-byte scales come in),
   // 153 us with 8. Two or four rows per lane at a time measured 135 to 180 us.
   const int64_t cap = (int64_t)num_sms * 64;

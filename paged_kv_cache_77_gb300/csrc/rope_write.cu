@@ -14,11 +14,12 @@
 //
 // Layout: a lane holds 16 elements of one head, either 8 whole pairs (two 16-byte vectors,
 // which are rope_dim / 2 apart or neighbours) or 16 elements that pass through, so a
-// head_dim of 128 takes 8 lanes and a warp 4 heads. The cosines and sines of a lane's 8
-// pairs are the same for every head of a token: they are loaded once and used for the q,
-// k and v heads of the warp's share (kUnroll passes of 4 heads; every load of the share is
-// issued before any arithmetic). Elements are read and written by the same thread, so q
-// may be rotated in place.
+// head_dim of 128 takes 8 lanes and a warp 4 heads. A warp's item is the q, the k or the v
+// heads of a token, up to kUnroll passes of 4 (one pass of heads that are quantised); every
+// load of an item is issued before any arithmetic. The cosines and sines of a lane's 8 pairs
+// are the same for every head: a q or k item loads them once for its heads, the token's other
+// items load them again, mostly from cache. Elements are read and written by the same thread,
+// so q may be rotated in place.
 //
 // Roofline: HBM. Algorithmic bytes per token = 2 (q) + 2 (k, v to bf16; 1.5 to FP8) times
 // the rows' bytes, the table row and 4 bytes of slot and of each position.
@@ -64,7 +65,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // off, so it is corrected once before: one division a row and five operations a value in place
 // of a division a value (FP8 prefill of 9,001 tokens: 61.4 us with divisions). Scales for which a remainder, y or an
 // infinite value would leave the normal numbers divide. (Telling the codes of two enclosing
-// products apart and dividing in between was slower: bf16 rows hit exact ties often.)
+// products apart and dividing in between gained little, 65.5 to 64.6 us at the time: bf16 rows
+// hit exact ties often.)
 __device__ __forceinline__ uint4 codes16(const float* f, float scale) {
   uint32_t u[4] = {0, 0, 0, 0};
   if (!__float_as_uint(scale)) return make_uint4(0, 0, 0, 0);  // (a comparison may flush it)
