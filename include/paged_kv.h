@@ -579,6 +579,59 @@ int pkv_paged_attention_decode_fp8(void* out, int32_t out_dtype, float* lse, con
                                    void* workspace, size_t workspace_bytes, int* dev_status,
                                    void* stream);
 
+/* 4-bit KV cache: write, read and decode. 72 bytes per row of 128 values where bf16 takes
+ * 256 and FP8 132 (the pages' QuantizedCache: 4-bit grouped quantisation, "KV Cache 笔记").
+ * Format: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), element 2i in the low
+ * half of byte i and 2i + 1 in the high half, and one scale byte per 16 consecutive values:
+ * the upper 8 of the 15 magnitude bits of an fp16 (5 bits of exponent, 3 of fraction).
+ *   scale = the scale nearest to amax / 6, ties to the even byte, 10240 (0xE2) at most
+ *   code  = the code nearest to x / scale, ties to the even one, magnitudes past 6 to 6
+ *   value = code * scale (6 significant bits: exact in bf16 and fp16)
+ * decided as in exact arithmetic. 16 values of which none reaches 6 * 2^-18 have scale 0 and
+ * codes 0; magnitudes past 61440 are held as 61440; 16 values with an infinity or a NaN among
+ * them have the scale 0xFF and read back as NaN. Scale bytes 0xE3 to 0xFE are never written;
+ * 0xF8 and above read as NaN, and the decode may take any of them for NaN.
+ *   k_cache, v_cache [num_blocks, H_kv, block_size, 64] uint8: head-major, so that what the
+ *                    decode reads of a block for one kv head is one piece
+ *   k_scale, v_scale [num_blocks, H_kv, block_size, 8] uint8
+ * Cache tensors like any other: pkv_copy_blocks copies them for a fork. head_dim must be 128
+ * (PKV_ERR_UNSUPPORTED). All pointers 16-byte aligned, slot_mapping 4. */
+
+/* Quantise new rows and write them through slot_mapping (negative slot: skipped; slot >=
+ * num_blocks * block_size: skipped and PKV_DEV_BAD_SLOT). k, v [num_tokens, H_kv, 128] bf16;
+ * *_stride: elements from one token to the next (a multiple of 8; the heads of a token are
+ * contiguous). k, v and slot_mapping may not overlap the caches (PKV_ERR_INVALID_ARG).
+ * Duplicate slots as for pkv_kv_cache_write. */
+int pkv_kv_cache_write_fp4(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,
+                           int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                           int* dev_status, void* stream);
+/* Rows of a 4-bit cache widened to bf16, as pkv_kv_cache_read_fp8 does for an FP8 cache: a
+ * negative slot gives a row of zeros, a slot >= num_blocks * block_size too and sets
+ * PKV_DEV_BAD_SLOT. k, v [num_tokens, H_kv, 128] bf16, which may overlap neither each other
+ * nor anything the call reads (PKV_ERR_INVALID_ARG). */
+int pkv_kv_cache_read_fp4(void* k, void* v, const void* k_cache, const void* v_cache,
+                          const void* k_scale, const void* v_scale, const int32_t* slot_mapping,
+                          int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                          int32_t num_kv_heads, int32_t head_dim, int* dev_status, void* stream);
+/* pkv_paged_attention_decode_spec over a 4-bit cache, q_len 1..4 rows per sequence (1: plain
+ * decode): same arguments, result, workspace (pkv_decode_spec_workspace_size) and limits, plus
+ * the two scale arrays. The attention is that of the dequantised cache; q stays bf16 (elements
+ * smaller than 2^-22 of their row's largest lose bits), the weights enter the value product
+ * rounded to fp16, and the same rounded weights divide it. Rows of positions that no query row
+ * sees are never used, whatever bytes they hold. A head with a NaN score has o = lse = NaN; a
+ * NaN among 16 values of V makes those 16 outputs NaN in the rows that see it. A block of the
+ * table outside [0, num_blocks) is skipped (PKV_DEV_BAD_BLOCK). */
+int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, const void* q,
+                                   const void* k_cache, const void* v_cache, const void* k_scale,
+                                   const void* v_scale, const int32_t* block_table,
+                                   int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t B,
+                                   int32_t q_len, int32_t H, int32_t H_kv, int32_t head_dim,
+                                   int32_t block_size, int64_t num_blocks, float scale,
+                                   int32_t window, void* workspace, size_t workspace_bytes,
+                                   int* dev_status, void* stream);
+
 /* Decode without any caller-provided scratch. The paper has no counterpart for
  * this call; it exists for callers that cannot allocate device memory (a plugin
  * inside a runtime that owns the allocator, a serving loop whose HBM is already

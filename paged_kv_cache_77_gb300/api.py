@@ -733,6 +733,107 @@ def paged_attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     return out
 
 
+def _fp4_cache(k_cache, v_cache, k_scale, v_scale):
+    """(num_blocks, H_kv, block_size) of a 4-bit cache after checking its four arrays."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"),
+                 (v_scale, "v_scale")):
+        if t is not None:
+            _fp8_cache(t, n)  # contiguous uint8 on the GPU
+    if k_cache.dim() != 4 or k_cache.shape[3] != 64:
+        raise ValueError("k_cache must be [num_blocks, H_kv, block_size, 64] codes of 128 values, "
+                         f"got {_shape_str(k_cache.shape)}")
+    nb, hkv, bs, _ = k_cache.shape
+    if v_cache is not None:
+        check_shape(v_cache, (nb, hkv, bs, 64), "v_cache")
+        check_shape(v_scale, (nb, hkv, bs, 8), "v_scale")
+    check_shape(k_scale, (nb, hkv, bs, 8), "k_scale")
+    return nb, hkv, bs
+
+
+def kv_cache_write_fp4(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, dev_status=None,
+                       stream=None) -> None:
+    """Quantise new K/V rows to 4 bits (E2M1 codes, a scale byte per 16 values) and scatter them.
+
+    k_cache / v_cache [nb, H_kv, bs, 64] uint8, k_scale / v_scale [nb, H_kv, bs, 8] uint8;
+    k / v [T, H_kv, 128] bf16 (slices of one projection's output will do)."""
+    nb, hkv, bs = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    _dev_i32(slot_mapping, "slot_mapping")
+    T = slot_mapping.numel()
+    kh, ks = _rope_rows(k, T, 128, "k")
+    vh, vs = _rope_rows(v, T, 128, "v")
+    if kh != hkv or vh != hkv:
+        raise ValueError(f"k and v must have the cache's {hkv} heads")
+    index = k_cache.get_device()
+    _check_gpu(index, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, k=k, v=v,
+               slot_mapping=slot_mapping)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, k_cache.device)
+    check(load().pkv_kv_cache_write_fp4(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.data_ptr(),
+        ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, nb, bs, hkv, 128, _ptr(dev_status), raw),
+        "pkv_kv_cache_write_fp4")
+
+
+def kv_cache_read_fp4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=None, v_out=None,
+                      dev_status=None, stream=None):
+    """Rows of a 4-bit cache widened to bf16 (exactly): returns (k, v), [T, H_kv, 128] each
+    (`k_out` and `v_out` if given). A negative slot gives a row of zeros."""
+    nb, hkv, bs = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    _dev_i32(slot_mapping, "slot_mapping")
+    T = slot_mapping.numel()
+    shape = (T, hkv, 128)
+    if k_out is None:
+        k_out = _empty(shape, torch.bfloat16, k_cache.device, stream)
+    if v_out is None:
+        v_out = _empty(shape, torch.bfloat16, k_cache.device, stream)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _dev_bf16(t, n)
+        check_shape(t, shape, n)
+    index = k_cache.get_device()
+    _check_gpu(index, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, slot_mapping=slot_mapping,
+               k_out=k_out, v_out=v_out)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, k_cache.device)
+    check(load().pkv_kv_cache_read_fp4(
+        k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), slot_mapping.data_ptr(), T, nb, bs, hkv, 128,
+        _ptr(dev_status), raw), "pkv_kv_cache_read_fp4")
+    return k_out, v_out
+
+
+def paged_attention_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                               scale: float, window: int = 0, out=None, lse=None,
+                               out_dtype=torch.float32, workspace=None, dev_status=None,
+                               stream=None):
+    """Decode attention over a 4-bit cache (the arrays of kv_cache_write_fp4).
+
+    q [B, H, 128], or [B, q_len, H, 128] for q_len 1..4 new rows per sequence (bottom-right
+    causal); returns out in q's shape (and fills lse, the shape without its last axis). The
+    workspace is decode_spec_workspace_size's."""
+    B, Q, H, d = _query_rows(q)
+    nb, hkv, bs = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    _table_and_lens(block_table, seq_lens, B)
+    index = q.get_device()
+    _check_gpu(index, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+               block_table=block_table, seq_lens=seq_lens)
+    raw = _launch_stream(index, stream)
+    dev = q.device
+    out = out_buffer(out, q.shape, out_dtype, dev, stream=stream)
+    lse_buffer(lse, tuple(q.shape[:-1]), dev)
+    status_buffer(dev_status, dev)
+    code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
+    workspace, ws_bytes = workspace_buffer(
+        workspace, decode_spec_workspace_size(B, Q, H, hkv, d), dev, stream=stream)
+    check(load().pkv_paged_attention_decode_fp4(
+        out.data_ptr(), code, _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), B, Q, H, hkv, d, bs, nb, float(scale), int(window),
+        workspace.data_ptr(), ws_bytes, _ptr(dev_status), raw), "pkv_paged_attention_decode_fp4")
+    return out
+
+
 def set_decode_kernel(kernel: int) -> None:
     """Select the decode kernel process-wide (KERNEL_AUTO / _CUDA_CORE / _TENSOR_CORE)."""
     check(load().pkv_set_decode_kernel(kernel), "pkv_set_decode_kernel")

@@ -291,6 +291,36 @@ bool rows_overlap(const void* a, int64_t a_stride, int64_t a_width, const void* 
   return !(off >= a_width && off + b_width <= a_stride);
 }
 
+// Validation and argument set-up shared by the 4-bit write and read.
+int fp4_setup(pkv::KvFp4Args& a, const char* what, const void* k_cache, const void* v_cache,
+              const void* k_scale, const void* v_scale, const void* k, const void* v,
+              const int32_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,
+              int32_t block_size, int32_t num_kv_heads, int32_t head_dim, int* dev_status) {
+  using namespace pkv;
+  PKV_REQUIRE(num_tokens >= 0 && num_blocks > 0 && block_size > 0 && num_kv_heads > 0,
+              PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  PKV_REQUIRE(head_dim == 128, PKV_ERR_UNSUPPORTED, "%s: only head_dim 128 is implemented", what);
+  PKV_REQUIRE(num_blocks * block_size <= INT32_MAX, PKV_ERR_UNSUPPORTED,
+              "%s: num_blocks * block_size must fit in int32", what);
+  PKV_REQUIRE(num_tokens <= INT32_MAX && num_kv_heads <= (1 << 20), PKV_ERR_UNSUPPORTED,
+              "%s: too many rows", what);
+  PKV_REQUIRE(k_cache && v_cache && k_scale && v_scale && (num_tokens == 0 || (k && v && slot_mapping)),
+              PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+  PKV_REQUIRE(aligned16(k_cache) && aligned16(v_cache) && aligned16(k_scale) && aligned16(v_scale) &&
+                  aligned16(k) && aligned16(v) && (((uintptr_t)slot_mapping) & 3) == 0,
+              PKV_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  a = KvFp4Args{(uint8_t*)k_cache, (uint8_t*)v_cache, (uint8_t*)k_scale, (uint8_t*)v_scale, slot_mapping,
+                dev_status, num_tokens, num_blocks, block_size, num_kv_heads};
+  return PKV_OK;
+}
+
+// Whether [p, p + bytes) shares a byte with a 4-bit cache's codes or scales.
+bool fp4_overlaps(const pkv::KvFp4Args& a, const void* p, int64_t bytes) {
+  const int64_t rows = a.num_blocks * a.block_size * a.hkv;
+  return overlap(p, bytes, a.k_cache, rows * 64) || overlap(p, bytes, a.v_cache, rows * 64) ||
+         overlap(p, bytes, a.k_scale, rows * 8) || overlap(p, bytes, a.v_scale, rows * 8);
+}
+
 // Validation and argument set-up shared by the two rotary writes.
 int rope_setup(pkv::RopeArgs& a, const char* what, void* k_cache, void* v_cache, void* q_out,
                int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
@@ -474,6 +504,79 @@ int pkv_paged_attention_decode_fp8(void* out, int32_t out_dtype, float* lse, con
   int rc = launch_status(launch_decode_fp8(a, s), "pkv_paged_attention_decode_fp8 (attention)");
   if (rc != PKV_OK) return rc;
   return launch_status(launch_decode_merge(a, s), "pkv_paged_attention_decode_fp8 (merge)");
+}
+
+int pkv_kv_cache_write_fp4(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* slot_mapping, int64_t num_tokens, int64_t num_blocks,
+                           int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                           int* dev_status, void* stream) {
+  const char* what = "pkv_kv_cache_write_fp4";
+  KvFp4Args a;
+  const int rc = fp4_setup(a, what, k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, num_tokens,
+                           num_blocks, block_size, num_kv_heads, head_dim, dev_status);
+  if (rc != PKV_OK) return rc;
+  const int64_t width = (int64_t)num_kv_heads * head_dim;
+  PKV_REQUIRE(k_stride >= 0 && v_stride >= 0 && k_stride % 8 == 0 && v_stride % 8 == 0,
+              PKV_ERR_INVALID_ARG, "%s: bad token stride", what);
+  if (num_tokens > 0)
+    PKV_REQUIRE(!fp4_overlaps(a, k, ((num_tokens - 1) * k_stride + width) * 2) &&
+                    !fp4_overlaps(a, v, ((num_tokens - 1) * v_stride + width) * 2) &&
+                    !fp4_overlaps(a, slot_mapping, num_tokens * 4),
+                PKV_ERR_INVALID_ARG, "%s: an input overlaps the caches", what);
+  clear_error();
+  return launch_status(launch_kv_write_fp4(a, k, k_stride, v, v_stride, (cudaStream_t)stream,
+                                           current_num_sms()),
+                       what);
+}
+
+int pkv_kv_cache_read_fp4(void* k, void* v, const void* k_cache, const void* v_cache,
+                          const void* k_scale, const void* v_scale, const int32_t* slot_mapping,
+                          int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                          int32_t num_kv_heads, int32_t head_dim, int* dev_status, void* stream) {
+  const char* what = "pkv_kv_cache_read_fp4";
+  KvFp4Args a;
+  const int rc = fp4_setup(a, what, k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, num_tokens,
+                           num_blocks, block_size, num_kv_heads, head_dim, dev_status);
+  if (rc != PKV_OK) return rc;
+  const int64_t bytes = num_tokens * num_kv_heads * 256;
+  PKV_REQUIRE(!overlap(k, bytes, v, bytes) && !fp4_overlaps(a, k, bytes) && !fp4_overlaps(a, v, bytes) &&
+                  !overlap(k, bytes, slot_mapping, num_tokens * 4) &&
+                  !overlap(v, bytes, slot_mapping, num_tokens * 4),
+              PKV_ERR_INVALID_ARG, "%s: k or v overlaps the other or an input", what);
+  clear_error();
+  return launch_status(launch_kv_read_fp4(a, k, v, (cudaStream_t)stream, current_num_sms()), what);
+}
+
+int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, const void* q,
+                                   const void* k_cache, const void* v_cache, const void* k_scale,
+                                   const void* v_scale, const int32_t* block_table,
+                                   int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t B,
+                                   int32_t q_len, int32_t H, int32_t H_kv, int32_t head_dim,
+                                   int32_t block_size, int64_t num_blocks, float scale,
+                                   int32_t window, void* workspace, size_t workspace_bytes,
+                                   int* dev_status, void* stream) {
+  const char* what = "pkv_paged_attention_decode_fp4";
+  PKV_REQUIRE(max_blocks_per_seq <= INT32_MAX / 128, PKV_ERR_UNSUPPORTED,
+              "%s: max_blocks_per_seq * 128 must fit in int32", what);
+  PKV_REQUIRE(B < 0 || H_kv < 0 || B <= INT32_MAX / (H_kv > 0 ? H_kv : 1), PKV_ERR_UNSUPPORTED,
+              "%s: B * H_kv must fit in int32", what);
+  DecodeArgs a;
+  bool empty;
+  const int rc0 = decode_setup(a, &empty, what, out, out_dtype, lse, q, k_cache, v_cache,
+                               block_table, max_blocks_per_seq, seq_lens, B, H, H_kv, head_dim,
+                               block_size, num_blocks, scale, window, workspace, workspace_bytes,
+                               dev_status, q_len);
+  if (rc0 != PKV_OK || empty) return rc0;
+  PKV_REQUIRE(k_scale && v_scale && aligned16(k_scale) && aligned16(v_scale), PKV_ERR_INVALID_ARG,
+              "%s: scale arrays must be set and 16-byte aligned", what);
+  a.k_scale4 = (const uint8_t*)k_scale;
+  a.v_scale4 = (const uint8_t*)v_scale;
+  clear_error();
+  cudaStream_t s = (cudaStream_t)stream;
+  const int rc = launch_status(launch_decode_fp4(a, s), "pkv_paged_attention_decode_fp4 (attention)");
+  if (rc != PKV_OK) return rc;
+  return launch_status(launch_decode_merge(a, s), "pkv_paged_attention_decode_fp4 (merge)");
 }
 
 size_t pkv_decode_sparse_workspace_size(int32_t B, int32_t q_len, int32_t H, int32_t H_kv,

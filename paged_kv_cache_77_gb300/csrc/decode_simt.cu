@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
   put(make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (a.lse && lane == 0) a.lse[row] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
+  // A piece whose log-sum-exp is NaN (the 4-bit decode's, for a NaN score) makes both NaN.
+  if (a.lse && lane == 0) a.lse[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * kLn2;
 }
 
 // H here counts every query row of a sequence (q_len * heads).

@@ -51,6 +51,20 @@ cudaError_t launch_kv_read_fp8(void* k, void* v, const void* k_cache, const void
                                int64_t num_tokens, int64_t num_blocks, int block_size, int hkv,
                                int* dev_status, cudaStream_t stream, int num_sms);
 
+// The 4-bit cache's write and read (kv_fp4.cu).
+struct KvFp4Args {
+  uint8_t *k_cache, *v_cache;  // [nb, Hkv, bs, 64] codes
+  uint8_t *k_scale, *v_scale;  // [nb, Hkv, bs, 8]
+  const int32_t* slots;        // [T]
+  int* dev_status;
+  int64_t num_tokens, num_blocks;
+  int block_size, hkv;
+};
+// Strides in elements, between tokens; the heads of a token are contiguous.
+cudaError_t launch_kv_write_fp4(const KvFp4Args& a, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, cudaStream_t stream, int num_sms);
+cudaError_t launch_kv_read_fp4(const KvFp4Args& a, void* k, void* v, cudaStream_t stream, int num_sms);
+
 // Block summaries and block selection (block_select.cu).
 constexpr int kSelectMaxBlocks = 8192;  // widest table of a selection: a million tokens
 struct SummaryArgs {
@@ -98,6 +112,8 @@ struct DecodeArgs {
   float scale_log2;           // scale * log2(e)
   const float* k_scale;       // FP8 cache only: [nb, Hkv, bs] per-row scales
   const float* v_scale;
+  const uint8_t* k_scale4;    // 4-bit cache only: [nb, Hkv, bs, 8]
+  const uint8_t* v_scale4;
   // Sparse decode only: B counts query rows, rows_per_seq of each sequence.
   const int32_t* block_indices;  // [B, Hkv, num_selected] blocks of the sequence, or null
   int num_selected, rows_per_seq;
@@ -118,6 +134,9 @@ cudaError_t launch_decode_sparse(const DecodeArgs& a, cudaStream_t stream);
 // tcgen05 split-KV decode over an FP8 (E4M3) cache with per-row scales; same
 // partials and merge as above.
 cudaError_t launch_decode_fp8(const DecodeArgs& a, cudaStream_t stream);
+// Split-KV decode over the 4-bit cache for q_len 1..4 query rows per sequence; same partials
+// and merge as above.
+cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t stream);
 
 // Absorbed MLA decode (tcgen05) plus its merge, q_len query rows per sequence
 // (1 for plain decode). Workspace: mla_workspace_bytes(B * q_len, num_sms / 2).
