@@ -632,6 +632,80 @@ int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, con
                                    int32_t window, void* workspace, size_t workspace_bytes,
                                    int* dev_status, void* stream);
 
+/* Eviction by accumulated attention weight: rows that the queries pay little attention to
+ * leave the cache (the pages drop positions by a window only, "KV Cache 管理设计文档" §2.3).
+ * Three calls: after a step's attention, add its weights; now and then, select the rows that
+ * stay and move them to the front. Each kv head keeps rows of its own, all heads of a sequence
+ * equally many, so its block table goes on serving every head; keys carry their rotary
+ * position, so a row's place in the cache does not matter to the attention.
+ *
+ * pkv_accumulate_attention_weights: for every position p < seq_lens[b] of sequence b, and kv
+ * head g,
+ *   weights[p] = (p is fresh ? 0 : decay weights[p]) +
+ *                sum_i sum_h exp(scale q[b,i,h] . k[p,g] - lse[b,i,h])
+ * over the query rows i with p <= seq_lens[b] - q_len + i and the H / H_kv heads h of g. lse is
+ * what the step's attention returned for these rows (fp32, natural log; of any of the decode
+ * calls, or the last rows of a prefill), so the terms of a head and row sum to 1. The
+ * num_fresh[b] newest positions are fresh (none if that is negative, all if it exceeds the
+ * length): rows that the step wrote, whose places may hold another request's sums.
+ *   weights [num_blocks, H_kv, block_size] fp32: a cache tensor like any other, in the blocks'
+ *     order (pkv_copy_blocks copies it for a fork, pkv_compact_rows moves it with its rows)
+ *   q [B, q_len, H, head_dim] bf16, lse [B, q_len, H] fp32, any q_len
+ *   k_cache, k_scale by key_format: PKV_KEYS_BF16 [num_blocks, block_size, H_kv, head_dim] bf16
+ *     and NULL; PKV_KEYS_FP8 the FP8 cache's codes and scales; PKV_KEYS_FP4 the 4-bit cache's
+ * Positions that no row sees hold any bytes; a NaN score makes the position's sum NaN. fp32
+ * sums in a fixed order: the same call gives the same bits. A block that two sequences of one
+ * call both hold must not be (their sums would race: call once per sequence). Table entries
+ * outside [0, num_blocks) are skipped (PKV_DEV_BAD_BLOCK), lengths past the table clamped
+ * (PKV_DEV_BAD_LENGTH). weights may not overlap anything the call reads
+ * (PKV_ERR_INVALID_ARG). Supported: head_dim 128, block_size 128, H % H_kv == 0,
+ * H / H_kv <= 16 (PKV_ERR_UNSUPPORTED otherwise). No workspace. */
+#define PKV_KEYS_BF16 0
+#define PKV_KEYS_FP8 1
+#define PKV_KEYS_FP4 2
+int pkv_accumulate_attention_weights(float* weights, const void* q, const float* lse,
+                                     const void* k_cache, const void* k_scale, int32_t key_format,
+                                     const int32_t* block_table, int32_t max_blocks_per_seq,
+                                     const int32_t* seq_lens, const int32_t* num_fresh, int32_t B,
+                                     int32_t q_len, int32_t H, int32_t H_kv, int32_t head_dim,
+                                     int32_t block_size, int64_t num_blocks, float scale,
+                                     float decay, int* dev_status, void* stream);
+
+/* pkv_select_rows: for each sequence and kv head the num_keep positions with the largest
+ * weights, ascending, -1 behind the last one. Positions [0, num_sink) and the last num_recent
+ * are always among them; equal weights are taken lowest position first (-0 equals 0), a NaN
+ * ranks above all. A sequence with no more than num_keep positions keeps every one, and no
+ * weight of it is read. Rows of a table entry outside [0, num_blocks) rank below all
+ * (PKV_DEV_BAD_BLOCK); lengths past the table are clamped (PKV_DEV_BAD_LENGTH).
+ *   kept [B, H_kv, num_keep] int32 (written), which may not overlap anything the call reads
+ * Supported: block_size 128, num_sink + num_recent <= num_keep. No workspace. */
+int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_table,
+                    int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t B, int32_t H_kv,
+                    int32_t block_size, int64_t num_blocks, int32_t num_keep, int32_t num_sink,
+                    int32_t num_recent, int* dev_status, void* stream);
+
+/* pkv_compact_rows: in each of num_caches caches, row i of sequence b and kv head g becomes
+ * what row kept[b][g][i] was, for i up to the first negative entry; afterwards the sequence has
+ * that many rows and its blocks behind them can go back to the pool. Rows behind stay as they
+ * were. kept[b][g] must ascend (pkv_select_rows' does).
+ *   caches, row_bytes, head_major: HOST arrays. A cache is [num_blocks, block_size, H_kv] rows
+ *     of row_bytes (head_major 0: the bf16 and FP8 caches), or [num_blocks, H_kv, block_size]
+ *     (head_major 1: the 4-bit cache, scales, weights). Caches may not overlap one another,
+ *     kept or the tables (PKV_ERR_INVALID_ARG).
+ *   new_block_table [B, new_max_blocks_per_seq] int32, or NULL: in place. With a table, rows are
+ *     read through block_table and written through the new one (for blocks that other requests
+ *     share); a block that both tables of a sequence hold must have the same place in both. No
+ *     block that one sequence writes may be read or written by another.
+ * Entries past block_table set PKV_DEV_BAD_LENGTH, rows of a block outside [0, num_blocks)
+ * PKV_DEV_BAD_BLOCK; neither is moved. Supported: row_bytes a multiple of 4, up to 16 caches
+ * (PKV_ERR_UNSUPPORTED otherwise). Caches 16-byte aligned. No workspace. */
+int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_t* head_major,
+                     int32_t num_caches, const int32_t* kept, int32_t num_keep,
+                     const int32_t* block_table, int32_t max_blocks_per_seq,
+                     const int32_t* new_block_table, int32_t new_max_blocks_per_seq, int32_t B,
+                     int32_t H_kv, int32_t block_size, int64_t num_blocks, int* dev_status,
+                     void* stream);
+
 /* Decode without any caller-provided scratch. The paper has no counterpart for
  * this call; it exists for callers that cannot allocate device memory (a plugin
  * inside a runtime that owns the allocator, a serving loop whose HBM is already

@@ -59,6 +59,11 @@ SIGNATURES = {
     "pkv_paged_attention_decode_fp4": (C.c_int, [vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32,
                                                  i32, i32, i32, i32, i32, i64, f32, i32, vp, sz,
                                                  vp, vp]),
+    "pkv_accumulate_attention_weights": (C.c_int, [vp, vp, vp, vp, vp, i32, vp, i32, vp, vp, i32, i32,
+                                                   i32, i32, i32, i32, i64, f32, f32, vp, vp]),
+    "pkv_select_rows": (C.c_int, [vp, vp, vp, i32, vp, i32, i32, i32, i64, i32, i32, i32, vp, vp]),
+    "pkv_compact_rows": (C.c_int, [vp, vp, vp, i32, vp, i32, vp, i32, vp, i32, i32, i32, i32, i64, vp,
+                                   vp]),
     "pkv_num_skipped_tokens": (i64, [i64, i64]),
     "pkv_build_block_table": (C.c_int, [vp, vp, i32, i32, i32, i32, vp]),
     "pkv_build_block_table_arange": (C.c_int, [i32, i32, vp]),

@@ -8,6 +8,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes as C
+import math
 from array import array
 
 import numpy as np
@@ -1032,6 +1033,158 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, block_table, seq_lens, bl
         K, B, Q, H, hkv, d, bs, nb, float(scale), workspace.data_ptr(), ws_bytes, _ptr(dev_status),
         raw), "pkv_paged_attention_decode_sparse")
     return out
+
+
+KEYS_BF16, KEYS_FP8, KEYS_FP4 = 0, 1, 2  # PKV_KEYS_*
+
+
+def accumulate_attention_weights(weights, q, lse, k_cache, block_table, seq_lens, num_fresh,
+                                 scale: float, k_scale=None, decay: float = 1.0, dev_status=None,
+                                 stream=None) -> None:
+    """Add the attention that a step's queries pay to each cached row to the row's running sum.
+
+    weights [nb, H_kv, bs] fp32, updated; q [B, H, d] or [B, q_len, H, d] and lse, the
+    log-sum-exps that the step's attention returned for them; keys in a bf16 cache
+    [nb, bs, H_kv, d], an FP8 one (uint8 with fp32 k_scale) or a 4-bit one (uint8 codes with
+    uint8 k_scale). The newest num_fresh[b] rows of a sequence start over at zero, the others'
+    sums are multiplied by `decay` first."""
+    B, Q, H, d = _query_rows(q)
+    _f32_dev(weights, "weights")
+    _f32_dev(lse, "lse")
+    check_shape(lse, tuple(q.shape[:-1]), "lse")
+    if k_scale is None:
+        _dev_bf16(k_cache, "k_cache")
+        fmt = KEYS_BF16
+        nb, bs, hkv, dk = _cache_dims(k_cache, "k_cache")
+    elif isinstance(k_scale, torch.Tensor) and k_scale.dtype == torch.uint8:
+        nb, hkv, bs = _fp4_cache(k_cache, None, k_scale, None)
+        fmt, dk = KEYS_FP4, 128
+    else:
+        _fp8_cache(k_cache, "k_cache")
+        _f32_dev(k_scale, "k_scale")
+        fmt = KEYS_FP8
+        nb, bs, hkv, dk = _cache_dims(k_cache, "k_cache")
+        check_shape(k_scale, (nb, hkv, bs), "k_scale")
+    if dk != d:
+        raise ValueError(f"k_cache head_dim {dk} differs from q's {d}")
+    check_shape(weights, (nb, hkv, bs), "weights")
+    _table_and_lens(block_table, seq_lens, B)
+    _dev_i32(num_fresh, "num_fresh")
+    check_shape(num_fresh, (B,), "num_fresh")
+    index = q.get_device()
+    _check_gpu(index, weights=weights, lse=lse, k_cache=k_cache, k_scale=k_scale,
+               block_table=block_table, seq_lens=seq_lens, num_fresh=num_fresh)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, q.device)
+    if Q == 0:
+        return
+    check(load().pkv_accumulate_attention_weights(
+        weights.data_ptr(), q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(), _ptr(k_scale), fmt,
+        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), num_fresh.data_ptr(), B, Q,
+        H, hkv, d, bs, nb, float(scale), float(decay), _ptr(dev_status), raw),
+        "pkv_accumulate_attention_weights")
+
+
+def select_rows(weights, block_table, seq_lens, num_keep: int, num_sink: int = 0,
+                num_recent: int = 0, out=None, dev_status=None, stream=None):
+    """The num_keep rows of each sequence and kv head with the largest weights.
+
+    weights [nb, H_kv, bs] fp32 (accumulate_attention_weights); returns int32
+    [B, H_kv, num_keep] (`out` if given): positions, ascending, -1 behind the last of a sequence
+    with fewer rows. The first num_sink and the last num_recent positions are always among
+    them."""
+    _f32_dev(weights, "weights")
+    if weights.dim() != 3:
+        raise ValueError("weights must be [num_blocks, H_kv, block_size]")
+    nb, hkv, bs = weights.shape
+    _dev_i32(seq_lens, "seq_lens")
+    B = seq_lens.numel()
+    _table_and_lens(block_table, seq_lens, B)
+    num_keep = _int32(num_keep, "num_keep")
+    num_sink, num_recent = _int32(num_sink, "num_sink"), _int32(num_recent, "num_recent")
+    if num_keep < 1:
+        raise ValueError("num_keep must be positive")
+    shape = (B, hkv, num_keep)
+    if out is None:
+        out = _empty(shape, torch.int32, weights.device, stream)
+    else:
+        _dev_i32(out, "out")
+        check_shape(out, shape, "out")
+    index = weights.get_device()
+    _check_gpu(index, block_table=block_table, seq_lens=seq_lens, out=out)
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, weights.device)
+    check(load().pkv_select_rows(
+        out.data_ptr(), weights.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+        seq_lens.data_ptr(), B, hkv, bs, nb, num_keep, num_sink, num_recent, _ptr(dev_status), raw),
+        "pkv_select_rows")
+    return out
+
+
+def compact_rows(kept, block_table, row_caches=(), head_caches=(), new_block_table=None,
+                 dev_status=None, stream=None) -> None:
+    """Move the kept rows of each sequence and kv head to the front of the sequence, in order.
+
+    kept [B, H_kv, K] int32, ascending, negative entries behind the last (select_rows). The
+    caches are contiguous CUDA tensors of any type, row_caches [nb, bs, H_kv, ...] and
+    head_caches [nb, H_kv, bs, ...]; row i becomes what row kept[i] was, in place or, with
+    new_block_table [B, blocks], in that table's blocks. The sequence then has as many rows as
+    were kept; rows behind them stay as they were."""
+    caches = [*row_caches, *head_caches]
+    if not caches:
+        raise ValueError("compact_rows needs at least one cache")
+    _dev_i32(kept, "kept")
+    if kept.dim() != 3:
+        raise ValueError("kept must be [B, H_kv, num_keep]")
+    B, hkv, K = kept.shape
+    if K < 1:
+        raise ValueError("num_keep must be positive")
+    nb = bs = None
+    data, sizes = [], []
+    for i, t in enumerate(caches):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
+            raise ValueError(f"cache {i} must be a contiguous CUDA tensor")
+        by_row = i < len(row_caches)
+        shape = t.shape
+        if len(shape) < 3 or shape[2 if by_row else 1] != hkv:
+            order = "[nb, bs, H_kv, ...]" if by_row else "[nb, H_kv, bs, ...]"
+            raise ValueError(f"cache {i} must be {order} with kept's {hkv} heads, "
+                             f"got {_shape_str(shape)}")
+        here = shape[0], shape[1 if by_row else 2]
+        if nb is None:
+            nb, bs = here
+        elif here != (nb, bs):
+            raise ValueError(f"cache {i} has {here[0]} blocks of {here[1]}, the first one {nb} of {bs}")
+        data.append(t.data_ptr())
+        # Bytes of one head's row (strides of axes of length one say nothing).
+        sizes.append(math.prod(shape[3:]) * t.element_size())
+    _dev_i32(block_table, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [B={B}, max_blocks_per_seq], "
+                         f"got {_shape_str(block_table.shape)}")
+    width = 0
+    if new_block_table is not None:
+        _dev_i32(new_block_table, "new_block_table")
+        if new_block_table.dim() != 2 or new_block_table.shape[0] != B:
+            raise ValueError(f"new_block_table must be [B={B}, blocks], "
+                             f"got {_shape_str(new_block_table.shape)}")
+        width = new_block_table.shape[1]
+        if B and K > width * bs:
+            raise ValueError(f"{K} rows do not fit in new_block_table's {width} blocks of {bs}")
+    index = kept.get_device()
+    _check_gpu(index, block_table=block_table, new_block_table=new_block_table,
+               **{f"cache {i}": t for i, t in enumerate(caches)})
+    raw = _launch_stream(index, stream)
+    if dev_status is not None:
+        status_buffer(dev_status, kept.device)
+    ptrs, rows = array("Q", data), array("i", sizes)
+    major = array("i", [0] * len(row_caches) + [1] * len(head_caches))
+    check(load().pkv_compact_rows(
+        ptrs.buffer_info()[0], rows.buffer_info()[0], major.buffer_info()[0], len(caches),
+        kept.data_ptr(), K, block_table.data_ptr(), block_table.shape[1], _ptr(new_block_table), width,
+        B, hkv, bs, nb, _ptr(dev_status), raw), "pkv_compact_rows")
 
 
 def prefill_workspace_size() -> int:

@@ -659,6 +659,160 @@ int pkv_update_block_summaries(void* summaries, const void* k_cache, const int32
   return launch_status(launch_block_summaries(a, (cudaStream_t)stream, current_num_sms()), what);
 }
 
+int pkv_accumulate_attention_weights(float* weights, const void* q, const float* lse,
+                                     const void* k_cache, const void* k_scale, int32_t key_format,
+                                     const int32_t* block_table, int32_t max_blocks_per_seq,
+                                     const int32_t* seq_lens, const int32_t* num_fresh, int32_t B,
+                                     int32_t q_len, int32_t H, int32_t H_kv, int32_t head_dim,
+                                     int32_t block_size, int64_t num_blocks, float scale,
+                                     float decay, int* dev_status, void* stream) {
+  const char* what = "pkv_accumulate_attention_weights";
+  PKV_REQUIRE(B >= 0 && q_len >= 1 && H > 0 && H_kv > 0 && max_blocks_per_seq > 0 && num_blocks > 0,
+              PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  PKV_REQUIRE(H % H_kv == 0, PKV_ERR_INVALID_ARG, "%s: H (%d) not a multiple of H_kv (%d)", what, H, H_kv);
+  PKV_REQUIRE(key_format == PKV_KEYS_BF16 || key_format == PKV_KEYS_FP8 || key_format == PKV_KEYS_FP4,
+              PKV_ERR_INVALID_ARG, "%s: bad key_format", what);
+  PKV_REQUIRE(head_dim == 128 && block_size == 128, PKV_ERR_UNSUPPORTED,
+              "%s: only head_dim 128 and block_size 128 are implemented", what);
+  PKV_REQUIRE(H / H_kv <= 16, PKV_ERR_UNSUPPORTED, "%s: H / H_kv = %d exceeds 16", what, H / H_kv);
+  PKV_REQUIRE(q_len <= (1 << 20), PKV_ERR_UNSUPPORTED, "%s: q_len too large", what);
+  PKV_REQUIRE(max_blocks_per_seq <= INT32_MAX / 128 && num_blocks * block_size <= INT32_MAX &&
+                  B <= INT32_MAX / H_kv,
+              PKV_ERR_UNSUPPORTED,
+              "%s: max_blocks_per_seq * 128, num_blocks * 128 and B * H_kv must fit in int32", what);
+  PKV_REQUIRE(std::isfinite(scale) && scale > 0.f, PKV_ERR_INVALID_ARG,
+              "%s: scale must be a positive finite number", what);
+  PKV_REQUIRE(decay >= 0.f && decay <= 1.f, PKV_ERR_INVALID_ARG, "%s: decay outside [0, 1]", what);
+  if (B == 0) return PKV_OK;
+  const bool scaled = key_format != PKV_KEYS_BF16;
+  PKV_REQUIRE(weights && q && lse && k_cache && block_table && seq_lens && num_fresh &&
+                  (scaled == (k_scale != nullptr)),
+              PKV_ERR_INVALID_ARG, "%s: null pointer, or k_scale where the format has none", what);
+  PKV_REQUIRE(aligned16(weights) && aligned16(q) && aligned16(k_cache) && aligned16(k_scale) &&
+                  (((uintptr_t)lse) & 3) == 0,
+              PKV_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  const int64_t rows = num_blocks * block_size * H_kv, queries = (int64_t)B * q_len * H;
+  auto reads = [&](const void* p, int64_t bytes) { return overlap(weights, rows * 4, p, bytes); };
+  PKV_REQUIRE(!reads(q, queries * 256) && !reads(lse, queries * 4) &&
+                  !reads(k_cache, rows * (key_format == PKV_KEYS_BF16 ? 256 : key_format == PKV_KEYS_FP8 ? 128 : 64)) &&
+                  !(scaled && reads(k_scale, rows * (key_format == PKV_KEYS_FP8 ? 4 : 8))) &&
+                  !reads(block_table, (int64_t)B * max_blocks_per_seq * 4) && !reads(seq_lens, B * (int64_t)4) &&
+                  !reads(num_fresh, B * (int64_t)4),
+              PKV_ERR_INVALID_ARG, "%s: weights overlaps an input", what);
+  WeightsArgs a = {};
+  a.weights = weights;
+  a.q = (const uint16_t*)q;
+  a.lse = lse;
+  a.k_cache = (const uint8_t*)k_cache;
+  a.k_scale = (const uint8_t*)k_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.num_fresh = num_fresh;
+  a.dev_status = dev_status;
+  a.num_blocks = num_blocks;
+  a.B = B;
+  a.q_len = q_len;
+  a.H = H;
+  a.Hkv = H_kv;
+  a.n_rep = H / H_kv;
+  a.max_blocks = max_blocks_per_seq;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.decay = decay;
+  clear_error();
+  return launch_status(launch_attn_weights(a, key_format, (cudaStream_t)stream, current_num_sms()), what);
+}
+
+int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_table,
+                    int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t B, int32_t H_kv,
+                    int32_t block_size, int64_t num_blocks, int32_t num_keep, int32_t num_sink,
+                    int32_t num_recent, int* dev_status, void* stream) {
+  const char* what = "pkv_select_rows";
+  PKV_REQUIRE(B >= 0 && H_kv > 0 && max_blocks_per_seq > 0 && num_blocks > 0 && num_keep >= 1 &&
+                  num_sink >= 0 && num_recent >= 0,
+              PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  PKV_REQUIRE(block_size == 128, PKV_ERR_UNSUPPORTED, "%s: only block_size 128 is implemented", what);
+  PKV_REQUIRE((int64_t)num_sink + num_recent <= num_keep, PKV_ERR_INVALID_ARG,
+              "%s: num_sink + num_recent exceeds num_keep", what);
+  PKV_REQUIRE(max_blocks_per_seq <= (INT32_MAX >> 1) / 128 && num_blocks * block_size <= INT32_MAX &&
+                  B <= INT32_MAX / H_kv,
+              PKV_ERR_UNSUPPORTED,
+              "%s: max_blocks_per_seq * 256, num_blocks * 128 and B * H_kv must fit in int32", what);
+  if (B == 0) return PKV_OK;
+  PKV_REQUIRE(kept && weights && block_table && seq_lens, PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+  PKV_REQUIRE(aligned16(weights) && aligned16(kept), PKV_ERR_INVALID_ARG,
+              "%s: pointers must be 16-byte aligned", what);
+  const int64_t bytes = (int64_t)B * H_kv * num_keep * 4;
+  PKV_REQUIRE(!overlap(kept, bytes, weights, num_blocks * H_kv * block_size * 4) &&
+                  !overlap(kept, bytes, block_table, (int64_t)B * max_blocks_per_seq * 4) &&
+                  !overlap(kept, bytes, seq_lens, (int64_t)B * 4),
+              PKV_ERR_INVALID_ARG, "%s: kept overlaps an input", what);
+  SelectRowsArgs a = {weights, block_table, seq_lens, kept, dev_status, num_blocks, B, H_kv, block_size,
+                      max_blocks_per_seq, num_keep, num_sink, num_recent};
+  clear_error();
+  return launch_status(launch_select_rows(a, (cudaStream_t)stream), what);
+}
+
+int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_t* head_major,
+                     int32_t num_caches, const int32_t* kept, int32_t num_keep,
+                     const int32_t* block_table, int32_t max_blocks_per_seq,
+                     const int32_t* new_block_table, int32_t new_max_blocks_per_seq, int32_t B,
+                     int32_t H_kv, int32_t block_size, int64_t num_blocks, int* dev_status,
+                     void* stream) {
+  const char* what = "pkv_compact_rows";
+  PKV_REQUIRE(B >= 0 && H_kv > 0 && max_blocks_per_seq > 0 && num_blocks > 0 && num_keep >= 1 &&
+                  block_size > 0 && num_caches >= 1,
+              PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+  PKV_REQUIRE(num_caches <= kCompactMaxCaches, PKV_ERR_UNSUPPORTED, "%s: more than %d caches", what,
+              kCompactMaxCaches);
+  PKV_REQUIRE(num_blocks * block_size <= INT32_MAX && B <= INT32_MAX / H_kv, PKV_ERR_UNSUPPORTED,
+              "%s: num_blocks * block_size and B * H_kv must fit in int32", what);
+  PKV_REQUIRE(!new_block_table || (new_max_blocks_per_seq > 0 &&
+                                   num_keep <= (int64_t)new_max_blocks_per_seq * block_size),
+              PKV_ERR_INVALID_ARG, "%s: num_keep rows do not fit in the new table", what);
+  if (B == 0) return PKV_OK;
+  PKV_REQUIRE(caches && row_bytes && head_major && kept && block_table, PKV_ERR_INVALID_ARG,
+              "%s: null pointer", what);
+  CompactArgs a = {};
+  const int64_t rows = num_blocks * block_size * H_kv;
+  auto reads = [&](const void* p, int64_t bytes) {
+    return overlap(p, bytes, kept, (int64_t)B * H_kv * num_keep * 4) ||
+           overlap(p, bytes, block_table, (int64_t)B * max_blocks_per_seq * 4) ||
+           (new_block_table &&
+            overlap(p, bytes, new_block_table, (int64_t)B * new_max_blocks_per_seq * 4));
+  };
+  for (int i = 0; i < num_caches; ++i) {
+    PKV_REQUIRE(caches[i], PKV_ERR_INVALID_ARG, "%s: null pointer", what);
+    PKV_REQUIRE(row_bytes[i] > 0 && row_bytes[i] % 4 == 0 && row_bytes[i] <= (1 << 20), PKV_ERR_UNSUPPORTED,
+                "%s: rows of %d bytes (a multiple of 4 up to 2^20 is implemented)", what, row_bytes[i]);
+    PKV_REQUIRE(aligned16(caches[i]), PKV_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
+    PKV_REQUIRE(!reads(caches[i], rows * row_bytes[i]), PKV_ERR_INVALID_ARG,
+                "%s: cache %d overlaps kept or a table", what, i);
+    for (int j = 0; j < i; ++j)
+      PKV_REQUIRE(!overlap(caches[i], rows * row_bytes[i], caches[j], rows * row_bytes[j]),
+                  PKV_ERR_INVALID_ARG, "%s: caches %d and %d overlap", what, j, i);
+    CompactCache& c = a.cache[i];
+    c.data = (uint8_t*)caches[i];
+    c.row_bytes = row_bytes[i];
+    c.block_stride = (int64_t)block_size * H_kv * row_bytes[i];
+    c.row_stride = head_major[i] ? row_bytes[i] : (int64_t)H_kv * row_bytes[i];
+    c.head_stride = head_major[i] ? (int64_t)block_size * row_bytes[i] : row_bytes[i];
+  }
+  a.kept = kept;
+  a.block_table = block_table;
+  a.new_table = new_block_table ? new_block_table : block_table;
+  a.dev_status = dev_status;
+  a.num_blocks = num_blocks;
+  a.B = B;
+  a.Hkv = H_kv;
+  a.block_size = block_size;
+  a.max_blocks = max_blocks_per_seq;
+  a.new_max_blocks = new_block_table ? new_max_blocks_per_seq : max_blocks_per_seq;
+  a.num_keep = num_keep;
+  a.num_caches = num_caches;
+  clear_error();
+  return launch_status(launch_compact_rows(a, (cudaStream_t)stream), what);
+}
+
 int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summaries,
                       const int32_t* block_table, int32_t max_blocks_per_seq,
                       const int32_t* seq_lens, int32_t B, int32_t q_len, int32_t H, int32_t H_kv,

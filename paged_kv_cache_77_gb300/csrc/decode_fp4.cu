@@ -27,6 +27,7 @@
 #include "launch.h"
 #include "mma_f16.cuh"
 #include "pdl.cuh"
+#include "query_f16.cuh"
 #include "row_cursor.cuh"
 #include "tc_ptx.cuh"
 
@@ -77,33 +78,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // loads then take four consecutive tokens, which lie in different banks.
 __device__ __forceinline__ int token_of(int r) { return (r >> 1) + ((r & 1) << 2); }
 
-// B operand of the scores for query row `x` (a lane's 32 consecutive channels, bf16; null: a
-// row of zeros) and the power of two that was taken out of it. Infinities and NaN pass through.
-__device__ __forceinline__ float load_query(const uint16_t* x, uint32_t (&r)[16]) {
-  uint32_t u[16];
+// A lane's 32 consecutive channels of a query row (null: a row of zeros) as fp16, and the power
+// of two that was taken out of the row.
+__device__ __forceinline__ float load_query(const uint16_t* x, uint4 (&w)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 w = x ? __ldg(reinterpret_cast<const uint4*>(x) + i) : make_uint4(0, 0, 0, 0);
-    u[4 * i] = w.x;
-    u[4 * i + 1] = w.y;
-    u[4 * i + 2] = w.z;
-    u[4 * i + 3] = w.w;
-  }
-  uint32_t top = 0;  // largest finite magnitude of the row, as bits
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t lo = u[i] << 16 & 0x7fffffffu, hi = u[i] & 0x7fff0000u;
-    if (lo < 0x7f800000u && lo > top) top = lo;
-    if (hi < 0x7f800000u && hi > top) top = hi;
-  }
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // Exponents of the factor that brings the largest magnitude to [2^8, 2^9), and of its inverse.
-  const int e = min(262 - (int)(top >> 23), 253);
-  const float up = __uint_as_float((uint32_t)e << 23), down = __uint_as_float((uint32_t)(254 - e) << 23);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = pack_f16(mul_ieee(bf16lo(u[i]), up), mul_ieee(bf16hi(u[i]), up));
-  return down;
+  for (int i = 0; i < 4; ++i) w[i] = x ? __ldg(reinterpret_cast<const uint4*>(x) + i) : make_uint4(0, 0, 0, 0);
+  return query_to_f16(w);
 }
 
 template <int NT>
@@ -186,7 +166,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) decode_fp4_kernel(const
   const int g = lane >> 2, c = lane & 3;
   const int tb = (warp & 7) * 16;  // this warp's tokens of a tile
   const int R = a.n_rep * a.q_len;
-  uint32_t qf[16];                 // NT == 1 only
+  uint4 qf[4];                     // NT == 1 only
   float f[NT][2], m[NT][2], o[NT][8][4], l[NT][4];
   int row_i[NT][2];                // query token of this lane's rows
 #pragma unroll
@@ -212,8 +192,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) decode_fp4_kernel(const
         if (warp < NT) {
           const float down = load_query(query(warp * 8 + g), qf);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sm.q[warp][i][lane] = make_uint4(qf[4 * i], qf[4 * i + 1], qf[4 * i + 2], qf[4 * i + 3]);
+          for (int i = 0; i < 4; ++i) sm.q[warp][i][lane] = qf[i];
           if (c == 0) sm.f[warp][g] = down * a.scale_log2;
         }
         tc::named_bar_sync(1, S::WARPS * 32);
@@ -283,7 +262,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) decode_fp4_kernel(const
             for (int n = 0; n < NT; ++n) {
               uint4 b;
               if constexpr (NT == 1)
-                b = make_uint4(qf[4 * i], qf[4 * i + 1], qf[4 * i + 2], qf[4 * i + 3]);
+                b = qf[i];
               else
                 b = sm.q[n][i][lane];
               mma_f16(s[n], y0[0], y1[0], y0[1], y1[1], b.x, b.y);

@@ -91,6 +91,54 @@ struct SelectArgs {
 };
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream, int num_sms);
 
+// Attention weights summed per cached row (attn_weights.cu).
+constexpr int kKeysBf16 = 0, kKeysFp8 = 1, kKeysFp4 = 2;  // PKV_KEYS_*
+constexpr int kWeightsMaxRows = 128;                       // query rows of one launch
+struct WeightsArgs {
+  float* weights;             // [nb, Hkv, 128]
+  const uint16_t* q;          // [B, q_len, H, 128] bf16
+  const float* lse;           // [B, q_len, H]
+  const uint8_t* k_cache;     // bf16 or E4M3 [nb, 128, Hkv, 128], or codes [nb, Hkv, 128, 64]
+  const uint8_t* k_scale;     // null, fp32 [nb, Hkv, 128], or bytes [nb, Hkv, 128, 8]
+  const int32_t* block_table; // [B, max_blocks]
+  const int32_t* seq_lens;    // [B]
+  const int32_t* num_fresh;   // [B]
+  int* dev_status;
+  int64_t num_blocks;
+  int B, q_len, H, Hkv, n_rep, max_blocks;
+  int row0, rows, start;      // query tokens of this launch; whether it is the first
+  float scale_log2, decay;
+};
+cudaError_t launch_attn_weights(WeightsArgs a, int format, cudaStream_t stream, int num_sms);
+
+// Eviction (evict.cu).
+struct SelectRowsArgs {
+  const float* weights;       // [nb, Hkv, bs]
+  const int32_t* block_table; // [B, max_blocks]
+  const int32_t* seq_lens;    // [B]
+  int32_t* out;               // [B, Hkv, num_keep]
+  int* dev_status;
+  int64_t num_blocks;
+  int B, Hkv, block_size, max_blocks, num_keep, num_sink, num_recent;
+};
+cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream);
+constexpr int kCompactMaxCaches = 16;
+struct CompactCache {
+  uint8_t* data;
+  int64_t block_stride, row_stride, head_stride;  // bytes
+  int row_bytes, vec, slice_bytes, slices;
+};
+struct CompactArgs {
+  CompactCache cache[kCompactMaxCaches];
+  const int32_t* kept;        // [B, Hkv, num_keep]
+  const int32_t* block_table; // [B, max_blocks]
+  const int32_t* new_table;   // [B, new_max_blocks]: block_table itself in place
+  int* dev_status;
+  int64_t num_blocks;
+  int B, Hkv, block_size, max_blocks, new_max_blocks, num_keep, num_caches;
+};
+cudaError_t launch_compact_rows(CompactArgs a, cudaStream_t stream);
+
 // Arguments of the split-KV decode kernels and their LSE merge.
 struct DecodeArgs {
   const uint16_t* q;          // [B, q_len, H, D] bf16
