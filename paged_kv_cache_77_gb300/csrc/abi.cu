@@ -749,7 +749,7 @@ int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_ta
   SelectRowsArgs a = {weights, block_table, seq_lens, kept, dev_status, num_blocks, B, H_kv, block_size,
                       max_blocks_per_seq, num_keep, num_sink, num_recent};
   clear_error();
-  return launch_status(launch_select_rows(a, (cudaStream_t)stream), what);
+  return launch_status(launch_select_rows(a, (cudaStream_t)stream, current_num_sms()), what);
 }
 
 int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_t* head_major,

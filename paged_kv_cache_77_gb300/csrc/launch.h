@@ -111,7 +111,7 @@ struct WeightsArgs {
 };
 cudaError_t launch_attn_weights(WeightsArgs a, int format, cudaStream_t stream, int num_sms);
 
-// Eviction (evict.cu).
+// Eviction (select_rows.cu, compact_rows.cu).
 struct SelectRowsArgs {
   const float* weights;       // [nb, Hkv, bs]
   const int32_t* block_table; // [B, max_blocks]
@@ -121,7 +121,7 @@ struct SelectRowsArgs {
   int64_t num_blocks;
   int B, Hkv, block_size, max_blocks, num_keep, num_sink, num_recent;
 };
-cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream);
+cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int num_sms);
 constexpr int kCompactMaxCaches = 16;
 struct CompactCache {
   uint8_t* data;
