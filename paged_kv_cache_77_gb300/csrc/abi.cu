@@ -180,7 +180,7 @@ int decode_setup(pkv::DecodeArgs& a, bool* empty, const char* what, void* out, i
   a.Hkv = H_kv;
   a.n_rep = n_rep;
   a.max_blocks = max_blocks_per_seq;
-  a.q_len = q_len;
+  a.q_len = a.q_total = q_len;
   a.row_window = window;
   a.window = window > 0 ? window + q_len - 1 : 0;
   a.out_f32 = out_dtype == PKV_F32;
@@ -573,10 +573,7 @@ int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, con
   a.k_scale4 = (const uint8_t*)k_scale;
   a.v_scale4 = (const uint8_t*)v_scale;
   clear_error();
-  cudaStream_t s = (cudaStream_t)stream;
-  const int rc = launch_status(launch_decode_fp4(a, s), "pkv_paged_attention_decode_fp4 (attention)");
-  if (rc != PKV_OK) return rc;
-  return launch_status(launch_decode_merge(a, s), "pkv_paged_attention_decode_fp4 (merge)");
+  return launch_status(launch_decode_fp4(a, (cudaStream_t)stream), what);
 }
 
 size_t pkv_decode_sparse_workspace_size(int32_t B, int32_t q_len, int32_t H, int32_t H_kv,

@@ -1,10 +1,11 @@
 // Split-KV decode over the 4-bit cache (fp4.cuh has the format).
 //
-// For each query row, o = softmax(scale q K^T) V over the row's visible positions. A CTA walks
-// its share of the (sequence, kv head, block) tiles; a tile is 18 KB in four contiguous pieces
-// (K codes, V codes, their scales) that one warp brings into a ring in shared memory with bulk
-// copies. Every consumer warp takes 16 tokens of a tile and keeps its own running maximum, sum
-// and output in registers; the warps meet once per segment.
+// For each query row, o = softmax(scale q K^T) V over the row's visible positions. A CTA has a
+// share of the (sequence, kv head, block) tiles, equal for all CTAs, and every warp of it an
+// equal run of that share in pieces of 32 tokens. A warp works alone: it brings its pieces into a
+// ring of its own in shared memory with asynchronous copies, keeps a running maximum, sum and output in registers, and writes what it
+// finishes. Only the segments that cross from warp to warp are joined, once, when the CTA's share
+// is done: the warp in which a segment starts adds up what the later ones left in shared memory.
 //
 // Both products run on mma.sync with the tokens (K) and the channels (V) as the 16 rows of A
 // and the query rows of the kv head as the 8 columns of B, so a group of 8 heads fills the
@@ -19,7 +20,8 @@
 // row's largest. Scores, maxima, sums and outputs are fp32. The weights exp(s - m) enter the
 // value product as fp16 (off by at most 2^-11 of themselves), scaled by 2^7 so that a weight keeps
 // its 11 bits down to 2^-21 of the largest and counts down to 2^-32; the same rounded weights
-// are summed (a row of ones as one more A operand) and divide the output.
+// are summed (a row of ones as one more A operand) and divide the output, so that a row of equal
+// values keeps its value. The log-sum-exp takes the sum of the unrounded ones.
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
@@ -29,44 +31,38 @@
 #include "pdl.cuh"
 #include "query_f16.cuh"
 #include "row_cursor.cuh"
-#include "tc_ptx.cuh"
 
+#ifndef XA
+#define XA 2
+#endif
 namespace pkv {
 namespace {
 
-constexpr int BS = 128, D = 128;
-constexpr int CODES = BS * fp4::kCodeBytes;    // 8192
-constexpr int SCALES = BS * fp4::kScaleBytes;  // 1024
-constexpr int STAGE = 2 * (CODES + SCALES);    // K codes, V codes, K scales, V scales
-constexpr int OPAD = 132;                      // floats per output row of a warp's partial
-constexpr float kShift = 7.f;                  // weights are 2^kShift exp(s - m)
-constexpr float kLazy = 8.f;                   // a maximum may be passed by this much (log2)
+constexpr int D = 128, TILE = 128, SUB = 32;     // tokens of a block, and of a piece of it
+constexpr int CODES = SUB * fp4::kCodeBytes;     // 2048
+constexpr int SCALES = SUB * fp4::kScaleBytes;   // 256
+constexpr int STAGE = 2 * (CODES + SCALES);      // K codes, V codes, K scales, V scales
+constexpr float kShift = 7.f;                    // weights are 2^kShift exp(s - m)
+constexpr float kLazy = 8.f;                     // a maximum may be passed by this much (log2)
 
+// NT: 8-row tiles of query rows.
 template <int NT>
 struct Shape {
-  static constexpr int WARPS = NT == 1 ? 16 : 8;  // consumer warps
-  static constexpr int GROUPS = WARPS / 8;        // tiles worked on at once
-  static constexpr int STAGES = 8;
-  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int WARPS = NT == 1 ? 16 : 8;
+  static constexpr int STAGES = NT == 1 ? 2 : 4;
+  static constexpr int AT_ONCE = XA;  // 16-token products side by side
 };
+
+enum : int { kNothing = 0, kGoesOn = 1, kEnds = 2 };  // what a warp left of its first segment
 
 template <int NT>
 struct Smem {
-  uint8_t stage[Shape<NT>::STAGES][STAGE];
-  float o[Shape<NT>::WARPS][8][OPAD];
-  float m[NT][Shape<NT>::WARPS][8], l[Shape<NT>::WARPS][8];
-  uint4 q[NT == 1 ? 1 : NT][4][32];     // B operands of the scores, for more than 8 rows
-  float f[NT][8];                       // score factor of each row
-  uint64_t full[Shape<NT>::STAGES], empty[Shape<NT>::STAGES];
-  int ok[Shape<NT>::STAGES];            // whether the tile's block exists
+  uint8_t stage[Shape<NT>::WARPS][Shape<NT>::STAGES][STAGE];
+  float4 o[Shape<NT>::WARPS][NT][8][32];      // a warp's part of a segment that an earlier one began
+  float stat[Shape<NT>::WARPS][NT][3][8];     // its maxima, sums, sums of the unrounded weights
+  int left[Shape<NT>::WARPS];
   int64_t total;
 };
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
@@ -74,32 +70,356 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// Row r (0..7) of a product's 8 rows is token token_of(r): lanes c and c + 4 of a quad's V
-// loads then take four consecutive tokens, which lie in different banks.
-__device__ __forceinline__ int token_of(int r) { return (r >> 1) + ((r & 1) << 2); }
+// Rows 2c and 2c + 1 of a product's 8 rows are tokens 0 3, 1 2, 4 7, 5 6 (and 8 further on): K's
+// 16-byte loads, 8 lanes at a time, then meet two rows of different banks, V's 8-byte loads rows
+// that share them by twos only.
+__device__ __forceinline__ int even_row(int c) { return (c & 1) | (c & 2) << 1; }
+__device__ __forceinline__ int token_of(int r) { return even_row(r >> 1) ^ ((r & 1) ? 3 : 0); }
 
-// A lane's 32 consecutive channels of a query row (null: a row of zeros) as fp16, and the power
-// of two that was taken out of the row.
-__device__ __forceinline__ float load_query(const uint16_t* x, uint4 (&w)[4]) {
+// A warp's walk over its run, segment by segment (a segment is the blocks that the rows of one
+// sequence and kv head see). The run is counted in pieces of 32 tokens of whole blocks; of the last
+// block only the pieces that hold tokens are visited.
+struct Walk {
+  int b, g, len;
+  int pos, stop;   // next position, and where the run leaves the segment or the tokens end
+  int todo;        // pieces of the run from this segment's first visit on
+  int padded;      // of them in this segment
+  bool ends;       // whether the segment's last token is in the run
+  __device__ __forceinline__ void enter(int at) {
+    const int end = (len + TILE - 1) & ~(TILE - 1);
+    pos = at;
+    padded = min((end - at) / SUB, todo);
+    ends = padded * SUB == end - at;
+    stop = min(at + padded * SUB, (len + SUB - 1) & ~(SUB - 1));
+  }
+  // The next segment of the run; false behind its end.
+  __device__ __forceinline__ bool next(const DenseRows& rows, int B, int Hkv) {
+    todo -= padded;
+    if (todo <= 0) return false;
+    if (++g == Hkv) {
+      g = 0;
+      do {
+        if (++b >= B) return false;
+        len = rows.len(b);
+      } while (len == 0);
+    }
+    enter(rows.blocks(len).jlo * TILE);
+    return true;
+  }
+};
+
+// A running softmax over part of a segment, spread over the lanes of a warp: lane 4 g + c has the
+// query rows 8 n + 2 c and 8 n + 2 c + 1 (x = 0, 1), of their outputs channels 16 g .. + 15
+// (o[n][d][x] and o[n][d][x + 2]: channels 16 g + 2 d and 16 g + 2 d + 1).
+template <int NT>
+struct Running {
+  float m[NT][2];        // maximum, log2
+  float l[NT][4];        // sum of the rounded weights ([2], [3]: copies)
+  float sum[NT][2];      // this lane's sum of the unrounded ones
+  float o[NT][8][4];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = x ? __ldg(reinterpret_cast<const uint4*>(x) + i) : make_uint4(0, 0, 0, 0);
-  return query_to_f16(w);
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      sum[n][0] = sum[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[n][i] = 0.f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][d][i] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void scale_row(int n, int x, float by) {
+    l[n][x] *= by;
+    sum[n][x] *= by;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      o[n][d][x] *= by;
+      o[n][d][x + 2] *= by;
+    }
+  }
+  __device__ __forceinline__ void sum_lanes() {  // every lane of a row gets the row's whole sum
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum[n][x] += __shfl_xor_sync(0xffffffffu, sum[n][x], d);
+  }
+};
+
+template <int NT>
+__device__ __forceinline__ void leave(Smem<NT>& sm, int warp, int lane, const Running<NT>& r) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) sm.o[warp][n][d][lane] = make_float4(r.o[n][d][0], r.o[n][d][1], r.o[n][d][2], r.o[n][d][3]);
+    if (lane < 4) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sm.stat[warp][n][0][2 * lane + x] = r.m[n][x];
+        sm.stat[warp][n][1][2 * lane + x] = r.l[n][x];
+        sm.stat[warp][n][2][2 * lane + x] = r.sum[n][x];
+      }
+    }
+  }
 }
 
 template <int NT>
-__global__ void __launch_bounds__(Shape<NT>::THREADS, 1) decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
-  using S = Shape<NT>;
+__device__ __forceinline__ void take(const Smem<NT>& sm, int warp, int lane, Running<NT>& r) {
+  const int c = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float by[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float other = sm.stat[warp][n][0][2 * c + x];
+      const float top = fmaxf(r.m[n][x], other);
+      // (A part without a finite score has sums of 0, or NaN, which any factor keeps.)
+      r.scale_row(n, x, r.m[n][x] == -INFINITY ? 1.f : exp2_approx(r.m[n][x] - top));
+      by[x] = other == -INFINITY ? 1.f : exp2_approx(other - top);
+      r.m[n][x] = top;
+      r.l[n][x] += sm.stat[warp][n][1][2 * c + x] * by[x];
+      r.sum[n][x] += sm.stat[warp][n][2][2 * c + x] * by[x];
+    }
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      const float4 v = sm.o[warp][n][d][lane];
+      r.o[n][d][0] += v.x * by[0];
+      r.o[n][d][1] += v.y * by[1];
+      r.o[n][d][2] += v.z * by[0];
+      r.o[n][d][3] += v.w * by[1];
+    }
+  }
+}
+
+// Writes a segment's rows, or a part of them (slot >= 0) to the workspace.
+template <int NT>
+__device__ __forceinline__ void put(const DecodeArgs& a, const Running<NT>& r, int lane, int b, int kv, int64_t slot) {
+  const int g = lane >> 2, c = lane & 3, R = a.n_rep * a.q_len;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = 8 * n + 2 * c + x;
+      if (row >= R) continue;
+      // A sum that is not a number (a NaN score) makes the row's output and lse NaN.
+      const bool none = r.l[n][x] == 0.f;
+      const float inv = none ? 0.f : 1.f / r.l[n][x];
+      const float lse2 = none ? -INFINITY : r.m[n][x] + log2f(r.sum[n][x]) - kShift;
+      float v[16];
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        v[2 * d] = r.o[n][d][x] * inv;
+        v[2 * d + 1] = r.o[n][d][x + 2] * inv;
+      }
+      const int64_t at = slot >= 0 ? slot * R + row
+                                   : ((int64_t)b * a.q_total + a.row0 + row / a.n_rep) * a.H +
+                                         (int64_t)kv * a.n_rep + row % a.n_rep;
+      if (slot >= 0 || a.out_f32) {
+        float4* dst = reinterpret_cast<float4*>((slot >= 0 ? a.ws_o : reinterpret_cast<float*>(a.out)) + at * D + 16 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at * D + 16 * g);
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      if (g == 0) {
+        if (slot >= 0)
+          a.ws_lse[at] = lse2;
+        else if (a.lse)
+          a.lse[at] = lse2 * kLn2;
+      }
+    }
+}
+
+// What the query rows of a launch see of a sequence: row i (of the call's) the positions in
+// (first + i - window, first + i].
+struct Sight {
+  int first, window, row0, rows;
+  __device__ __forceinline__ bool sees(int pos, int i) const {
+    return pos <= first + i && (window <= 0 || pos > first + i - window);
+  }
+  __device__ __forceinline__ bool any(int pos) const {  // of the launch's rows
+    return pos <= first + row0 + rows - 1 && (window <= 0 || pos > first + row0 - window);
+  }
+  __device__ __forceinline__ bool all(int lo, int hi) const {  // every row every position of [lo, hi]
+    return hi <= first + row0 && (window <= 0 || lo > first + row0 + rows - 1 - window);
+  }
+};
+
+// N times 16 tokens, from position p0 on, whose codes and scales lie at kc, vc, ks and vs in shared
+// memory. kMask: some row may not see some of them.
+template <int NT, int N, bool kMask>
+__device__ __forceinline__ void attend(Running<NT>& r, const uint4 (&qf)[NT][4], const float (&f)[NT][2],
+                                       float (&limit)[NT][2], float (&shift)[NT][2],
+                                       const int (&row_i)[NT][2], const uint8_t* kc, const uint8_t* vc,
+                                       const uint8_t* ks, const uint8_t* vs, int p0, const Sight& sight,
+                                       int g, int c) {
+  // ---- scores: 16 tokens x 8 NT query rows at a time
+  float s[N][NT][4];
+#pragma unroll
+  for (int h = 0; h < N; ++h) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[h][n][i] = 0.f;
+    const int r0 = 16 * h + token_of(g);
+    const uint4 w0 = *reinterpret_cast<const uint4*>(kc + r0 * fp4::kCodeBytes + 16 * c);
+    const uint4 w1 = *reinterpret_cast<const uint4*>(kc + (r0 + 8) * fp4::kCodeBytes + 16 * c);
+    const uint32_t e0 = *reinterpret_cast<const uint16_t*>(ks + r0 * fp4::kScaleBytes + 2 * c);
+    const uint32_t e1 = *reinterpret_cast<const uint16_t*>(ks + (r0 + 8) * fp4::kScaleBytes + 2 * c);
+    const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t sc0 = i < 2 ? fp4::scale_dup0(e0) : fp4::scale_dup1(e0);
+      const uint32_t sc1 = i < 2 ? fp4::scale_dup0(e1) : fp4::scale_dup1(e1);
+      uint32_t y0[4], y1[4];
+      fp4::widen(x0[i], y0);
+      fp4::widen(x1[i], y1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        y0[k] = fp4::mul2(y0[k], sc0);
+        y1[k] = fp4::mul2(y1[k], sc1);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_f16(s[h][n], y0[0], y1[0], y0[1], y1[1], qf[n][i].x, qf[n][i].y);
+        mma_f16(s[h][n], y0[2], y1[2], y0[3], y1[3], qf[n][i].z, qf[n][i].w);
+      }
+    }
+  }
+  // ---- running maxima, raised only when a score passes one by 2^kLazy (limit: that score)
+  bool past = false;
+  bool seen[N][NT][4];
+  float top[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      top[n][x] = -INFINITY;
+#pragma unroll
+      for (int h = 0; h < N; ++h)
+#pragma unroll
+        for (int i = x; i < 4; i += 2) {
+          seen[h][n][i] = !kMask || sight.sees(p0 + 16 * h + token_of(g) + (i >> 1) * 8, row_i[n][x]);
+          top[n][x] = fmaxf(top[n][x], seen[h][n][i] ? s[h][n][i] : -INFINITY);
+        }
+      past = past || top[n][x] > limit[n][x];
+    }
+  if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float t = top[n][x] == -INFINITY ? -INFINITY : top[n][x] * f[n][x];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+        t = fmaxf(r.m[n][x], t);
+        r.scale_row(n, x, r.m[n][x] == -INFINITY ? 1.f : exp2_approx(r.m[n][x] - t));
+        r.m[n][x] = t;
+        if (t > -INFINITY) {
+          limit[n][x] = (t + kLazy) / f[n][x];
+          shift[n][x] = kShift - t;
+        }
+      }
+  }
+  // ---- weights, transposed into the B operand of the value product
+  uint32_t pb[N][NT][2];
+#pragma unroll
+  for (int h = 0; h < N; ++h)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = seen[h][n][i] ? exp2_approx(fmaf(s[h][n][i], f[n][i & 1], shift[n][i & 1])) : 0.f;
+        r.sum[n][i & 1] += p[i];
+      }
+      pb[h][n][0] = transpose8(pack_f16(p[0], p[1]));
+      pb[h][n][1] = transpose8(pack_f16(p[2], p[3]));
+    }
+  // ---- values: of each 16 tokens the four of rows 2c, 2c + 1, 2c + 8, 2c + 9; channels 16 g .. + 15
+  const int even = even_row(c);
+#pragma unroll
+  for (int h = 0; h < N; ++h) {
+    uint2 w[4];
+    uint32_t e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * h + (even ^ (i & 1 ? 3 : 0)) + (i & 2) * 4;
+      w[i] = *reinterpret_cast<const uint2*>(vc + t * fp4::kCodeBytes + 8 * g);
+      e[i] = vs[t * fp4::kScaleBytes + g];
+    }
+    uint32_t poison = 0;
+    if (kMask) {
+      // A token that no row sees may hold any bytes, and 0 times NaN is NaN: its scales become zero.
+      // So do those past the largest of a token that some rows see; the rows that do see it get their
+      // NaN below.
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = (even ^ (i & 1 ? 3 : 0)) + (i & 2) * 4;
+        const bool by_some = sight.any(p0 + 16 * h + t);
+        if (by_some && e[i] > (uint32_t)fp4::kMaxScale) poison |= 1u << t;
+        if (!by_some || e[i] > (uint32_t)fp4::kMaxScale) e[i] = 0;
+      }
+    }
+    const uint32_t sa = fp4::scale_pair(e[0], e[1]), sb = fp4::scale_pair(e[2], e[3]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t x0 = k ? w[0].y : w[0].x, x1 = k ? w[1].y : w[1].x;
+      const uint32_t x2 = k ? w[2].y : w[2].x, x3 = k ? w[3].y : w[3].x;
+      constexpr uint32_t lo = 0x0f0f0f0fu, hi = 0xf0f0f0f0u;
+      uint32_t a0[4], a1[4], a2[4], a3[4];
+      fp4::widen((x0 & lo) | (x1 << 4 & hi), a0);  // even channels
+      fp4::widen((x0 >> 4 & lo) | (x1 & hi), a1);  // odd ones
+      fp4::widen((x2 & lo) | (x3 << 4 & hi), a2);
+      fp4::widen((x2 >> 4 & lo) | (x3 & hi), a3);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t y0 = fp4::mul2(a0[d], sa), y1 = fp4::mul2(a1[d], sa);
+        const uint32_t y2 = fp4::mul2(a2[d], sb), y3 = fp4::mul2(a3[d], sb);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(r.o[n][4 * k + d], y0, y1, y2, y3, pb[h][n][0], pb[h][n][1]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      mma_f16(r.l[n], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[h][n][0], pb[h][n][1]);
+    if (kMask) {
+      poison |= __shfl_xor_sync(0xffffffffu, poison, 1);
+      poison |= __shfl_xor_sync(0xffffffffu, poison, 2);
+      for (; poison; poison &= poison - 1) {
+        const int pos = p0 + 16 * h + __ffs((int)poison) - 1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!sight.sees(pos, row_i[n][x])) continue;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) r.o[n][d][x] = r.o[n][d][x + 2] = __uint_as_float(0x7fc00000u);
+          }
+      }
+    }
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int WARPS = Shape<NT>::WARPS, STAGES = Shape<NT>::STAGES, AT_ONCE = Shape<NT>::AT_ONCE;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<NT>& sm = *reinterpret_cast<Smem<NT>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const DenseRows rows = {a.seq_lens, BS, a.window, a.max_blocks * BS};
-  if (tid == 0) {
-    for (int i = 0; i < S::STAGES; ++i) {
-      tc::mbar_init(smem_u32(&sm.full[i]), 1);
-      tc::mbar_init(smem_u32(&sm.empty[i]), 8);
-    }
-    tc::fence_mbar_init();
-  }
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform, and known to be)
+  const DenseRows rows = {a.seq_lens, TILE, a.window, a.max_blocks * TILE};
   pdl_wait_then_launch();
   if (warp == 0) {
     const int64_t tot = total_live_blocks(rows, a.B, a.dev_status);
@@ -109,351 +429,171 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1) decode_fp4_kernel(const
   const int64_t T = sm.total, G = gridDim.x;
   const int64_t t0 = cta_tile_start(blockIdx.x, T, G), t1 = cta_tile_start(blockIdx.x + 1, T, G);
   if (t0 >= t1) return;
-  TileCursor cur;
-  cursor_seek_warp(cur, rows, a.B, a.Hkv, t0, t1);
 
-  if (warp == S::WARPS) {
-    // ---------------------------------------------------------------- producer
-    int ids = 0, ids_b = -1, ids_j = 0;  // 32 table entries of sequence ids_b, from ids_j on
-    int it = 0;
-    bool alive = true;
-    do {
-      const int st = it % S::STAGES;
-      if (cur.b != ids_b || cur.j < ids_j || cur.j >= ids_j + 32) {
-        ids_b = cur.b;
-        ids_j = cur.j;
-        ids = cur.j + lane < cur.n
-                  ? __ldg(a.block_table + (int64_t)cur.b * a.max_blocks + cur.jlo + cur.j + lane)
-                  : 0;
-      }
-      const int blk = __shfl_sync(0xffffffffu, ids, cur.j - ids_j);
-      const bool ok = blk >= 0 && (int64_t)blk < a.num_blocks;
-      if (!ok && lane == 0) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
-      if (it >= S::STAGES) alive = tc::mbar_wait_sleepy(smem_u32(&sm.empty[st]), (it / S::STAGES - 1) & 1);
-      if (!__all_sync(0xffffffffu, alive)) break;
-      const uint32_t full = smem_u32(&sm.full[st]);
-      // Rows behind the sequence's end stay where they are (an even number is copied: 16 bytes
-      // of scales are two rows).
-      const int live = min(BS, (cur.len - (cur.jlo + cur.j) * BS + 1) & ~1);
-      if (lane == 0) {
-        sm.ok[st] = ok;
-        tc::mbar_expect_tx(full, ok ? (uint32_t)live * 2 * (fp4::kCodeBytes + fp4::kScaleBytes) : 0u);
-      }
-      __syncwarp();
-      if (ok && lane < 4) {
-        const int64_t row = ((int64_t)blk * a.Hkv + cur.g) * BS;
-        const uint32_t dst = smem_u32(sm.stage[st]);
-        if (lane < 2)
-          bulk_load(dst + lane * CODES, (lane ? a.v_cache : a.k_cache) + row * fp4::kCodeBytes,
-                    live * fp4::kCodeBytes, full);
-        else
-          bulk_load(dst + 2 * CODES + (lane - 2) * SCALES,
-                    (lane == 3 ? a.v_scale4 : a.k_scale4) + row * fp4::kScaleBytes,
-                    live * fp4::kScaleBytes, full);
-      }
-      ++it;
-    } while (cursor_next(cur, rows, a.B, a.Hkv));
-    if (!__all_sync(0xffffffffu, alive)) {
-      if (lane == 0) flag_status(a.dev_status, PKV_DEV_TIMEOUT);
-      // Nothing may land in shared memory after the block has gone.
-      for (int i = it > S::STAGES ? it - S::STAGES : 0; i < it; ++i)
-        tc::mbar_wait_sleepy(smem_u32(&sm.full[i % S::STAGES]), (i / S::STAGES) & 1);
+  // This warp's run: pieces u0 .. u1 - 1 of the CTA's.
+  constexpr int PER = TILE / SUB;
+  const int64_t u0 = (t1 - t0) * PER * warp / WARPS, u1 = (t1 - t0) * PER * (warp + 1) / WARPS;
+  const int g = lane >> 2, c = lane & 3, R = a.n_rep * a.q_len;
+  Running<NT> r;
+  Walk cur = {};
+  bool begun = false;  // whether the segment that the warp is in began in its run
+  bool open = false;   // whether it goes on behind the run, and is this warp's to finish
+  int left = kNothing;
+  if (u0 < u1) {
+    {
+      TileCursor t;
+      cursor_seek_warp(t, rows, a.B, a.Hkv, t0 + u0 / PER, t1);
+      cur.b = t.b;
+      cur.g = t.g;
+      cur.len = t.len;
+      cur.todo = (int)(u1 - u0);
+      begun = t.j == 0 && u0 % PER == 0;
+      cur.enter((t.jlo + t.j) * TILE + (int)(u0 % PER) * SUB);
     }
-    return;
-  }
-
-  // ------------------------------------------------------------------ consumers
-  const int g = lane >> 2, c = lane & 3;
-  const int tb = (warp & 7) * 16;  // this warp's tokens of a tile
-  const int R = a.n_rep * a.q_len;
-  uint4 qf[4];                     // NT == 1 only
-  float f[NT][2], m[NT][2], o[NT][8][4], l[NT][4];
-  int row_i[NT][2];                // query token of this lane's rows
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) row_i[n][x] = min(n * 8 + 2 * c + x, R - 1) / a.n_rep;
-  int64_t piece_first = t0;
-  int it = 0;
-  bool dead = false;
-  for (;;) {
-    if (cur.t == t0 || cur.j == 0) {
-      piece_first = cur.t;
-      auto query = [&](int r) {
-        return r < R ? a.q + (((int64_t)cur.b * a.q_len + r / a.n_rep) * a.H + (int64_t)cur.g * a.n_rep +
-                              r % a.n_rep) * D + 32 * c
-                     : nullptr;
-      };
-      if constexpr (NT == 1) {
-        const float down = load_query(query(g), qf) * a.scale_log2;
-        f[0][0] = __shfl_sync(0xffffffffu, down, 8 * c);
-        f[0][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
-      } else {
-        if (warp < NT) {
-          const float down = load_query(query(warp * 8 + g), qf);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sm.q[warp][i][lane] = qf[i];
-          if (c == 0) sm.f[warp][g] = down * a.scale_log2;
-        }
-        tc::named_bar_sync(1, S::WARPS * 32);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          f[n][0] = sm.f[n][2 * c];
-          f[n][1] = sm.f[n][2 * c + 1];
-        }
+    // ---- the ring: the run's it-th visited piece is in stage it % STAGES, one group of
+    // asynchronous copies each. A lane copies 16 bytes of every eighth row of the codes, and 16 bytes
+    // of the scales of K (lanes 0 to 15) or V.
+    Walk ahead = cur;
+    bool more = true;
+    int ids = 0, ids_j = -64;  // 32 table entries of the sequence, from block ids_j on
+    bool enter = true;         // whether the piece's block has to be looked up
+    const uint8_t *k_src = nullptr, *v_src = nullptr, *s_src = nullptr;
+    unsigned bad = 0;          // stages whose block does not exist
+    const uint32_t ring = smem_u32(sm.stage[warp]) + 16 * lane;
+    auto issue = [&](int st) {
+      while (more && ahead.pos >= ahead.stop) {
+        const int b = ahead.b;
+        more = ahead.next(rows, a.B, a.Hkv);
+        if (ahead.b != b) ids_j = -64;
+        enter = true;
       }
+      if (more) {
+        if (enter || ahead.pos % TILE == 0) {
+          enter = false;
+          const int j = ahead.pos / TILE;
+          if ((unsigned)(j - ids_j) >= 32u) {
+            ids_j = j;
+            ids = (j + lane) * TILE < ahead.len ? __ldg(a.block_table + (int64_t)ahead.b * a.max_blocks + j + lane) : 0;
+          }
+          const int blk = __shfl_sync(0xffffffffu, ids, j - ids_j);
+          const bool ok = blk >= 0 && (int64_t)blk < a.num_blocks;
+          if (!ok && lane == 0) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+          const int64_t row = ((int64_t)(ok ? blk : 0) * a.Hkv + ahead.g) * TILE + ahead.pos % TILE;
+          k_src = ok ? a.k_cache + row * fp4::kCodeBytes + 16 * lane : nullptr;
+          v_src = a.v_cache + row * fp4::kCodeBytes + 16 * lane;
+          s_src = (lane < 16 ? a.k_scale4 : a.v_scale4) + row * fp4::kScaleBytes + 16 * (lane & 15);
+        }
+        const uint32_t dst = ring + st * STAGE;
+        if (k_src != nullptr) {
+          bad &= ~(1u << st);
+          if (ahead.len - ahead.pos >= SUB) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l[n][i] = 0.f;
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[n][x][i] = 0.f;
-      }
-    }
-
-    if (S::GROUPS == 1 || (it % S::GROUPS) == (warp >> 3)) {
-      const int st = it % S::STAGES;
-      if (!dead && !tc::mbar_wait(smem_u32(&sm.full[st]), (it / S::STAGES) & 1)) {
-        dead = true;
-        flag_status(a.dev_status, PKV_DEV_TIMEOUT);
-      }
-      dead = __any_sync(0xffffffffu, dead);
-      const int p0 = (cur.jlo + cur.j) * BS + tb;  // position of this warp's first token
-      // Positions that the query rows see: row i those in (first + i - window, first + i].
-      const int first = cur.len - a.q_len;
-      const int low = a.row_window > 0 ? max(first - a.row_window + 1, 0) : 0;  // of row 0
-      if (!dead && sm.ok[st] && p0 < cur.len && p0 + 15 >= low) {
-        const uint8_t* kc = sm.stage[st] + tb * fp4::kCodeBytes;
-        const uint8_t* vc = kc + CODES;
-        const uint8_t* ks = sm.stage[st] + 2 * CODES + tb * fp4::kScaleBytes;
-        const uint8_t* vs = ks + SCALES;
-        // Whether every query row sees all 16 tokens.
-        const bool inside = p0 + 15 <= first && (a.row_window <= 0 || p0 >= cur.len - a.row_window);
-
-        // ---- scores: 16 tokens x 8 NT query rows
-        float s[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-        {
-          const int r0 = token_of(g);
-          const uint4 w0 = *reinterpret_cast<const uint4*>(kc + r0 * fp4::kCodeBytes + 16 * c);
-          const uint4 w1 = *reinterpret_cast<const uint4*>(kc + (r0 + 8) * fp4::kCodeBytes + 16 * c);
-          const uint32_t u0 = *reinterpret_cast<const uint16_t*>(ks + r0 * fp4::kScaleBytes + 2 * c);
-          const uint32_t u1 = *reinterpret_cast<const uint16_t*>(ks + (r0 + 8) * fp4::kScaleBytes + 2 * c);
-          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t sc0 = i < 2 ? fp4::scale_dup0(u0) : fp4::scale_dup1(u0);
-            const uint32_t sc1 = i < 2 ? fp4::scale_dup0(u1) : fp4::scale_dup1(u1);
-            uint32_t y0[4], y1[4];
-            fp4::widen(x0[i], y0);
-            fp4::widen(x1[i], y1);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              y0[h] = fp4::mul2(y0[h], sc0);
-              y1[h] = fp4::mul2(y1[h], sc1);
+            for (int i = 0; i < 4; ++i) {
+              cp_async_16(dst + 512 * i, k_src + 512 * i, 16);
+              cp_async_16(dst + CODES + 512 * i, v_src + 512 * i, 16);
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              uint4 b;
-              if constexpr (NT == 1)
-                b = qf[i];
-              else
-                b = sm.q[n][i][lane];
-              mma_f16(s[n], y0[0], y1[0], y0[1], y1[1], b.x, b.y);
-              mma_f16(s[n], y0[2], y1[2], y0[3], y1[3], b.z, b.w);
-            }
-          }
-        }
-        const int pa = p0 + token_of(g);  // position of s[.][0..1]; s[.][2..3] is 8 further
-        bool past = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float& x = s[n][i];
-            x *= f[n][i & 1];
-            if (!inside) {
-              const int pos = pa + (i >> 1) * 8, at = first + row_i[n][i & 1];
-              if (pos > at || (a.row_window > 0 && pos <= at - a.row_window)) x = -INFINITY;
-            }
-            past |= x > m[n][i & 1] + kLazy;
-          }
-        // ---- running maxima, raised only when a score passes one by 2^kLazy
-        if (__any_sync(0xffffffffu, past)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float t = fmaxf(s[n][x], s[n][x + 2]);
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-              const float top = fmaxf(m[n][x], t);
-              const float scale = m[n][x] == -INFINITY ? 0.f : exp2_approx(m[n][x] - top);
-              m[n][x] = top;
-              l[n][x] *= scale;
-#pragma unroll
-              for (int d = 0; d < 8; ++d) {
-                o[n][d][x] *= scale;
-                o[n][d][x + 2] *= scale;
-              }
-            }
-        }
-        // ---- weights, transposed into the B operand of the value product
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float base[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) base[x] = m[n][x] == -INFINITY ? 0.f : m[n][x] - kShift;
-          pb[n][0] = transpose8(pack_f16(exp2_approx(s[n][0] - base[0]), exp2_approx(s[n][1] - base[1])));
-          pb[n][1] = transpose8(pack_f16(exp2_approx(s[n][2] - base[0]), exp2_approx(s[n][3] - base[1])));
-        }
-        // ---- values: tokens c, c + 4, c + 8, c + 12; channels 16 g .. 16 g + 15
-        uint2 w[4];
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = *reinterpret_cast<const uint2*>(vc + (c + 4 * i) * fp4::kCodeBytes + 8 * g);
-          u[i] = vs[(c + 4 * i) * fp4::kScaleBytes + g];
-        }
-        uint32_t poison = 0;
-        if (!inside) {
-          // A token that no row sees may hold any bytes, and 0 times NaN is NaN: its scales become
-          // zero. So do those past the largest of a token that some rows see; the rows that do see
-          // it get their NaN below.
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int pos = p0 + c + 4 * i;
-            const bool seen = pos < cur.len && pos >= low;
-            if (seen && u[i] > (uint32_t)fp4::kMaxScale) poison |= 1u << (c + 4 * i);
-            if (!seen || u[i] > (uint32_t)fp4::kMaxScale) u[i] = 0;
-          }
-        }
-        const uint32_t sa = fp4::scale_pair(u[0], u[1]), sb = fp4::scale_pair(u[2], u[3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t x0 = h ? w[0].y : w[0].x, x1 = h ? w[1].y : w[1].x;
-          const uint32_t x2 = h ? w[2].y : w[2].x, x3 = h ? w[3].y : w[3].x;
-          constexpr uint32_t lo = 0x0f0f0f0fu, hi = 0xf0f0f0f0u;
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          fp4::widen((x0 & lo) | (x1 << 4 & hi), a0);  // even channels
-          fp4::widen((x0 >> 4 & lo) | (x1 & hi), a1);  // odd ones
-          fp4::widen((x2 & lo) | (x3 << 4 & hi), a2);
-          fp4::widen((x2 >> 4 & lo) | (x3 & hi), a3);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const uint32_t y0 = fp4::mul2(a0[d], sa), y1 = fp4::mul2(a1[d], sa);
-            const uint32_t y2 = fp4::mul2(a2[d], sb), y3 = fp4::mul2(a3[d], sb);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * h + d], y0, y1, y2, y3, pb[n][0], pb[n][1]);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          mma_f16(l[n], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[n][0], pb[n][1]);
-        if (!inside) {
-          poison |= __shfl_xor_sync(0xffffffffu, poison, 1);
-          poison |= __shfl_xor_sync(0xffffffffu, poison, 2);
-          for (; poison; poison &= poison - 1) {
-            const int pos = p0 + __ffs((int)poison) - 1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int at = first + row_i[n][x];
-                if (pos > at || (a.row_window > 0 && pos <= at - a.row_window)) continue;
-#pragma unroll
-                for (int d = 0; d < 8; ++d) o[n][d][x] = o[n][d][x + 2] = __uint_as_float(0x7fc00000u);
-              }
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(smem_u32(&sm.empty[st]));
-    }
-    ++it;
-
-    const bool piece_end = cur.t + 1 == t1 || cur.j + 1 == cur.n;
-    if (piece_end) {
-      // ---- join the warps: maxima, then the outputs relative to the largest
-      const bool whole = piece_first == cur.seg_base && cur.j + 1 == cur.n;
-      const int64_t slot =
-          piece_first == cur.seg_base ? (int64_t)cur.b * a.Hkv + cur.g : (int64_t)a.B * a.Hkv + blockIdx.x;
-      if (g == 0) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          sm.m[n][warp][2 * c] = m[n][0];
-          sm.m[n][warp][2 * c + 1] = m[n][1];
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n && n * 8 >= R) break;
-        tc::named_bar_sync(1, S::WARPS * 32);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < S::WARPS; ++i) top = fmaxf(top, sm.m[n][i][2 * c + x]);
-          const float scale = m[n][x] == -INFINITY ? (l[n][x] == 0.f ? 0.f : 1.f) : exp2_approx(m[n][x] - top);
-          float4* dst = reinterpret_cast<float4*>(&sm.o[warp][2 * c + x][16 * g]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_float4(o[n][2 * i][x] * scale, o[n][2 * i][x + 2] * scale,
-                                 o[n][2 * i + 1][x] * scale, o[n][2 * i + 1][x + 2] * scale);
-          if (g == 0) sm.l[warp][2 * c + x] = l[n][x] * scale;
-        }
-        tc::named_bar_sync(1, S::WARPS * 32);
-        // Eight rows of 128 outputs over the consumer threads.
-        constexpr int PER = 8 * D / (32 * S::WARPS);
-        const int h = tid * PER / D, d = tid * PER % D, row = n * 8 + h;
-        if (row < R) {
-          float sum = 0.f, top = -INFINITY, acc[PER];
-#pragma unroll
-          for (int x = 0; x < PER; ++x) acc[x] = 0.f;
-#pragma unroll
-          for (int i = 0; i < S::WARPS; ++i) {
-            sum += sm.l[i][h];
-            top = fmaxf(top, sm.m[n][i][h]);
-#pragma unroll
-            for (int x = 0; x < PER; ++x) acc[x] += sm.o[i][h][d + x];
-          }
-          // A sum that is not a number (a NaN score) makes the row's output and lse NaN.
-          const bool none = sum == 0.f;
-          const float inv = none ? 0.f : 1.f / sum;
-          const float lse2 = none ? -INFINITY : top + log2f(sum) - kShift;
-          if (whole) {
-            const int64_t at = ((int64_t)cur.b * a.q_len + row / a.n_rep) * a.H + (int64_t)cur.g * a.n_rep +
-                               row % a.n_rep;
-#pragma unroll
-            for (int x = 0; x < PER; x += 2) {
-              if (a.out_f32) {
-                *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + at * D + d + x) =
-                    make_float2(acc[x] * inv, acc[x + 1] * inv);
-              } else {
-                *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + d + x) =
-                    __floats2bfloat162_rn(acc[x] * inv, acc[x + 1] * inv);
-              }
-            }
-            if (a.lse && d == 0) a.lse[at] = lse2 * kLn2;
+            cp_async_16(dst + 2 * CODES, s_src, 16);
           } else {
-            const int64_t at = slot * R + row;
+            // Zeros instead of the rows behind the sequence's end (two rows of scales at a time).
+            const int live = ahead.len - ahead.pos;
 #pragma unroll
-            for (int x = 0; x < PER; x += 2)
-              *reinterpret_cast<float2*>(a.ws_o + at * D + d + x) = make_float2(acc[x] * inv, acc[x + 1] * inv);
-            if (d == 0) a.ws_lse[at] = lse2;
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t bytes = 8 * i + (lane >> 2) < live ? 16 : 0;
+              cp_async_16(dst + 512 * i, k_src + 512 * i, bytes);
+              cp_async_16(dst + CODES + 512 * i, v_src + 512 * i, bytes);
+            }
+            cp_async_16(dst + 2 * CODES, s_src, 2 * (lane & 15) < live ? 16 : 0);
+          }
+          k_src += CODES;
+        } else {
+          bad |= 1u << st;
+        }
+        v_src += CODES;
+        s_src += SCALES;
+        ahead.pos += SUB;
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st) issue(st);
+
+    int row_i[NT][2];  // query tokens of this lane's rows
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) row_i[n][x] = a.row0 + min(n * 8 + 2 * c + x, R - 1) / a.n_rep;
+    const bool reaches_in = u0 == 0 && !begun;  // the run starts with a segment of the CTA before
+    for (int st = 0, seg = 0;; ++seg) {
+      if (seg) begun = true;
+      r.clear();
+      uint4 qf[NT][4];              // B operands of the scores
+      // Factors of this lane's rows, scores that raise their maxima, kShift less their maxima.
+      float f[NT][2], limit[NT][2], shift[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = 8 * n + g;
+        const uint16_t* src = a.q + (((int64_t)cur.b * a.q_total + a.row0 + row / a.n_rep) * a.H +
+                                     (int64_t)cur.g * a.n_rep + row % a.n_rep) * D + 32 * c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          qf[n][i] = row < R ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+        const float down = query_to_f16(qf[n]) * a.scale_log2;
+        f[n][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+        f[n][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+        limit[n][0] = limit[n][1] = -INFINITY;
+        shift[n][0] = shift[n][1] = kShift;
+      }
+      const Sight sight = {cur.len - a.q_total, a.row_window, a.row0, a.q_len};
+      for (; cur.pos < cur.stop; cur.pos += SUB) {
+        cp_async_wait<STAGES - 1>();
+        __syncwarp();  // every lane's copies are there
+        if (!(bad >> st & 1)) {
+          const uint8_t* tile = sm.stage[warp][st];
+          const uint8_t *k = tile, *v = tile + CODES, *ks = tile + 2 * CODES, *vs = ks + SCALES;
+          constexpr int C16 = 16 * fp4::kCodeBytes, S16 = 16 * fp4::kScaleBytes;
+          if (sight.all(cur.pos, cur.pos + SUB - 1)) {
+            attend<NT, AT_ONCE, false>(r, qf, f, limit, shift, row_i, k, v, ks, vs, cur.pos, sight, g, c);
+            if (AT_ONCE == 1)
+              attend<NT, AT_ONCE, false>(r, qf, f, limit, shift, row_i, k + C16, v + C16, ks + S16, vs + S16,
+                                         cur.pos + 16, sight, g, c);
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+              attend<NT, 1, true>(r, qf, f, limit, shift, row_i, k + h * C16, v + h * C16, ks + h * S16,
+                                  vs + h * S16, cur.pos + 16 * h, sight, g, c);
           }
         }
+        __syncwarp();  // every lane has read the stage
+        issue(st);
+        st = (st + 1) % STAGES;
       }
+      r.sum_lanes();
+      const bool own = begun || reaches_in;
+      if (cur.ends && own) {
+        put(a, r, lane, cur.b, cur.g, begun ? (int64_t)-1 : (int64_t)a.B * a.Hkv + blockIdx.x);
+      } else if (own) {
+        open = true;
+      } else {
+        leave(sm, warp, lane, r);
+        left = cur.ends ? kEnds : kGoesOn;
+      }
+      if (!cur.ends || !cur.next(rows, a.B, a.Hkv)) break;
     }
-    if (!cursor_next(cur, rows, a.B, a.Hkv)) break;
+    cp_async_wait<0>();
   }
+  if (lane == 0) sm.left[warp] = left;
+  __syncthreads();
+  if (!open) return;
+  // The segment that this warp began (or that reaches into the CTA's share from the one before)
+  // goes on in the next warps.
+  bool ended = false;
+  for (int x = warp + 1; x < WARPS && !ended; ++x) {
+    if (sm.left[x] == kNothing) continue;
+    take(sm, x, lane, r);
+    ended = sm.left[x] == kEnds;
+  }
+  put(a, r, lane, cur.b, cur.g,
+      begun ? (ended ? (int64_t)-1 : (int64_t)cur.b * a.Hkv + cur.g) : (int64_t)a.B * a.Hkv + blockIdx.x);
 }
 
 template <int NT>
@@ -463,16 +603,21 @@ cudaError_t launch_n(const DecodeArgs& a, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_fp4_kernel<NT>, dim3(a.num_ctas), dim3(Shape<NT>::THREADS), smem, stream, a);
+  return launch_dependent(decode_fp4_kernel<NT>, dim3(a.num_ctas), dim3(32 * Shape<NT>::WARPS), smem, stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t stream) {
-  const int rows = a.n_rep * a.q_len;
-  if (rows <= 8) return launch_n<1>(a, stream);
-  if (rows <= 16) return launch_n<2>(a, stream);
-  return launch_n<4>(a, stream);
+// Query tokens in pieces of at most 16 rows per kv head, each with a pass over the cache of its own.
+cudaError_t launch_decode_fp4(DecodeArgs a, cudaStream_t stream) {
+  const int per = 16 / a.n_rep;
+  for (a.row0 = 0; a.row0 < a.q_total; a.row0 += per) {
+    a.q_len = a.q_total - a.row0 < per ? a.q_total - a.row0 : per;
+    cudaError_t e = a.n_rep * a.q_len <= 8 ? launch_n<1>(a, stream) : launch_n<2>(a, stream);
+    if (e == cudaSuccess) e = launch_decode_merge(a, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pkv

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   const int n = live_blocks(clamp_len(__ldg(a.seq_lens + b), cap), bs, a.window).n;
   const int64_t base = before * a.Hkv + (int64_t)g * n;
   const int64_t row =
-      ((int64_t)b * a.q_len + h / a.n_rep) * a.H + (int64_t)g * a.n_rep + h % a.n_rep;
+      ((int64_t)b * a.q_total + a.row0 + h / a.n_rep) * a.H + (int64_t)g * a.n_rep + h % a.n_rep;
   auto put = [&](float4 v) {
     if (a.out_f32) {
       reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * D)[lane] = v;
@@ -323,22 +323,37 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
       wsum += w;
     }
   } else {
-    // More pieces than registers hold (segments far longer than a CTA's share).
-    for (int64_t i = i0; i <= i1; ++i) {
+    // More pieces than registers hold (segments far longer than a CTA's share): first the largest
+    // log-sum-exp, a piece per lane, then the sums in the pieces' order, kMaxPieces at a time.
+    for (int64_t i = i0 + lane; i <= i1; i += 32) {
       if (i > i0 && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G)) continue;
       mx = fmaxf(mx, a.ws_lse[slot_of(i) * n_rep + h]);
     }
-    for (int64_t i = i0; i <= i1; ++i) {
-      if (i > i0 && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G)) continue;
-      const int64_t slot = slot_of(i);
-      const float l2 = a.ws_lse[slot * n_rep + h];
-      const float w = (l2 == -INFINITY) ? 0.f : exp2f(l2 - mx);
-      const float4 x = reinterpret_cast<const float4*>(a.ws_o + (slot * n_rep + h) * D)[lane];
-      acc.x += w * x.x;
-      acc.y += w * x.y;
-      acc.z += w * x.z;
-      acc.w += w * x.w;
-      wsum += w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int64_t i = i0; i <= i1; i += kMaxPieces) {
+      float l2[kMaxPieces];
+      float4 x[kMaxPieces];
+      bool has[kMaxPieces];
+#pragma unroll
+      for (int p = 0; p < kMaxPieces; ++p) {
+        has[p] = i + p <= i1 && (i + p == i0 || cta_tile_start(i + p + 1, T, G) != cta_tile_start(i + p, T, G));
+        if (has[p]) {
+          const int64_t slot = slot_of(i + p);
+          l2[p] = a.ws_lse[slot * n_rep + h];
+          x[p] = reinterpret_cast<const float4*>(a.ws_o + (slot * n_rep + h) * D)[lane];
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < kMaxPieces; ++p) {
+        if (!has[p]) continue;
+        const float w = (l2[p] == -INFINITY) ? 0.f : exp2f(l2[p] - mx);
+        acc.x += w * x[p].x;
+        acc.y += w * x[p].y;
+        acc.z += w * x[p].z;
+        acc.w += w * x[p].w;
+        wsum += w;
+      }
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;

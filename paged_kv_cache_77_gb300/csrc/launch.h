@@ -153,7 +153,8 @@ struct DecodeArgs {
   int* dev_status;
   int64_t num_blocks;
   int B, H, Hkv, n_rep, max_blocks, out_f32;
-  int q_len;                  // new query rows per sequence (1 = plain decode)
+  int q_len;                  // new query rows per sequence (1 = plain decode) of this launch,
+  int q_total, row0;          // which are row0 .. row0 + q_len - 1 of the q_total of q and out
   int row_window;             // window of one query row (0 = full attention)
   int window;                 // live-block span: row_window + q_len - 1 (0 = all)
   int num_ctas;               // G: CTAs of the attention kernel (one per SM)
@@ -182,9 +183,9 @@ cudaError_t launch_decode_sparse(const DecodeArgs& a, cudaStream_t stream);
 // tcgen05 split-KV decode over an FP8 (E4M3) cache with per-row scales; same
 // partials and merge as above.
 cudaError_t launch_decode_fp8(const DecodeArgs& a, cudaStream_t stream);
-// Split-KV decode over the 4-bit cache for q_len 1..4 query rows per sequence; same partials
-// and merge as above.
-cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t stream);
+// Split-KV decode over the 4-bit cache for q_len 1..4 query rows per sequence, same partials as
+// above, and its merge.
+cudaError_t launch_decode_fp4(DecodeArgs a, cudaStream_t stream);
 
 // Absorbed MLA decode (tcgen05) plus its merge, q_len query rows per sequence
 // (1 for plain decode). Workspace: mla_workspace_bytes(B * q_len, num_sms / 2).
