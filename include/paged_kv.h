@@ -692,12 +692,12 @@ int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_ta
  *     of row_bytes (head_major 0: the bf16 and FP8 caches), or [num_blocks, H_kv, block_size]
  *     (head_major 1: the 4-bit cache, scales, weights). Caches may not overlap one another,
  *     kept or the tables (PKV_ERR_INVALID_ARG).
- *   new_block_table [B, new_max_blocks_per_seq] int32, or NULL: in place. With a table, rows are
- *     read through block_table and written through the new one (for blocks that other requests
- *     share); a block that both tables of a sequence hold must have the same place in both. No
- *     block that one sequence writes may be read or written by another.
+ *   new_block_table [B, new_max_blocks_per_seq] int32, or NULL (or block_table itself): in place.
+ *     With a table, rows are read through block_table and written through the new one (for blocks
+ *     that other requests share); the new one's blocks for the kept rows must be none of those
+ *     that the call reads. No block that one sequence writes may be read or written by another.
  * Entries past block_table set PKV_DEV_BAD_LENGTH, rows of a block outside [0, num_blocks)
- * PKV_DEV_BAD_BLOCK; neither is moved. Supported: row_bytes a multiple of 4, up to 16 caches
+ * PKV_DEV_BAD_BLOCK; neither is moved. Supported: row_bytes a multiple of 4 up to 65536, up to 16 caches
  * (PKV_ERR_UNSUPPORTED otherwise). Caches 16-byte aligned. No workspace. */
 int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_t* head_major,
                      int32_t num_caches, const int32_t* kept, int32_t num_keep,

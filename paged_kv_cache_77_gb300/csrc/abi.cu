@@ -779,8 +779,8 @@ int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_
   };
   for (int i = 0; i < num_caches; ++i) {
     PKV_REQUIRE(caches[i], PKV_ERR_INVALID_ARG, "%s: null pointer", what);
-    PKV_REQUIRE(row_bytes[i] > 0 && row_bytes[i] % 4 == 0 && row_bytes[i] <= (1 << 20), PKV_ERR_UNSUPPORTED,
-                "%s: rows of %d bytes (a multiple of 4 up to 2^20 is implemented)", what, row_bytes[i]);
+    PKV_REQUIRE(row_bytes[i] > 0 && row_bytes[i] % 4 == 0 && row_bytes[i] <= (1 << 16), PKV_ERR_UNSUPPORTED,
+                "%s: rows of %d bytes (a multiple of 4 up to 2^16 is implemented)", what, row_bytes[i]);
     PKV_REQUIRE(aligned16(caches[i]), PKV_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", what);
     PKV_REQUIRE(!reads(caches[i], rows * row_bytes[i]), PKV_ERR_INVALID_ARG,
                 "%s: cache %d overlaps kept or a table", what, i);
@@ -807,7 +807,7 @@ int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_
   a.num_keep = num_keep;
   a.num_caches = num_caches;
   clear_error();
-  return launch_status(launch_compact_rows(a, (cudaStream_t)stream), what);
+  return launch_status(launch_compact_rows(a, (cudaStream_t)stream, current_num_sms()), what);
 }
 
 int pkv_select_blocks(int32_t* block_indices, const void* q, const void* summaries,

@@ -136,8 +136,9 @@ struct CompactArgs {
   int* dev_status;
   int64_t num_blocks;
   int B, Hkv, block_size, max_blocks, new_max_blocks, num_keep, num_caches;
+  int slices, part_rows;      // of a row's bytes at most; rows of the list that one CTA moves
 };
-cudaError_t launch_compact_rows(CompactArgs a, cudaStream_t stream);
+cudaError_t launch_compact_rows(CompactArgs a, cudaStream_t stream, int num_sms);
 
 // Arguments of the split-KV decode kernels and their LSE merge.
 struct DecodeArgs {
