@@ -589,8 +589,8 @@ int pkv_paged_attention_decode_fp8(void* out, int32_t out_dtype, float* lse, con
  *   value = code * scale (6 significant bits: exact in bf16 and fp16)
  * decided as in exact arithmetic. 16 values of which none reaches 6 * 2^-18 have scale 0 and
  * codes 0; magnitudes past 61440 are held as 61440; 16 values with an infinity or a NaN among
- * them have the scale 0xFF and read back as NaN. Scale bytes 0xE3 to 0xFE are never written;
- * 0xF8 and above read as NaN, and the decode may take any of them for NaN.
+ * them have the scale 0xFF and read back as NaN. Scale bytes 0xE3 to 0xFE are never written, and
+ * what they stand for is left open.
  *   k_cache, v_cache [num_blocks, H_kv, block_size, 64] uint8: head-major, so that what the
  *                    decode reads of a block for one kv head is one piece
  *   k_scale, v_scale [num_blocks, H_kv, block_size, 8] uint8

@@ -302,15 +302,15 @@ int fp4_setup(pkv::KvFp4Args& a, const char* what, const void* k_cache, const vo
   PKV_REQUIRE(head_dim == 128, PKV_ERR_UNSUPPORTED, "%s: only head_dim 128 is implemented", what);
   PKV_REQUIRE(num_blocks * block_size <= INT32_MAX, PKV_ERR_UNSUPPORTED,
               "%s: num_blocks * block_size must fit in int32", what);
-  PKV_REQUIRE(num_tokens <= INT32_MAX && num_kv_heads <= (1 << 20), PKV_ERR_UNSUPPORTED,
-              "%s: too many rows", what);
+  PKV_REQUIRE(num_tokens <= INT32_MAX / 2 / num_kv_heads, PKV_ERR_UNSUPPORTED,
+              "%s: too many rows (2 num_tokens * H_kv must fit in int32)", what);
   PKV_REQUIRE(k_cache && v_cache && k_scale && v_scale && (num_tokens == 0 || (k && v && slot_mapping)),
               PKV_ERR_INVALID_ARG, "%s: null pointer", what);
   PKV_REQUIRE(aligned16(k_cache) && aligned16(v_cache) && aligned16(k_scale) && aligned16(v_scale) &&
                   aligned16(k) && aligned16(v) && (((uintptr_t)slot_mapping) & 3) == 0,
               PKV_ERR_INVALID_ARG, "%s: misaligned pointer", what);
   a = KvFp4Args{(uint8_t*)k_cache, (uint8_t*)v_cache, (uint8_t*)k_scale, (uint8_t*)v_scale, slot_mapping,
-                dev_status, num_tokens, num_blocks, block_size, num_kv_heads};
+                dev_status, num_tokens, num_blocks, block_size, num_kv_heads, 0, {}, {}};
   return PKV_OK;
 }
 

@@ -62,13 +62,20 @@ __device__ __forceinline__ float scale_value(uint32_t u) {
   return r;
 }
 
+// x / d for a quotient that decides between codes or scales: exact where the exact quotient is an
+// fp32 number, else within 2^-22 of itself (the remainder of a product with an approximate
+// reciprocal, added back).
+__device__ __forceinline__ float quotient(float x, float d, float reciprocal) {
+  const float q = mul_ieee(x, reciprocal);
+  return fma_ieee(fma_ieee(-q, d, x), reciprocal, q);
+}
+
 // Scale byte of 16 bf16 values with largest magnitude `amax` (finite, not negative): the
 // scale nearest to amax / 6, ties to the even byte. amax has 8 significant bits and 6 times
-// a border between two scales 7, so an fp32 quotient can equal a border only where the exact
-// one does, and a correctly rounded one then does: the quotient decides as in exact
-// arithmetic.
+// a border between two scales 7: a quotient that does not equal a border is 2^-8 of itself away
+// from it or more, one that does is exact.
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
-  const float want = div_ieee(amax, 6.f);
+  const float want = quotient(amax, 6.f, 1.f / 6.f);
   uint32_t u;
   if (want >= 0x1p-14f) {
     const uint32_t w = __float_as_uint(want);
@@ -79,18 +86,18 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
   return u < (uint32_t)kMaxScale ? u : (uint32_t)kMaxScale;
 }
 
-// Codes of 16 values under a scale byte (not 0xFF), x / scale rounded to the nearest code,
-// ties to the even one, magnitudes past 6 to 6. The border between two codes times the scale
-// has 7 bits, x has 8: as above, only a quotient at a border has to be exact, and the
-// corrected one is (the remainder of a product with the reciprocal, added back).
-__device__ __forceinline__ uint2 quantise(const float (&x)[16], uint32_t scale) {
+// Codes of 16 bf16 values, in pairs, under a scale byte (not 0xFF): x / scale rounded to the nearest
+// code, ties to the even one, magnitudes past 6 to 6. A border between two codes times the scale
+// has 7 bits, x has 8: the quotient decides as above.
+__device__ __forceinline__ uint2 quantise(const uint32_t (&x)[8], uint32_t scale) {
   if (scale == 0) return make_uint2(0, 0);
-  const float s = scale_value(scale), inv = div_ieee(1.f, s);
-  float q[16];
+  const float s = scale_value(scale);
+  float inv, q[16];
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(s));
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float q0 = mul_ieee(x[i], inv);
-    q[i] = fma_ieee(fma_ieee(-q0, s, x[i]), inv, q0);
+  for (int i = 0; i < 8; ++i) {
+    q[2 * i] = quotient(__uint_as_float(x[i] << 16), s, inv);
+    q[2 * i + 1] = quotient(__uint_as_float(x[i] & 0xffff0000u), s, inv);
   }
   return make_uint2(codes(q), codes(q + 8));
 }

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fast_divide.cuh"
+
 namespace pkv {
 
 cudaError_t launch_kv_write(void* k_cache, void* v_cache, const void* k, const void* v,
@@ -59,11 +61,13 @@ struct KvFp4Args {
   int* dev_status;
   int64_t num_tokens, num_blocks;
   int block_size, hkv;
+  uint32_t items;              // rows of k and v together, set by the launch, as the divisors are
+  FastDivide heads, block;
 };
 // Strides in elements, between tokens; the heads of a token are contiguous.
-cudaError_t launch_kv_write_fp4(const KvFp4Args& a, const void* k, int64_t k_stride, const void* v,
+cudaError_t launch_kv_write_fp4(KvFp4Args a, const void* k, int64_t k_stride, const void* v,
                                 int64_t v_stride, cudaStream_t stream, int num_sms);
-cudaError_t launch_kv_read_fp4(const KvFp4Args& a, void* k, void* v, cudaStream_t stream, int num_sms);
+cudaError_t launch_kv_read_fp4(KvFp4Args a, void* k, void* v, cudaStream_t stream, int num_sms);
 
 // Block summaries and block selection (block_select.cu).
 constexpr int kSelectMaxBlocks = 8192;  // widest table of a selection: a million tokens
