@@ -678,7 +678,8 @@ int pkv_accumulate_attention_weights(float* weights, const void* q, const float*
  * weight of it is read. Rows of a table entry outside [0, num_blocks) rank below all
  * (PKV_DEV_BAD_BLOCK); lengths past the table are clamped (PKV_DEV_BAD_LENGTH).
  *   kept [B, H_kv, num_keep] int32 (written), which may not overlap anything the call reads
- * Supported: block_size 128, num_sink + num_recent <= num_keep. No workspace. */
+ * Supported: block_size 128, num_sink + num_recent <= num_keep, max_blocks_per_seq <= 32768
+ * (4,194,304 tokens). No workspace. */
 int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_table,
                     int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t B, int32_t H_kv,
                     int32_t block_size, int64_t num_blocks, int32_t num_keep, int32_t num_sink,

@@ -730,10 +730,10 @@ int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_ta
   PKV_REQUIRE(block_size == 128, PKV_ERR_UNSUPPORTED, "%s: only block_size 128 is implemented", what);
   PKV_REQUIRE((int64_t)num_sink + num_recent <= num_keep, PKV_ERR_INVALID_ARG,
               "%s: num_sink + num_recent exceeds num_keep", what);
-  PKV_REQUIRE(max_blocks_per_seq <= (INT32_MAX >> 1) / 128 && num_blocks * block_size <= INT32_MAX &&
-                  B <= INT32_MAX / H_kv,
-              PKV_ERR_UNSUPPORTED,
-              "%s: max_blocks_per_seq * 256, num_blocks * 128 and B * H_kv must fit in int32", what);
+  PKV_REQUIRE(max_blocks_per_seq <= kSelectRowsMaxBlocks, PKV_ERR_UNSUPPORTED,
+              "%s: max_blocks_per_seq exceeds %d", what, kSelectRowsMaxBlocks);
+  PKV_REQUIRE(num_blocks * block_size <= INT32_MAX && B <= INT32_MAX / 8 / H_kv, PKV_ERR_UNSUPPORTED,
+              "%s: num_blocks * 128 and 8 B * H_kv must fit in int32", what);
   if (B == 0) return PKV_OK;
   PKV_REQUIRE(kept && weights && block_table && seq_lens, PKV_ERR_INVALID_ARG, "%s: null pointer", what);
   PKV_REQUIRE(aligned16(weights) && aligned16(kept), PKV_ERR_INVALID_ARG,

@@ -62,12 +62,12 @@ __device__ __forceinline__ float scale_value(uint32_t u) {
   return r;
 }
 
-// x / d for a quotient that decides between codes or scales: exact where the exact quotient is an
+// x / d, given -d, for a quotient that decides between codes or scales: exact where the exact quotient is an
 // fp32 number, else within 2^-22 of itself (the remainder of a product with an approximate
 // reciprocal, added back).
-__device__ __forceinline__ float quotient(float x, float d, float reciprocal) {
+__device__ __forceinline__ float quotient(float x, float minus_d, float reciprocal) {
   const float q = mul_ieee(x, reciprocal);
-  return fma_ieee(fma_ieee(-q, d, x), reciprocal, q);
+  return fma_ieee(fma_ieee(q, minus_d, x), reciprocal, q);
 }
 
 // Scale byte of 16 bf16 values with largest magnitude `amax` (finite, not negative): the
@@ -75,7 +75,7 @@ __device__ __forceinline__ float quotient(float x, float d, float reciprocal) {
 // a border between two scales 7: a quotient that does not equal a border is 2^-8 of itself away
 // from it or more, one that does is exact.
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
-  const float want = quotient(amax, 6.f, 1.f / 6.f);
+  const float want = quotient(amax, -6.f, 1.f / 6.f);
   uint32_t u;
   if (want >= 0x1p-14f) {
     const uint32_t w = __float_as_uint(want);
@@ -91,13 +91,13 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
 // has 7 bits, x has 8: the quotient decides as above.
 __device__ __forceinline__ uint2 quantise(const uint32_t (&x)[8], uint32_t scale) {
   if (scale == 0) return make_uint2(0, 0);
-  const float s = scale_value(scale);
+  const float s = scale_value(scale), minus = -s;
   float inv, q[16];
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(s));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    q[2 * i] = quotient(__uint_as_float(x[i] << 16), s, inv);
-    q[2 * i + 1] = quotient(__uint_as_float(x[i] & 0xffff0000u), s, inv);
+    q[2 * i] = quotient(__uint_as_float(x[i] << 16), minus, inv);
+    q[2 * i + 1] = quotient(__uint_as_float(x[i] & 0xffff0000u), minus, inv);
   }
   return make_uint2(codes(q), codes(q + 8));
 }

@@ -1,17 +1,24 @@
 // Eviction: the choice of the rows that stay.
 //
 // For each sequence and kv head the num_keep positions with the largest weights, ascending. The
-// border, the weight of the last row taken, is found digit by digit (11, 11 and 10 bits of the
-// weights' order-preserving integers): a histogram of the digit over the rows that share the
-// digits before, and a scan from the top. Then each warp counts what it takes and, knowing what
-// the warps before it take, writes its positions in order. The first num_sink and the last
-// num_recent positions are taken without being ranked.
+// first num_sink and the last num_recent are taken without being ranked; of the others, as
+// integers in the weights' order, the border is searched, the weight of the last row taken:
+//   - a sample of the weights (8 of each block's 128, a sector of memory) gives a bracket that
+//     holds the border with near certainty: the digits (11 bits) of the weights that lie three
+//     and a half standard deviations of the sample's rank to either side;
+//   - one pass over the weights: two bit masks in shared memory, of those above the bracket and
+//     of those inside it; the few inside (some 10 %; all of a short row, without a sample) go into
+//     a list;
+//   - the border is found in the list digit by digit, a histogram and a scan from the top each;
+//   - the list's rows above it enter the first mask, those that equal it a mask of their own, of
+//     which the lowest positions are taken; every lane writes the positions of words of the masks.
+// Where the bracket misses, or the list overflows (weights of few different values), all of it is
+// done again with every digit over all weights, read from L2 each time.
 //
 // A row (sequence, kv head) is the work of a cluster of 1 to 8 CTAs, each with its own run of
-// blocks and, for the digits, its own histogram, which every CTA of the cluster sums up for
-// itself through distributed shared memory. A warp's run of blocks is consecutive; it reads
-// their weights once, keeps them as integers in shared memory, and reads those that do not fit
-// there again, from L2, for each later pass.
+// blocks, list and histograms; every CTA sums the histograms of the cluster for itself through
+// distributed shared memory. What bounds it is instructions: per block of 128 weights some 90 of a
+// warp, of which the pass over the weights takes half.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -23,10 +30,13 @@ namespace cg = cooperative_groups;
 namespace pkv {
 namespace {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32, BS = 128;
-constexpr int HELD = 4;          // blocks of a warp in flight
-constexpr int MAX_KEPT = 384;    // blocks of a CTA whose keys stay in shared memory
+constexpr int THREADS = 512, WARPS = THREADS / 32, BS = 128, BINS = 2048;
+constexpr int FLIGHT = 4;        // blocks of a warp in flight
+constexpr int LIST = 5120;       // rows of a CTA inside the bracket
+constexpr int SHORT = 1024;      // rows of a CTA that need no bracket
 constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_PER_CTA = 4096;  // blocks of a CTA, whose masks take 128 KB
+static_assert(kSelectRowsMaxBlocks <= MAX_CLUSTER * MAX_PER_CTA, "a row's masks fit its cluster");
 constexpr uint32_t ABSENT = 0, BAD = 1;  // keys of positions that are not ranked, and of bad blocks
 
 // Whole numbers in the order of weights given by their bits: -0 equals 0, NaN is above all; the
@@ -45,19 +55,43 @@ __device__ __forceinline__ uint4 weight_keys(uint4 w) {
 }
 
 struct Shared {
-  int hist[3][2048];
+  int hist[2][BINS];
   int wsum[WARPS], wabove[WARPS], wequal[WARPS];
-  int pick_bin, pick_left, pick_all;
-  int above, equal;  // of this CTA
+  int bin[2], rest, all, total;          // what a scan found
+  int above, inside;                     // of this CTA: rows above the bracket, rows in the list
+  int taken, equal;                      // rows taken without ties, rows of the border's weight
 };
 
-__global__ void __launch_bounds__(THREADS, 1) select_rows_kernel(const __grid_constant__ SelectRowsArgs a, int keep_blocks) {
-  extern __shared__ uint4 kept_keys[];  // [WARPS][keep_blocks][32]
+// Dynamic shared memory: masks of a CTA's blocks, four words each (bit l of word j: position 4 l + j),
+// of rows taken and of rows inside the bracket, later of rows that equal the border; then the list,
+// its rows' places as 4 * 32 * block + 32 j + l.
+struct Lists {
+  uint4 *take, *other;
+  uint32_t *key, *place;
+  __device__ __forceinline__ Lists(uint4* base, int blocks)
+      : take(base), other(take + blocks), key(reinterpret_cast<uint32_t*>(other + blocks)), place(key + LIST) {}
+};
+
+// Bits 0 to 7 of x as bits 0, 4, .. 28.
+__device__ __forceinline__ uint32_t spread8(uint32_t x) {
+  x &= 0xffu;
+  x = (x | x << 12) & 0x000f000fu;
+  x = (x | x << 6) & 0x03030303u;
+  return (x | x << 3) & 0x11111111u;
+}
+// Positions 32 t .. 32 t + 31 of a block's mask in order.
+__device__ __forceinline__ uint32_t in_order(uint4 m, int t) {
+  return spread8(m.x >> 8 * t) | spread8(m.y >> 8 * t) << 1 | spread8(m.z >> 8 * t) << 2 | spread8(m.w >> 8 * t) << 3;
+}
+__device__ __forceinline__ int size(uint4 m) { return __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w); }
+
+__global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_constant__ SelectRowsArgs a, int cta_blocks) {
   __shared__ __align__(16) Shared sh;
+  extern __shared__ __align__(16) uint4 dynamic[];
   pdl_wait_then_launch();
   const int C = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
   const int row = blockIdx.x / C, b = row / a.Hkv, g = row % a.Hkv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int raw = __ldg(a.seq_lens + b), n = clamp_len(raw, a.max_blocks * BS);
   if (n != raw && g == 0 && rank == 0 && tid == 0) flag_status(a.dev_status, PKV_DEV_BAD_LENGTH);
   int32_t* out = a.out + (int64_t)row * a.num_keep;
@@ -69,40 +103,43 @@ __global__ void __launch_bounds__(THREADS, 1) select_rows_kernel(const __grid_co
   for (int i = rank * THREADS + tid; i < a.num_sink; i += C * THREADS) out[i] = i;
   for (int i = rank * THREADS + tid; i < a.num_recent; i += C * THREADS)
     out[a.num_keep - a.num_recent + i] = hi + i;
-  int left = a.num_keep - a.num_sink - a.num_recent;  // rows still to take among those at the border
-  if (left == 0) return;
+  const int want = a.num_keep - a.num_sink - a.num_recent;  // of hi - lo > want
+  if (want == 0) return;
   auto sync = [&] {
     if (C == 1)
       __syncthreads();
     else
       cg::this_cluster().sync();
   };
+  const Lists list(dynamic, cta_blocks);
 
-  // This warp's blocks: `count` from `first` on.
+  // This warp's blocks: `count` from `first` on; their masks begin at the own-th of the CTA's.
   const int blocks = (hi + BS - 1) / BS, per = (blocks + C * WARPS - 1) / (C * WARPS);
-  const int first = (rank * WARPS + warp) * per, count = max(0, min(per, blocks - first));
+  const int first = (rank * WARPS + warp) * per, count = max(0, min(per, blocks - first)), own = warp * per;
   const int32_t* table = a.block_table + (int64_t)b * a.max_blocks + first;
-  uint4* mine = kept_keys + warp * keep_blocks * 32 + lane;
-  // The warp's blocks in order, HELD at a time: f(block, its four keys of this lane).
-  auto stream = [&](int q, auto&& f) {
-    for (; q < count; q += HELD) {
-      const int ids = lane < HELD && q + lane < count ? __ldg(table + q + lane) : 0;
+  const uint32_t* weights = reinterpret_cast<const uint32_t*>(a.weights) + (int64_t)g * BS;
+  const int64_t stride = (int64_t)a.Hkv * BS;  // from block to block
+  // What another CTA of the cluster has where this one has *mine; r is clamped to the cluster.
+  auto theirs = [&](auto* mine, int r) { return cg::this_cluster().map_shared_rank(mine, min(r, C - 1)); };
+  // The warp's blocks in order, FLIGHT at a time: f(block, its four keys of this lane).
+  auto stream = [&](auto&& f) {
+    for (int q = 0; q < count; q += FLIGHT) {
+      const int ids = lane < FLIGHT && q + lane < count ? __ldg(table + q + lane) : 0;
       const bool wrong = ids < 0 || (int64_t)ids >= a.num_blocks;
       if (wrong) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
       const unsigned bad = __ballot_sync(0xffffffffu, wrong);
-      uint4 w[HELD];
+      uint4 w[FLIGHT];
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) {
+      for (int i = 0; i < FLIGHT; ++i) {
         const int blk = __shfl_sync(0xffffffffu, ids, i);
-        if (q + i < count && !(bad >> i & 1))
-          w[i] = __ldg(reinterpret_cast<const uint4*>(a.weights + ((int64_t)blk * a.Hkv + g) * BS) + lane);
+        if (q + i < count && !(bad >> i & 1)) w[i] = __ldg(reinterpret_cast<const uint4*>(weights + blk * stride) + lane);
       }
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) {
+      for (int i = 0; i < FLIGHT; ++i) {
         if (q + i >= count) break;
         uint4 k = bad >> i & 1 ? make_uint4(BAD, BAD, BAD, BAD) : weight_keys(w[i]);
-        const int pos = (first + q + i) * BS + 4 * lane;
-        if (pos - 4 * lane < lo || pos - 4 * lane + BS > hi) {
+        const int start = (first + q + i) * BS, pos = start + 4 * lane;
+        if (start < lo || start + BS > hi) {
           if (pos < lo || pos >= hi) k.x = ABSENT;
           if (pos + 1 < lo || pos + 1 >= hi) k.y = ABSENT;
           if (pos + 2 < lo || pos + 2 >= hi) k.z = ABSENT;
@@ -112,52 +149,43 @@ __global__ void __launch_bounds__(THREADS, 1) select_rows_kernel(const __grid_co
       }
     }
   };
-  auto each = [&](auto&& f) {
-    const int kept = min(count, keep_blocks);
-#pragma unroll 2
-    for (int q = 0; q < kept; ++q) f(q, mine[q * 32]);
-    if (count > keep_blocks) stream(keep_blocks, f);
+  // The mask of the keys that p holds for.
+  auto mask = [&](uint4 k, auto&& p) {
+    return make_uint4(__ballot_sync(0xffffffffu, p(k.x)), __ballot_sync(0xffffffffu, p(k.y)),
+                      __ballot_sync(0xffffffffu, p(k.z)), __ballot_sync(0xffffffffu, p(k.w)));
   };
-  for (int i = tid; i < 3 * 2048 / 4; i += THREADS) reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
-  __syncthreads();
-
-  uint32_t border = 0;  // its digits so far
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    int* hist = sh.hist[pass];
-    if (pass == 0) {
-      stream(0, [&](int q, uint4 k) {
-        if (q < keep_blocks) mine[q * 32] = k;
-        // (Keys that are not ranked count in bin 0, which is put right below.)
-        atomicAdd(hist + (k.x >> 21), 1);
-        atomicAdd(hist + (k.y >> 21), 1);
-        atomicAdd(hist + (k.z >> 21), 1);
-        atomicAdd(hist + (k.w >> 21), 1);
-      });
-    } else {
-      const uint32_t base = border << (shift + bits), span = 1u << (shift + bits);
-      each([&](int, uint4 k) {
-        auto add = [&](uint32_t x) {
-          if (x - base < span && x != ABSENT) atomicAdd(hist + (x >> shift & ((1 << bits) - 1)), 1);
-        };
-        add(k.x);
-        add(k.y);
-        add(k.z);
-        add(k.w);
-      });
+  // Sums of x over the lanes before this one, and over all.
+  auto before = [&](int x, int& all) {
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
-    sync();
-    // Thread t sums the bins 4 (511 - t) .. + 3 over the cluster; the scan runs from the top.
-    int4 h = make_int4(0, 0, 0, 0);
-    if (tid < 512 && (bits == 11 || tid >= 256)) {
-      for (int r = 0; r < C; ++r) {
-        const int* from = C == 1 ? hist : cg::this_cluster().map_shared_rank(hist, r);
-        const int4 x = reinterpret_cast<const int4*>(from)[511 - tid];
-        h = make_int4(h.x + x.x, h.y + x.y, h.z + x.z, h.w + x.w);
+    all = __shfl_sync(0xffffffffu, incl, 31);
+    return incl - x;
+  };
+  // Behind a sync(): EACH bins of a histogram, from bin BINS - 1 - EACH * tid down, summed over the
+  // cluster, and how many rows lie in the bins above them.
+  constexpr int EACH = BINS / THREADS;
+  int held[EACH], higher;
+  auto scan = [&](const int* hist) {
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) held[i] = 0;
+    for (int r = 0; r < C; ++r) {
+      const int* from = C == 1 ? hist : theirs(hist, r);
+#pragma unroll
+      for (int i = 0; i < EACH; i += 4) {
+        const int4 x = reinterpret_cast<const int4*>(from + BINS - EACH * (tid + 1))[EACH / 4 - 1 - i / 4];
+        held[i] += x.w;
+        held[i + 1] += x.z;
+        held[i + 2] += x.y;
+        held[i + 3] += x.x;
       }
     }
-    const int sum = h.x + h.y + h.z + h.w;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) sum += held[i];
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -166,51 +194,249 @@ __global__ void __launch_bounds__(THREADS, 1) select_rows_kernel(const __grid_co
     }
     if (lane == 31) sh.wsum[warp] = incl;
     __syncthreads();
-    int before = lane < warp ? sh.wsum[lane & (WARPS - 1)] : 0;
-    before = __reduce_add_sync(0xffffffffu, before);
-    incl += before;
-    int rest = left - (incl - sum);  // to take from this thread's bins on
-    if (rest > 0 && left <= incl) {
-      int bin = 4 * (511 - tid) + 3, size = h.w;
-      if (rest > size) {
-        rest -= size;
-        --bin;
-        size = h.z;
-        if (rest > size) {
-          rest -= size;
-          --bin;
-          size = h.y;
-          if (rest > size) {
-            rest -= size;
-            --bin;
-            size = h.x;
-          }
-        }
+    incl += __reduce_add_sync(0xffffffffu, lane < warp ? sh.wsum[lane & (WARPS - 1)] : 0);
+    higher = incl - sum;
+    if (tid == THREADS - 1) sh.total = incl;
+  };
+  // The bin with the rank-th row from the top (1 <= rank <= total), in the thread that holds it:
+  // f(bin, rows still to take in it, rows in it).
+  auto find = [&](int rank_, auto&& f) {
+    int rest = rank_ - higher;
+    if (rest <= 0) return;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      if (rest > 0 && rest <= held[i]) f(BINS - 1 - EACH * tid - i, rest, held[i]);
+      rest -= held[i];
+    }
+  };
+
+  // Two histograms in turn: one is cleared once every CTA has come to the barrier behind which the
+  // other is read.
+  auto clear = [&](int* hist) {
+    for (int i = tid; i < BINS / 4; i += THREADS) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  };
+  clear(sh.hist[0]);
+  clear(sh.hist[1]);
+  if (tid == 0) sh.above = sh.inside = 0;
+  __syncthreads();
+
+  // ---- bracket [low, top]
+  uint32_t low = 1, top = 0xffffffffu;
+  if (per * WARPS * BS > SHORT) {
+    for (int q = 0; q < count; q += 4 * 4) {
+      // Four blocks a load, eight lanes each: a sector of the block, another one for every block.
+      uint32_t w[4];
+      int pos[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = q + 4 * i + (lane >> 3);
+        const int blk = at < count ? __ldg(table + at) : -1;
+        const int off = ((first + at) * 5 % 16) * 8 + (lane & 7);
+        pos[i] = blk < 0 || (int64_t)blk >= a.num_blocks ? -1 : (first + at) * BS + off;
+        w[i] = pos[i] < 0 ? 0u : __ldg(weights + blk * stride + off);
       }
-      sh.pick_bin = bin;
-      sh.pick_left = rest;
-      sh.pick_all = rest == size;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (pos[i] >= lo && pos[i] < hi) atomicAdd(&sh.hist[0][weight_key(w[i]) >> 21], 1);
+    }
+    sync();
+    scan(sh.hist[0]);
+    if (tid == 0) {
+      sh.bin[0] = BINS - 1;  // (the last bin: no row is above the bracket)
+      sh.bin[1] = 0;
     }
     __syncthreads();
-    border = border << bits | (uint32_t)sh.pick_bin;
-    left = sh.pick_left;
-    if (sh.pick_all && border > 0) {
-      // Every row of the bin is taken: the border lies below its least weight.
-      border = (border << shift) - 1;
-      left = 0;
-      break;
-    }
-    // (What a CTA writes next, the next digit's scan, comes behind that digit's barrier.)
+    const float m = (float)sh.total, p = (float)want / (float)(hi - lo);
+    const float margin = 3.5f * sqrtf(m * p * (1.f - p)) + 2.f;
+    const int upper = (int)floorf(m * p - margin), lower = (int)ceilf(m * p + margin);
+    if (upper >= 1) find(upper, [&](int bin, int, int) { sh.bin[0] = bin; });
+    if (lower <= sh.total) find(lower, [&](int bin, int, int) { sh.bin[1] = bin; });
+    __syncthreads();
+    top = (uint32_t)sh.bin[0] << 21 | 0x1fffffu;
+    low = max(1u, (uint32_t)sh.bin[1] << 21);
   }
 
-  // `left` rows of exactly the border's weight go, lowest position first.
+  // ---- masks of the rows above the bracket and inside it
+  uint32_t border = 0;  // rows above it are taken
+  int rest = 0;         // and so many of those that equal it
+  {
+    int above = 0, inside = 0;
+    const uint32_t width = top - low;
+    stream([&](int q, uint4 k) {
+      const uint4 high = mask(k, [&](uint32_t x) { return x > top; });
+      const uint4 in = mask(k, [&](uint32_t x) { return x - low <= width; });
+      above += size(high);
+      inside += size(in);
+      if (lane == 0) {
+        list.take[own + q] = high;
+        list.other[own + q] = in;
+      }
+    });
+    if (lane == 0) {
+      atomicAdd(&sh.above, above);
+      sh.wequal[warp] = inside;
+    }
+  }
+  __syncthreads();
+  // ---- the list, and the histogram of its first digit; a word of the masks per lane
+  int shift = max(0, 32 - __clz(top - low) - 11);
+  {
+    int at = lane < WARPS ? sh.wequal[lane] : 0;
+    const int inside = __reduce_add_sync(0xffffffffu, at);
+    at = __reduce_add_sync(0xffffffffu, lane < warp ? at : 0);
+    if (tid == 0) sh.inside = inside;
+    if (inside <= LIST) {
+      uint32_t* words = reinterpret_cast<uint32_t*>(list.other + own);
+      for (int w0 = 0; w0 < 4 * count; w0 += 32) {
+        const int w = w0 + lane;
+        uint32_t bits = 0;
+        if (w < 4 * count) {
+          bits = words[w];
+          words[w] = 0;
+        }
+        int all;
+        int to = at + before(__popc(bits), all);
+        at += all;
+        const int blk = bits ? __ldg(table + w / 4) : 0;
+        const bool good = blk >= 0 && (int64_t)blk < a.num_blocks;
+        const uint32_t* from = weights + (good ? blk : 0) * stride + w % 4;
+        while (bits) {
+          uint32_t key[4];
+          int bit[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bit[i] = __ffs((int)bits) - 1;
+            bits &= bits - 1;
+            key[i] = bit[i] >= 0 && good ? __ldg(from + 4 * bit[i]) : 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (bit[i] >= 0) {
+              const uint32_t k = good ? weight_key(key[i]) : BAD;
+              list.key[to] = k;
+              list.place[to] = 32 * (4 * own + w) + bit[i];
+              ++to;
+              atomicAdd(&sh.hist[1][(k - low) >> shift], 1);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  sync();
+  bool found;
+  {
+    int over = 0, sum_above = 0;
+    const Shared* s = C == 1 ? &sh : theirs(&sh, lane);
+    if (lane < C) {
+      over = s->inside > LIST;
+      sum_above = s->above;
+    }
+    sum_above = __reduce_add_sync(0xffffffffu, sum_above);
+    int left = want - sum_above;
+    scan(sh.hist[1]);
+    __syncthreads();
+    // (All CTAs of the cluster come to the same answer.)
+    found = !__any_sync(0xffffffffu, over) && left >= 1 && left <= sh.total;
+    if (found) {
+      // ---- the border among the list
+      const int inside = sh.inside;
+      uint32_t base = low;
+      for (int round = 1;; ++round) {
+        find(left, [&](int bin, int r, int size) {
+          sh.bin[0] = bin;
+          sh.rest = r;
+          sh.all = r == size;
+        });
+        __syncthreads();
+        base += (uint32_t)sh.bin[0] << shift;
+        left = sh.rest;
+        if (sh.all) {  // every row of the bin is taken: the border lies below its least weight
+          border = base - 1;
+          left = 0;
+          break;
+        }
+        if (shift == 0) {
+          border = base;
+          break;
+        }
+        const uint32_t width = (1u << shift) - 1;
+        shift = max(0, shift - 11);
+        int* hist = sh.hist[(round + 1) & 1];
+        clear(hist);
+        __syncthreads();
+        for (int i = tid; i < inside; i += THREADS) {
+          const uint32_t d = list.key[i] - base;
+          if (d <= width) atomicAdd(hist + (d >> shift), 1);
+        }
+        sync();
+        scan(hist);
+        __syncthreads();
+      }
+      rest = left;
+      for (int i = tid; i < inside; i += THREADS) {
+        const uint32_t k = list.key[i], p = list.place[i];
+        uint4* to = k > border ? list.take : list.other;
+        if (k > border || (k == border && rest > 0))
+          atomicOr(reinterpret_cast<uint32_t*>(to) + p / 32, 1u << (p % 32));
+      }
+      __syncthreads();
+    }
+  }
+
+  if (!found) {
+    // ---- every digit over all weights
+    sync();  // nobody reads the histograms any more
+    clear(sh.hist[0]);
+    __syncthreads();
+    rest = want;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int down = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      int* hist = sh.hist[pass & 1];
+      stream([&](int, uint4 k) {
+        auto add = [&](uint32_t x) {
+          if (x != ABSENT && (pass == 0 || x >> (down + bits) == border))
+            atomicAdd(hist + (x >> down & ((1 << bits) - 1)), 1);
+        };
+        add(k.x);
+        add(k.y);
+        add(k.z);
+        add(k.w);
+      });
+      sync();
+      clear(sh.hist[~pass & 1]);
+      scan(hist);
+      find(rest, [&](int bin, int r, int) {
+        sh.bin[0] = bin;
+        sh.rest = r;
+      });
+      __syncthreads();
+      border = border << bits | (uint32_t)sh.bin[0];
+      rest = sh.rest;
+      __syncthreads();
+    }
+    stream([&](int q, uint4 k) {
+      const uint4 high = mask(k, [&](uint32_t x) { return x > border; });
+      const uint4 same = mask(k, [&](uint32_t x) { return x == border; });
+      if (lane == 0) {
+        list.take[own + q] = high;
+        list.other[own + q] = same;
+      }
+    });
+    __syncwarp();
+  }
+
+  // ---- positions: a word of the masks per lane, its positions in order; `rest` rows of exactly the
+  // border's weight go, lowest first
   int above = 0, equal = 0;
-  each([&](int, uint4 k) {
-    above += (k.x > border) + (k.y > border) + (k.z > border) + (k.w > border);
-    equal += (k.x == border) + (k.y == border) + (k.z == border) + (k.w == border);
-  });
+  for (int q = lane; q < count; q += 32) {
+    above += size(list.take[own + q]);
+    if (rest > 0) equal += size(list.other[own + q]);
+  }
   above = __reduce_add_sync(0xffffffffu, above);
   equal = __reduce_add_sync(0xffffffffu, equal);
+  __syncthreads();  // (the sums below were counts of the list)
   if (lane == 0) {
     sh.wabove[warp] = above;
     sh.wequal[warp] = equal;
@@ -221,48 +447,44 @@ __global__ void __launch_bounds__(THREADS, 1) select_rows_kernel(const __grid_co
     if (warp == 0) {
       const int x = __reduce_add_sync(0xffffffffu, at), y = __reduce_add_sync(0xffffffffu, eq);
       if (lane == 0) {
-        sh.above = x;
+        sh.taken = x;
         sh.equal = y;
       }
     }
     sync();
   }
   if (lane >= warp) at = eq = 0;
-  if (C > 1 && lane < rank) {
-    at += *cg::this_cluster().map_shared_rank(&sh.above, lane);
-    eq += *cg::this_cluster().map_shared_rank(&sh.equal, lane);
+  if (C > 1) {
+    const int *t = theirs(&sh.taken, lane), *e = theirs(&sh.equal, lane);
+    if (lane < rank) {
+      at += *t;
+      eq += *e;
+    }
   }
   at = __reduce_add_sync(0xffffffffu, at);  // rows above the border, and at it, before this warp's
   eq = __reduce_add_sync(0xffffffffu, eq);
-  at += a.num_sink + min(eq, left);
-  const unsigned lower = (1u << lane) - 1;
-  each([&](int q, uint4 k) {
-    unsigned take = (k.x > border) | (k.y > border) << 1 | (k.z > border) << 2 | (k.w > border) << 3;
-    const unsigned same = (k.x == border) | (k.y == border) << 1 | (k.z == border) << 2 | (k.w == border) << 3;
-    if (__any_sync(0xffffffffu, same)) {
-      int rankq = eq;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned all = __ballot_sync(0xffffffffu, same >> j & 1);
-        rankq += __popc(all & lower);
-        eq += __popc(all);
+  at += a.num_sink + min(eq, rest);
+  for (int w0 = 0; w0 < 4 * count; w0 += 32) {
+    const int w = w0 + lane;
+    const bool mine = w < 4 * count;
+    uint32_t bits = mine ? in_order(list.take[own + w / 4], w % 4) : 0;
+    int all;
+    if (eq < rest) {
+      uint32_t same = mine ? in_order(list.other[own + w / 4], w % 4) : 0;
+      int places = rest - eq - before(__popc(same), all);
+      eq += all;
+      for (; same && places > 0; --places) {
+        bits |= same & (0u - same);
+        same &= same - 1;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (same >> j & 1 && rankq++ < left) take |= 1u << j;
+      __syncwarp();
     }
-    int to = at;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned all = __ballot_sync(0xffffffffu, take >> j & 1);
-      to += __popc(all & lower);
-      at += __popc(all);
-    }
-    const int pos = (first + q) * BS + 4 * lane;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (take >> j & 1) out[to++] = pos + j;
-  });
+    int to = at + before(__popc(bits), all);
+    at += all;
+    const int pos = first * BS + 32 * w;
+    for (; bits; bits &= bits - 1) out[to++] = pos + __ffs((int)bits) - 1;
+    __syncwarp();
+  }
   if (C > 1) sync();  // no CTA goes while another may read its shared memory
 }
 
@@ -270,20 +492,17 @@ __global__ void __launch_bounds__(THREADS, 1) select_rows_kernel(const __grid_co
 
 cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int num_sms) {
   const int64_t rows = (int64_t)a.B * a.Hkv;
-  // Cluster width: CTAs for every SM where the rows alone are too few, with two blocks or more a
-  // warp; two CTAs per SM where the keys of a row do not fit one. Measured on GB300 (us for 1, 2, 4,
-  // 8 CTAs a row): 8 rows of 256 blocks 16.0, 13.7, 11.5, 13.8; 16 of 8,192 578, 289, 147, 142; 128
-  // of up to 1,024 72, 55, 68, 138; 512 of up to 256 42, 68, 138, 367.
+  // Cluster width: room for the rows inside the bracket (some 13 % of 256 blocks), and CTAs for every
+  // SM where the rows are few, of four blocks a warp or more. Measured on GB300 (us for 1, 2, 4, 8 CTAs
+  // a row): 8 rows of 256 blocks 15.5, 12.9, 12.6, 15.9; 64 of 64 10.2, 12.5, 20; 512 of up to 256 31,
+  // 44, 83, 258; 128 of up to 1,024 145 (the lists overflow), 46, 46, 94; 16 of 8,192 535, 535, 285, 68.
   int C = 1;
-  while (C < MAX_CLUSTER && a.max_blocks > 2 * WARPS * C &&
-         rows * 2 * C <= (a.max_blocks > MAX_KEPT * C ? 2 : 1) * (int64_t)num_sms)
+  while (C < MAX_CLUSTER && (a.max_blocks > 256 * C || (a.max_blocks > 4 * WARPS * C && rows * 2 * C <= num_sms)))
     C *= 2;
-  // Blocks of a warp whose keys stay in shared memory.
-  int keep = (a.max_blocks + C * WARPS - 1) / (C * WARPS);
-  if (keep > MAX_KEPT / WARPS) keep = MAX_KEPT / WARPS;
-  const size_t smem = (size_t)keep * WARPS * BS * 4;
-  const cudaError_t e =
-      cudaFuncSetAttribute(select_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_KEPT * BS * 4);
+  const int cta_blocks = (a.max_blocks + C * WARPS - 1) / (C * WARPS) * WARPS;
+  const size_t smem = (size_t)cta_blocks * 2 * sizeof(uint4) + LIST * 8;
+  const cudaError_t e = cudaFuncSetAttribute(select_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             MAX_PER_CTA * 2 * (int)sizeof(uint4) + LIST * 8);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C));
@@ -299,7 +518,7 @@ cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_rows_kernel, a, keep);
+  return cudaLaunchKernelEx(&cfg, select_rows_kernel, a, cta_blocks);
 }
 
 }  // namespace pkv

@@ -54,8 +54,9 @@ def test_accumulate_refusals(kw, code, word):
     (dict(block_size=64), -2, b"block_size"),
     (dict(sink=5, recent=6), -1, b"num_keep"),
     (dict(sink=2**31 - 1, recent=2**31 - 1, keep=2**31 - 1), -1, b"num_keep"),
-    (dict(max_blocks=1 << 24), -2, b"int32"),
-    (dict(B=1 << 30), -2, b"int32"),
+    (dict(max_blocks=32769), -2, b"max_blocks"),
+    (dict(num_blocks=1 << 24), -2, b"int32"),
+    (dict(B=1 << 27), -2, b"int32"),
     (dict(weights=None), -1, b"null"),
     (dict(kept=P + 4), -1, b"aligned"),
     (dict(kept=2 * P + 512), -1, b"overlaps"),

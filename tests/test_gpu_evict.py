@@ -249,6 +249,49 @@ def test_select_rows_of_long_sequences(B, hkv, n, keep):
             np.testing.assert_array_equal(got[b, g, :len(want)], want)
 
 
+@pytest.mark.parametrize("kind", ["few", "one", "special", "close", "ascending", "descending", "period", "two levels",
+                                  "outliers", "zeros"])
+@pytest.mark.parametrize("n,keep,sink,recent", [(9000, 700, 4, 64), (70001, 9000, 0, 1), (200000, 199000, 1, 0)])
+def test_select_rows_where_a_sample_misleads(kind, n, keep, sink, recent):
+    """Weights of few values, all but equal, in order, or with a period of the blocks': against
+    numpy's sort."""
+    rng = np.random.default_rng(n)
+    lens = [n, n - 129]
+    table, nb = make_table(rng, lens)
+    w = _weights(rng, kind, nb, 2)
+    place = np.zeros(nb * BS)
+    for b in range(2):
+        p = np.arange(lens[b])
+        place[table[b, p // BS] * BS + p % BS] = p
+    place = np.broadcast_to(place.reshape(nb, 1, BS), w.shape)
+    if kind == "ascending":
+        w = place.astype(np.float32)
+    elif kind == "descending":
+        w = (1e6 - place).astype(np.float32)
+    elif kind == "period":      # a block's large weights all in one place
+        w = np.where(place % BS < 8, 1.0 + place % 7, 1e-3 * (1 + place % 11)).astype(np.float32)
+    elif kind == "two levels":  # the border lies between two plateaus
+        w = (1.0 + (rng.random(w.shape) < (keep - sink - recent) / n)).astype(np.float32)
+    elif kind == "outliers":
+        w = np.where(rng.random(w.shape) < 1e-3, 1e30, 1.0 + 1e-6 * rng.random(w.shape)).astype(np.float32)
+    elif kind == "zeros":
+        w = np.where(rng.random(w.shape) < 0.01, rng.random(w.shape), 0.0).astype(np.float32)
+    kept = api.select_rows(torch.as_tensor(np.ascontiguousarray(w)).cuda(), ints(table), ints(lens), keep, sink,
+                           recent)
+    torch.cuda.synchronize()
+    got = kept.cpu().numpy()
+    for b in range(2):
+        m = lens[b]
+        for g in range(2):
+            row = w[table[b, :-(-m // BS)], g].reshape(-1)[:m]
+            # Rows always kept, then NaN, then the others by weight; equal ones by position.
+            rank = np.where(np.isnan(row), 1, 2)
+            rank[:sink] = rank[m - recent:] = 0
+            weight = np.where(rank == 2, row, 0.0)
+            want = np.sort(np.lexsort((np.arange(m), -weight, rank))[:keep])
+            np.testing.assert_array_equal(got[b, g, :len(want)], want)
+
+
 def test_select_rows_of_bad_blocks_and_lengths():
     rng = np.random.default_rng(3)
     lens = [500, 300]
