@@ -99,6 +99,21 @@ def _check_gpu(index, **tensors) -> None:
             raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
+def _all_as(index, *specs) -> bool:
+    """Whether every (tensor, dtype, shape) is a contiguous tensor of that type and shape on GPU
+    `index`. Where one is not, the checks that name it take longer than a small kernel."""
+    if index < 0:
+        return False
+    try:
+        for t, dtype, shape in specs:
+            if (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+                    or not t.is_contiguous()):
+                return False
+    except AttributeError:  # no tensor
+        return False
+    return True
+
+
 def _launch_stream(index, stream=None):
     """The raw stream of a launch on device `index`, which must be the current one."""
     current = torch.cuda.current_device()
@@ -735,7 +750,19 @@ def paged_attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
 
 
 def _fp4_cache(k_cache, v_cache, k_scale, v_scale):
-    """(num_blocks, H_kv, block_size) of a 4-bit cache after checking its four arrays."""
+    """(num_blocks, H_kv, block_size, GPU index) of a 4-bit cache after checking its four arrays
+    (v_cache and v_scale None: the two of K)."""
+    if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 and k_cache.shape[3] == 64:
+        nb, hkv, bs, _ = codes = k_cache.shape
+        scales = (nb, hkv, bs, 8)
+        index = k_cache.get_device()
+        u8 = torch.uint8
+        if v_cache is None:
+            if _all_as(index, (k_cache, u8, codes), (k_scale, u8, scales)):
+                return nb, hkv, bs, index
+        elif _all_as(index, (k_cache, u8, codes), (v_cache, u8, codes), (k_scale, u8, scales),
+                     (v_scale, u8, scales)):
+            return nb, hkv, bs, index
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"),
                  (v_scale, "v_scale")):
         if t is not None:
@@ -748,7 +775,23 @@ def _fp4_cache(k_cache, v_cache, k_scale, v_scale):
         check_shape(v_cache, (nb, hkv, bs, 64), "v_cache")
         check_shape(v_scale, (nb, hkv, bs, 8), "v_scale")
     check_shape(k_scale, (nb, hkv, bs, 8), "k_scale")
-    return nb, hkv, bs
+    index = k_cache.get_device()
+    _check_gpu(index, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    return nb, hkv, bs, index
+
+
+def _tables(index, B, block_table, seq_lens, **more):
+    """_table_and_lens, further int32 vectors of B entries, and that all are on GPU `index`."""
+    i32, lens = torch.int32, (B,)
+    width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() else 0
+    if _all_as(index, (block_table, i32, (B, width)), (seq_lens, i32, lens),
+               *((t, i32, lens) for t in more.values())):
+        return
+    _table_and_lens(block_table, seq_lens, B)
+    for n, t in more.items():
+        _dev_i32(t, n)
+        check_shape(t, lens, n)
+    _check_gpu(index, block_table=block_table, seq_lens=seq_lens, **more)
 
 
 def kv_cache_write_fp4(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, dev_status=None,
@@ -757,16 +800,14 @@ def kv_cache_write_fp4(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, d
 
     k_cache / v_cache [nb, H_kv, bs, 64] uint8, k_scale / v_scale [nb, H_kv, bs, 8] uint8;
     k / v [T, H_kv, 128] bf16 (slices of one projection's output will do)."""
-    nb, hkv, bs = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, bs, index = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
     _dev_i32(slot_mapping, "slot_mapping")
     T = slot_mapping.numel()
     kh, ks = _rope_rows(k, T, 128, "k")
     vh, vs = _rope_rows(v, T, 128, "v")
     if kh != hkv or vh != hkv:
         raise ValueError(f"k and v must have the cache's {hkv} heads")
-    index = k_cache.get_device()
-    _check_gpu(index, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, k=k, v=v,
-               slot_mapping=slot_mapping)
+    _check_gpu(index, k=k, v=v, slot_mapping=slot_mapping)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, k_cache.device)
@@ -780,7 +821,7 @@ def kv_cache_read_fp4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=No
                       dev_status=None, stream=None):
     """Rows of a 4-bit cache widened to bf16 (exactly): returns (k, v), [T, H_kv, 128] each
     (`k_out` and `v_out` if given). A negative slot gives a row of zeros."""
-    nb, hkv, bs = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, bs, index = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
     _dev_i32(slot_mapping, "slot_mapping")
     T = slot_mapping.numel()
     shape = (T, hkv, 128)
@@ -788,12 +829,12 @@ def kv_cache_read_fp4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=No
         k_out = _empty(shape, torch.bfloat16, k_cache.device, stream)
     if v_out is None:
         v_out = _empty(shape, torch.bfloat16, k_cache.device, stream)
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _dev_bf16(t, n)
-        check_shape(t, shape, n)
-    index = k_cache.get_device()
-    _check_gpu(index, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, slot_mapping=slot_mapping,
-               k_out=k_out, v_out=v_out)
+    if not _all_as(index, (k_out, torch.bfloat16, shape), (v_out, torch.bfloat16, shape)):
+        for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+            _dev_bf16(t, n)
+            check_shape(t, shape, n)
+        _check_gpu(index, k_out=k_out, v_out=v_out)
+    _check_gpu(index, slot_mapping=slot_mapping)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, k_cache.device)
@@ -814,24 +855,26 @@ def paged_attention_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     causal); returns out in q's shape (and fills lse, the shape without its last axis). The
     workspace is decode_spec_workspace_size's."""
     B, Q, H, d = _query_rows(q)
-    nb, hkv, bs = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
-    _table_and_lens(block_table, seq_lens, B)
-    index = q.get_device()
-    _check_gpu(index, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-               block_table=block_table, seq_lens=seq_lens)
+    nb, hkv, bs, index = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    _check_gpu(index, q=q)
+    _tables(index, B, block_table, seq_lens)
     raw = _launch_stream(index, stream)
-    dev = q.device
-    out = out_buffer(out, q.shape, out_dtype, dev, stream=stream)
-    lse_buffer(lse, tuple(q.shape[:-1]), dev)
-    status_buffer(dev_status, dev)
-    code = PKV_F32 if out.dtype == torch.float32 else PKV_BF16
+    shape = q.shape
+    if out is None or not _all_as(index, (out, torch.bfloat16, shape)):
+        out = out_buffer(out, shape, out_dtype, q.device, stream=stream)
+    if lse is not None and not _all_as(index, (lse, torch.float32, shape[:-1])):
+        lse_buffer(lse, tuple(shape[:-1]), q.device)
+    if dev_status is not None:
+        status_buffer(dev_status, q.device)
+    code = PKV_F32 if out.dtype is torch.float32 else PKV_BF16
+    lib = load()
     workspace, ws_bytes = workspace_buffer(
-        workspace, decode_spec_workspace_size(B, Q, H, hkv, d), dev, stream=stream)
-    check(load().pkv_paged_attention_decode_fp4(
+        workspace, lib.pkv_decode_spec_workspace_size(B, Q, H, hkv, d), q.device, stream=stream)
+    check(lib.pkv_paged_attention_decode_fp4(
         out.data_ptr(), code, _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), B, Q, H, hkv, d, bs, nb, float(scale), int(window),
-        workspace.data_ptr(), ws_bytes, _ptr(dev_status), raw), "pkv_paged_attention_decode_fp4")
+        seq_lens.data_ptr(), B, Q, H, hkv, d, bs, nb, float(scale), _int32(window, "window"),
+        workspace.data_ptr(), ws_bytes,        _ptr(dev_status), raw), "pkv_paged_attention_decode_fp4")
     return out
 
 
@@ -1049,31 +1092,34 @@ def accumulate_attention_weights(weights, q, lse, k_cache, block_table, seq_lens
     uint8 k_scale). The newest num_fresh[b] rows of a sequence start over at zero, the others'
     sums are multiplied by `decay` first."""
     B, Q, H, d = _query_rows(q)
-    _f32_dev(weights, "weights")
-    _f32_dev(lse, "lse")
-    check_shape(lse, tuple(q.shape[:-1]), "lse")
+    index = q.get_device()
     if k_scale is None:
         _dev_bf16(k_cache, "k_cache")
         fmt = KEYS_BF16
         nb, bs, hkv, dk = _cache_dims(k_cache, "k_cache")
+        _check_gpu(index, k_cache=k_cache)
     elif isinstance(k_scale, torch.Tensor) and k_scale.dtype == torch.uint8:
-        nb, hkv, bs = _fp4_cache(k_cache, None, k_scale, None)
+        nb, hkv, bs, at = _fp4_cache(k_cache, None, k_scale, None)
         fmt, dk = KEYS_FP4, 128
+        if at != index:
+            raise ValueError(f"k_cache is on cuda:{at}, expected cuda:{index}")
     else:
         _fp8_cache(k_cache, "k_cache")
         _f32_dev(k_scale, "k_scale")
         fmt = KEYS_FP8
         nb, bs, hkv, dk = _cache_dims(k_cache, "k_cache")
         check_shape(k_scale, (nb, hkv, bs), "k_scale")
+        _check_gpu(index, k_cache=k_cache, k_scale=k_scale)
     if dk != d:
         raise ValueError(f"k_cache head_dim {dk} differs from q's {d}")
-    check_shape(weights, (nb, hkv, bs), "weights")
-    _table_and_lens(block_table, seq_lens, B)
-    _dev_i32(num_fresh, "num_fresh")
-    check_shape(num_fresh, (B,), "num_fresh")
-    index = q.get_device()
-    _check_gpu(index, weights=weights, lse=lse, k_cache=k_cache, k_scale=k_scale,
-               block_table=block_table, seq_lens=seq_lens, num_fresh=num_fresh)
+    rows = q.shape[:-1]
+    if not _all_as(index, (weights, torch.float32, (nb, hkv, bs)), (lse, torch.float32, rows)):
+        _f32_dev(weights, "weights")
+        _f32_dev(lse, "lse")
+        check_shape(lse, tuple(rows), "lse")
+        check_shape(weights, (nb, hkv, bs), "weights")
+        _check_gpu(index, weights=weights, lse=lse)
+    _tables(index, B, block_table, seq_lens, num_fresh=num_fresh)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, q.device)
@@ -1100,7 +1146,8 @@ def select_rows(weights, block_table, seq_lens, num_keep: int, num_sink: int = 0
     nb, hkv, bs = weights.shape
     _dev_i32(seq_lens, "seq_lens")
     B = seq_lens.numel()
-    _table_and_lens(block_table, seq_lens, B)
+    index = weights.get_device()
+    _tables(index, B, block_table, seq_lens)
     num_keep = _int32(num_keep, "num_keep")
     num_sink, num_recent = _int32(num_sink, "num_sink"), _int32(num_recent, "num_recent")
     if num_keep < 1:
@@ -1108,11 +1155,10 @@ def select_rows(weights, block_table, seq_lens, num_keep: int, num_sink: int = 0
     shape = (B, hkv, num_keep)
     if out is None:
         out = _empty(shape, torch.int32, weights.device, stream)
-    else:
+    elif not _all_as(index, (out, torch.int32, shape)):
         _dev_i32(out, "out")
         check_shape(out, shape, "out")
-    index = weights.get_device()
-    _check_gpu(index, block_table=block_table, seq_lens=seq_lens, out=out)
+        _check_gpu(index, out=out)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, weights.device)
@@ -1174,8 +1220,10 @@ def compact_rows(kept, block_table, row_caches=(), head_caches=(), new_block_tab
         if B and K > width * bs:
             raise ValueError(f"{K} rows do not fit in new_block_table's {width} blocks of {bs}")
     index = kept.get_device()
-    _check_gpu(index, block_table=block_table, new_block_table=new_block_table,
-               **{f"cache {i}": t for i, t in enumerate(caches)})
+    _check_gpu(index, block_table=block_table, new_block_table=new_block_table)
+    for i, t in enumerate(caches):
+        if t.get_device() != index:
+            raise ValueError(f"cache {i} is on {t.device}, expected cuda:{index}")
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, kept.device)
