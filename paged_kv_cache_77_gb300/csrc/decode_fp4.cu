@@ -29,6 +29,7 @@
 #include "launch.h"
 #include "mma_f16.cuh"
 #include "pdl.cuh"
+#include "piece_walk.cuh"
 #include "query_f16.cuh"
 #include "row_cursor.cuh"
 
@@ -38,7 +39,7 @@
 namespace pkv {
 namespace {
 
-constexpr int D = 128, TILE = 128, SUB = 32;     // tokens of a block, and of a piece of it
+constexpr int D = 128;
 constexpr int CODES = SUB * fp4::kCodeBytes;     // 2048
 constexpr int SCALES = SUB * fp4::kScaleBytes;   // 256
 constexpr int STAGE = 2 * (CODES + SCALES);      // K codes, V codes, K scales, V scales
@@ -69,44 +70,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
 }
-
-// Rows 2c and 2c + 1 of a product's 8 rows are tokens 0 3, 1 2, 4 7, 5 6 (and 8 further on): K's
-// 16-byte loads, 8 lanes at a time, then meet two rows of different banks, V's 8-byte loads rows
-// that share them by twos only.
-__device__ __forceinline__ int even_row(int c) { return (c & 1) | (c & 2) << 1; }
-__device__ __forceinline__ int token_of(int r) { return even_row(r >> 1) ^ ((r & 1) ? 3 : 0); }
-
-// A warp's walk over its run, segment by segment (a segment is the blocks that the rows of one
-// sequence and kv head see). The run is counted in pieces of 32 tokens of whole blocks; of the last
-// block only the pieces that hold tokens are visited.
-struct Walk {
-  int b, g, len;
-  int pos, stop;   // next position, and where the run leaves the segment or the tokens end
-  int todo;        // pieces of the run from this segment's first visit on
-  int padded;      // of them in this segment
-  bool ends;       // whether the segment's last token is in the run
-  __device__ __forceinline__ void enter(int at) {
-    const int end = (len + TILE - 1) & ~(TILE - 1);
-    pos = at;
-    padded = min((end - at) / SUB, todo);
-    ends = padded * SUB == end - at;
-    stop = min(at + padded * SUB, (len + SUB - 1) & ~(SUB - 1));
-  }
-  // The next segment of the run; false behind its end.
-  __device__ __forceinline__ bool next(const DenseRows& rows, int B, int Hkv) {
-    todo -= padded;
-    if (todo <= 0) return false;
-    if (++g == Hkv) {
-      g = 0;
-      do {
-        if (++b >= B) return false;
-        len = rows.len(b);
-      } while (len == 0);
-    }
-    enter(rows.blocks(len).jlo * TILE);
-    return true;
-  }
-};
 
 // A running softmax over part of a segment, spread over the lanes of a warp: lane 4 g + c has the
 // query rows 8 n + 2 c and 8 n + 2 c + 1 (x = 0, 1), of their outputs channels 16 g .. + 15
@@ -431,8 +394,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
   if (t0 >= t1) return;
 
   // This warp's run: pieces u0 .. u1 - 1 of the CTA's.
-  constexpr int PER = TILE / SUB;
-  const int64_t u0 = (t1 - t0) * PER * warp / WARPS, u1 = (t1 - t0) * PER * (warp + 1) / WARPS;
+  const int64_t u0 = Walk::run(t1 - t0, warp, WARPS), u1 = Walk::run(t1 - t0, warp + 1, WARPS);
   const int g = lane >> 2, c = lane & 3, R = a.n_rep * a.q_len;
   Running<NT> r;
   Walk cur = {};
@@ -440,16 +402,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
   bool open = false;   // whether it goes on behind the run, and is this warp's to finish
   int left = kNothing;
   if (u0 < u1) {
-    {
-      TileCursor t;
-      cursor_seek_warp(t, rows, a.B, a.Hkv, t0 + u0 / PER, t1);
-      cur.b = t.b;
-      cur.g = t.g;
-      cur.len = t.len;
-      cur.todo = (int)(u1 - u0);
-      begun = t.j == 0 && u0 % PER == 0;
-      cur.enter((t.jlo + t.j) * TILE + (int)(u0 % PER) * SUB);
-    }
+    begun = cur.seek(rows, a.B, a.Hkv, t0, t1, u0, u1);
     // ---- the ring: the run's it-th visited piece is in stage it % STAGES, one group of
     // asynchronous copies each. A lane copies 16 bytes of every eighth row of the codes, and 16 bytes
     // of the scales of K (lanes 0 to 15) or V.
