@@ -283,11 +283,13 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   // The pieces' workspace slots, found before the wait (they depend on the inputs
   // only), so that after it every piece's loads are issued at once.
   constexpr int kMaxPieces = 8;
+  // A CTA without a tile has no piece; with tiles for all of them there is none such to look for.
+  auto without = [&](int64_t i) { return T < G && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G); };
   auto slot_of = [&](int64_t i) { return (i == i0) ? (int64_t)seg : (int64_t)a.B * a.Hkv + i; };
   int64_t slots[kMaxPieces];
   int np = 0;
   for (int64_t i = i0; n > 0 && i <= i1; ++i) {
-    if (i > i0 && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G)) continue;  // empty CTA
+    if (i > i0 && without(i)) continue;
     if (np < kMaxPieces) slots[np] = slot_of(i);
     ++np;
   }
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
     // More pieces than registers hold (segments far longer than a CTA's share): first the largest
     // log-sum-exp, a piece per lane, then the sums in the pieces' order, kMaxPieces at a time.
     for (int64_t i = i0 + lane; i <= i1; i += 32) {
-      if (i > i0 && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G)) continue;
+      if (i > i0 && without(i)) continue;
       mx = fmaxf(mx, a.ws_lse[slot_of(i) * n_rep + h]);
     }
 #pragma unroll
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
       bool has[kMaxPieces];
 #pragma unroll
       for (int p = 0; p < kMaxPieces; ++p) {
-        has[p] = i + p <= i1 && (i + p == i0 || cta_tile_start(i + p + 1, T, G) != cta_tile_start(i + p, T, G));
+        has[p] = i + p <= i1 && (i + p == i0 || !without(i + p));
         if (has[p]) {
           const int64_t slot = slot_of(i + p);
           l2[p] = a.ws_lse[slot * n_rep + h];
