@@ -165,6 +165,10 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
     all = __shfl_sync(0xffffffffu, incl, 31);
     return incl - x;
   };
+  // Lanes take words of the masks, or bytes of them where a warp has a block or two: lane or item w of a
+  // warp's words, 32 >> fine bits each, as bits of the whole word.
+  const int fine = per <= 2 ? 2 : 0;
+  auto share = [&](uint32_t word, int w) { return fine ? word & 0xffu << 8 * (w & 3) : word; };
   // Behind a sync(): EACH bins of a histogram, from bin BINS - 1 - EACH * tid down, summed over the
   // cluster, and how many rows lie in the bins above them.
   constexpr int EACH = BINS / THREADS;
@@ -287,19 +291,19 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
     if (tid == 0) sh.inside = inside;
     if (inside <= LIST) {
       uint32_t* words = reinterpret_cast<uint32_t*>(list.other + own);
-      for (int w0 = 0; w0 < 4 * count; w0 += 32) {
+      for (int w0 = 0; w0 < 4 * count << fine; w0 += 32) {
         const int w = w0 + lane;
-        uint32_t bits = 0;
-        if (w < 4 * count) {
-          bits = words[w];
-          words[w] = 0;
-        }
+        const bool mine = w < 4 * count << fine;
+        uint32_t bits = mine ? share(words[w >> fine], w) : 0;
+        __syncwarp();
+        if (mine) words[w >> fine] = 0;
         int all;
         int to = at + before(__popc(bits), all);
         at += all;
-        const int blk = bits ? __ldg(table + w / 4) : 0;
+        const int word = w >> fine;
+        const int blk = bits ? __ldg(table + word / 4) : 0;
         const bool good = blk >= 0 && (int64_t)blk < a.num_blocks;
-        const uint32_t* from = weights + (good ? blk : 0) * stride + w % 4;
+        const uint32_t* from = weights + (good ? blk : 0) * stride + word % 4;
         while (bits) {
           uint32_t key[4];
           int bit[4];
@@ -312,9 +316,10 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (bit[i] >= 0) {
-              const uint32_t k = good ? weight_key(key[i]) : BAD;
+              uint32_t k = key[i] | 0x80000000u;
+              if (key[i] > 0x7f800000u || !good) k = good ? weight_key(key[i]) : BAD;
               list.key[to] = k;
-              list.place[to] = 32 * (4 * own + w) + bit[i];
+              list.place[to] = 32 * (4 * own + word) + bit[i];
               ++to;
               atomicAdd(&sh.hist[1][(k - low) >> shift], 1);
             }
@@ -464,13 +469,13 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
   at = __reduce_add_sync(0xffffffffu, at);  // rows above the border, and at it, before this warp's
   eq = __reduce_add_sync(0xffffffffu, eq);
   at += a.num_sink + min(eq, rest);
-  for (int w0 = 0; w0 < 4 * count; w0 += 32) {
-    const int w = w0 + lane;
-    const bool mine = w < 4 * count;
-    uint32_t bits = mine ? in_order(list.take[own + w / 4], w % 4) : 0;
+  for (int w0 = 0; w0 < 4 * count << fine; w0 += 32) {
+    const int w = w0 + lane, word = w >> fine;
+    const bool mine = w < 4 * count << fine;
+    uint32_t bits = mine ? share(in_order(list.take[own + word / 4], word % 4), w) : 0;
     int all;
     if (eq < rest) {
-      uint32_t same = mine ? in_order(list.other[own + w / 4], w % 4) : 0;
+      uint32_t same = mine ? share(in_order(list.other[own + word / 4], word % 4), w) : 0;
       int places = rest - eq - before(__popc(same), all);
       eq += all;
       for (; same && places > 0; --places) {
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
     }
     int to = at + before(__popc(bits), all);
     at += all;
-    const int pos = first * BS + 32 * w;
+    const int pos = first * BS + 32 * word;
     for (; bits; bits &= bits - 1) out[to++] = pos + __ffs((int)bits) - 1;
     __syncwarp();
   }
