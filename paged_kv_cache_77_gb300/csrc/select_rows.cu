@@ -31,7 +31,7 @@ namespace pkv {
 namespace {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32, BS = 128, BINS = 2048;
-constexpr int FLIGHT = 4;        // blocks of a warp in flight
+constexpr int FLIGHT = 2;        // blocks of a warp in flight while as many are worked on
 constexpr int LIST = 5120;       // rows of a CTA inside the bracket
 constexpr int SHORT = 1024;      // rows of a CTA that need no bracket
 constexpr int MAX_CLUSTER = 8;
@@ -121,23 +121,36 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
   const int64_t stride = (int64_t)a.Hkv * BS;  // from block to block
   // What another CTA of the cluster has where this one has *mine; r is clamped to the cluster.
   auto theirs = [&](auto* mine, int r) { return cg::this_cluster().map_shared_rank(mine, min(r, C - 1)); };
-  // The warp's blocks in order, FLIGHT at a time: f(block, its four keys of this lane).
+  // The warp's blocks in order: f(block, its four keys of this lane). FLIGHT blocks are loaded while
+  // those before them are worked on.
   auto stream = [&](auto&& f) {
-    for (int q = 0; q < count; q += FLIGHT) {
-      const int ids = lane < FLIGHT && q + lane < count ? __ldg(table + q + lane) : 0;
-      const bool wrong = ids < 0 || (int64_t)ids >= a.num_blocks;
-      if (wrong) flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
-      const unsigned bad = __ballot_sync(0xffffffffu, wrong);
-      uint4 w[FLIGHT];
-#pragma unroll
-      for (int i = 0; i < FLIGHT; ++i) {
-        const int blk = __shfl_sync(0xffffffffu, ids, i);
-        if (q + i < count && !(bad >> i & 1)) w[i] = __ldg(reinterpret_cast<const uint4*>(weights + blk * stride) + lane);
+    int ids = 0;        // of 32 blocks, lane l's that of block l of them
+    unsigned bad = 0;
+    auto load = [&](int q, uint4(&w)[FLIGHT]) {
+      if (q % 32 == 0) {
+        ids = q + lane < count ? __ldg(table + q + lane) : 0;
+        const bool wrong = ids < 0 || (int64_t)ids >= a.num_blocks;
+        if (wrong) {
+          flag_status(a.dev_status, PKV_DEV_BAD_BLOCK);
+          ids = 0;
+        }
+        bad = __ballot_sync(0xffffffffu, wrong);
       }
 #pragma unroll
       for (int i = 0; i < FLIGHT; ++i) {
+        const int blk = __shfl_sync(0xffffffffu, ids, (q + i) % 32);
+        if (q + i < count) w[i] = __ldg(reinterpret_cast<const uint4*>(weights + blk * stride) + lane);
+      }
+      return bad >> (q % 32);
+    };
+    uint4 now[FLIGHT], then[FLIGHT];
+    unsigned bad_now = load(0, now), bad_then = 0;
+    for (int q = 0; q < count; q += FLIGHT) {
+      if (q + FLIGHT < count) bad_then = load(q + FLIGHT, then);
+#pragma unroll
+      for (int i = 0; i < FLIGHT; ++i) {
         if (q + i >= count) break;
-        uint4 k = bad >> i & 1 ? make_uint4(BAD, BAD, BAD, BAD) : weight_keys(w[i]);
+        uint4 k = bad_now >> i & 1 ? make_uint4(BAD, BAD, BAD, BAD) : weight_keys(now[i]);
         const int start = (first + q + i) * BS, pos = start + 4 * lane;
         if (start < lo || start + BS > hi) {
           if (pos < lo || pos >= hi) k.x = ABSENT;
@@ -147,6 +160,9 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
         }
         f(q + i, k);
       }
+#pragma unroll
+      for (int i = 0; i < FLIGHT; ++i) now[i] = then[i];
+      bad_now = bad_then;
     }
   };
   // The mask of the keys that p holds for.
@@ -269,13 +285,18 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
     stream([&](int q, uint4 k) {
       const uint4 high = mask(k, [&](uint32_t x) { return x > top; });
       const uint4 in = mask(k, [&](uint32_t x) { return x - low <= width; });
-      above += size(high);
-      inside += size(in);
       if (lane == 0) {
         list.take[own + q] = high;
         list.other[own + q] = in;
       }
     });
+    __syncwarp();
+    for (int q = lane; q < count; q += 32) {
+      above += size(list.take[own + q]);
+      inside += size(list.other[own + q]);
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    inside = __reduce_add_sync(0xffffffffu, inside);
     if (lane == 0) {
       atomicAdd(&sh.above, above);
       sh.wequal[warp] = inside;
@@ -498,9 +519,10 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
 cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int num_sms) {
   const int64_t rows = (int64_t)a.B * a.Hkv;
   // Cluster width: room for the rows inside the bracket (some 13 % of 256 blocks), and CTAs for every
-  // SM where the rows are few, of four blocks a warp or more. Measured on GB300 (us for 1, 2, 4, 8 CTAs
-  // a row): 8 rows of 256 blocks 15.5, 12.9, 12.6, 15.9; 64 of 64 10.2, 12.5, 20; 512 of up to 256 31,
-  // 44, 83, 258; 128 of up to 1,024 145 (the lists overflow), 46, 46, 94; 16 of 8,192 535, 535, 285, 68.
+  // SM where the rows are few, of four blocks a warp or more. Measured on GB300 with wider and narrower
+  // clusters (us for 1, 2, 4, 8 CTAs a row): 8 rows of 256 blocks 15.5, 12.9, 12.6, 15.9; 64 of 64 10.2,
+  // 12.5, 20, 42; 512 of up to 256 31, 44, 83, 258; 128 of up to 1,024 145 (the lists overflow), 46, 46,
+  // 94; 16 of 8,192 535, 535, 285, 68, with 16 CTAs 98.
   int C = 1;
   while (C < MAX_CLUSTER && (a.max_blocks > 256 * C || (a.max_blocks > 4 * WARPS * C && rows * 2 * C <= num_sms)))
     C *= 2;
