@@ -645,7 +645,9 @@ int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, con
  *                sum_i sum_h exp(scale q[b,i,h] . k[p,g] - lse[b,i,h])
  * over the query rows i with p <= seq_lens[b] - q_len + i and the H / H_kv heads h of g. lse is
  * what the step's attention returned for these rows (fp32, natural log; of any of the decode
- * calls, or the last rows of a prefill), so the terms of a head and row sum to 1. The
+ * calls, or the last rows of a prefill), so the terms of a head and row sum to 1. That holds for
+ * attention over every visible position: what a window or a selection of blocks leaves out has
+ * no part in its lse, but gets its terms here. The
  * num_fresh[b] newest positions are fresh (none if that is negative, all if it exceeds the
  * length): rows that the step wrote, whose places may hold another request's sums.
  *   weights [num_blocks, H_kv, block_size] fp32: a cache tensor like any other, in the blocks'
@@ -654,8 +656,9 @@ int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, con
  *   k_cache, k_scale by key_format: PKV_KEYS_BF16 [num_blocks, block_size, H_kv, head_dim] bf16
  *     and NULL; PKV_KEYS_FP8 the FP8 cache's codes and scales; PKV_KEYS_FP4 the 4-bit cache's
  * Positions that no row sees hold any bytes; a NaN score makes the position's sum NaN. fp32
- * sums in a fixed order: the same call gives the same bits. A block that two sequences of one
- * call both hold must not be (their sums would race: call once per sequence). Table entries
+ * sums in a fixed order: the same call gives the same bits. No block may be there twice in a
+ * call, in two sequences (their sums would race: call once per sequence) or in one (the null
+ * blocks in front of a sliding window's table). Table entries
  * outside [0, num_blocks) are skipped (PKV_DEV_BAD_BLOCK), lengths past the table clamped
  * (PKV_DEV_BAD_LENGTH). weights may not overlap anything the call reads
  * (PKV_ERR_INVALID_ARG). Supported: head_dim 128, block_size 128, H % H_kv == 0,

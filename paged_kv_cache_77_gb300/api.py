@@ -874,7 +874,7 @@ def paged_attention_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_tabl
         out.data_ptr(), code, _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
         seq_lens.data_ptr(), B, Q, H, hkv, d, bs, nb, float(scale), _int32(window, "window"),
-        workspace.data_ptr(), ws_bytes,        _ptr(dev_status), raw), "pkv_paged_attention_decode_fp4")
+        workspace.data_ptr(), ws_bytes, _ptr(dev_status), raw), "pkv_paged_attention_decode_fp4")
     return out
 
 

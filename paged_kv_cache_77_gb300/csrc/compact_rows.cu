@@ -9,7 +9,9 @@
 // with four loads in flight in half as many registers again per SM (16 prompts cut to 2,000 4-bit
 // rows 21.1 us with six CTAs per SM and four loads, 26.1 with four and eight; 64 x 2,048 bf16 rows
 // in place 215 and 184 us).
-// Roofline: HBM; every moved row read once and written once (+ 4 bytes of the list).
+// Roofline: HBM; every moved row read once and written once (+ 4 bytes of the list). Measured on GB300:
+// 64 sequences x 8 heads x 2,048 bf16 rows in place 184 us, 86 % of the copy rate; the same 4-bit rows 81
+// us (8-byte scales and 4-byte sums come and go in sectors of 32).
 #include "device_common.cuh"
 #include "launch.h"
 #include "pdl.cuh"

@@ -568,3 +568,57 @@ def test_rows_past_32_bits_of_bytes():
     after = cache[[nb - 2, nb - 7]].view(torch.int16).cpu().numpy()
     np.testing.assert_array_equal(after, ev.compact(rows.view(torch.int16).cpu().numpy(), kept.cpu().numpy(),
                                                     np.array([[0, 1]]), np.array([[0, 1]]), False))
+
+
+def test_compact_rows_with_the_same_table_as_the_new_one():
+    rng = np.random.default_rng(16)
+    table, nb = make_table(rng, [600, 300])
+    kept = ints(_kept(rng, 2, 2, [600, 300], 250))
+    t = ints(table)
+    cache = torch.as_tensor(rng.random((nb, 2, BS)), dtype=torch.float32).cuda()
+    before = cache.cpu().numpy()
+    api.compact_rows(kept, t, head_caches=[cache], new_block_table=t)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(cache.cpu().numpy(), ev.compact(before, kept.cpu().numpy(), table, table, True))
+
+
+def test_two_evictions_at_once():
+    """The calls have no workspace: two at once on streams of their own give what each gives alone."""
+    rng = np.random.default_rng(17)
+    jobs = []
+    for lens, H, fmt in (([3000, 900], 8, "fp4"), ([2500, 128, 0, 700], 4, "bf16")):
+        table, nb = make_table(rng, lens)
+        cache, scale, _ = keys_of(fmt, rng, nb, 2)
+        q = torch.as_tensor(rng.standard_normal((len(lens), H, D)), dtype=torch.float32).to(torch.bfloat16).cuda()
+        lse = torch.full((len(lens), H), 4.0, device="cuda")
+        w = torch.as_tensor(rng.random((nb, 2, BS)), dtype=torch.float32).cuda()
+        kept = torch.zeros((len(lens), 2, 500), dtype=torch.int32, device="cuda")
+        own = w.clone(), cache.clone(), kept
+        jobs.append((own, (w, cache), q, lse, ints(table), ints(lens), ints([1] * len(lens)), scale, fmt))
+
+    def evict(own, first, q, lse, t, n, fresh, scale, fmt, stream=None):
+        w, cache, kept = own
+        api.accumulate_attention_weights(w, q, lse, cache, t, n, fresh, 0.09, k_scale=scale, stream=stream)
+        api.select_rows(w, t, n, 500, 2, 16, out=kept, stream=stream)
+        api.compact_rows(kept, t, [cache] if fmt == "bf16" else [], [w] + ([cache] if fmt == "fp4" else []), stream=stream)
+
+    def back(job):
+        for t, x in zip(job[0], job[1]):
+            t.copy_(x)
+        job[0][2].zero_()
+
+    alone = []
+    for job in jobs:
+        evict(*job)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in job[0]])
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(10):
+        for job in jobs:
+            back(job)
+        torch.cuda.synchronize()
+        for job, stream in zip(jobs, streams):
+            evict(*job, stream=stream)
+        torch.cuda.synchronize()
+        for job, want in zip(jobs, alone):
+            assert all(torch.equal(a, b) for a, b in zip(job[0], want))

@@ -395,3 +395,38 @@ def test_blocks_past_32_bits_of_bytes():
     np.testing.assert_array_equal(f64(k), b.key)
     np.testing.assert_array_equal(f64(v), b.val)
     b.check(out, lse, 0.09)
+
+
+def test_a_fork_of_4_bit_blocks():
+    """copy_blocks copies codes and scales: the child reads what the parent does, and what it then
+    writes is its own."""
+    b = Batch(71, [300], 8, 2, 1, nb_more=4)
+    free = np.setdiff1d(np.arange(b.cache[0].shape[0]), b.table)
+    child = b.table.copy()
+    child[0, 2] = free[0]  # shared full blocks, a copy of the last one
+    for t in b.cache:
+        api.copy_blocks(t, ints(b.table[0, 2:3]), ints(free[:1]))
+    q, k_cache, v_cache, k_scale, v_scale, table, lens = b.args()
+    both = torch.cat([table, ints(child)])
+    args = torch.cat([q, q]), k_cache, v_cache, k_scale, v_scale, both, ints([300, 300])
+    out = api.paged_attention_decode_fp4(*args, 0.09)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[1])
+    new = rows_of(np.random.default_rng(72), 1, 2, D)
+    api.kv_cache_write_fp4(*b.cache, new, new, ints([child[0, 2] * BS + 44]))
+    after = api.paged_attention_decode_fp4(*args[:-1], ints([300, 301]), 0.09)
+    torch.cuda.synchronize()
+    assert torch.equal(after[0], out[0]) and not torch.equal(after[1], out[1])
+
+
+def test_two_decodes_at_once():
+    """Workspaces of their own on streams of their own: the results of each alone."""
+    batches = [Batch(73, [2000, 17, 900], 16, 2, 1), Batch(74, [1300, 5], 8, 1, 3)]
+    jobs = [b.args() for b in batches]
+    alone = [api.paged_attention_decode_fp4(*args, 0.09) for args in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(10):
+        outs = [api.paged_attention_decode_fp4(*args, 0.09, stream=s) for args, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, alone))
