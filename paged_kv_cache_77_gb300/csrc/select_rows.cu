@@ -19,11 +19,13 @@
 // blocks, list and histograms; every CTA sums the histograms of the cluster for itself through
 // distributed shared memory.
 //
-// Roofline: HBM by bytes (4 per weight), instructions and latencies in practice. Measured on GB300:
-// 512 rows of up to 32,768 weights (4,096 kept) 29 us, where the bytes take 5.5: a CTA of 256 blocks
-// spends some 45,000 cycles, 2,900 on the sample, 10,700 on the pass over the weights, 5,400 on the
-// list, 6,000 on scans and digits, 5,500 on the positions, the rest on lookups and barriers, three CTAs
-// to an SM. 16 rows of a million weights (65,536 kept) 61 us for 10: clusters of 8, one CTA to an SM.
+// Roofline: HBM by bytes (4 per weight), instructions in practice: some 350 of a warp per block of 128
+// weights, issue slots 67 % busy. Measured on GB300: 512 rows of up to 32,768 weights (4,096 kept) 30 us,
+// where the bytes take 5.5: a CTA of 256 blocks, one of three on its SM, spends some 45,000 cycles, 2,900
+// on the sample, 10,700 on the pass over the weights, 5,400 on the list, 6,000 on scans and digits, 5,500
+// on the positions, the rest on lookups and barriers. 16 rows of a million weights (65,536 kept) 61 us
+// where the bytes take 10: clusters of 8, one CTA to an SM. More blocks in flight (eight: 84 us),
+// prefetches into L2 (68) and the longest sequences first (512 rows 31 us, 1,600 rows 100 and 116) do not help.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
