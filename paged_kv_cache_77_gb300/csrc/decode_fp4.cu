@@ -28,7 +28,7 @@
 // kv head, issue slots 65 % busy. Before: the warps of a CTA on one tile, joined at each segment's end
 // through shared memory, 368 us (a segment's end cost 6 us, and 64 sequences of up to 2,048 tokens 78 us
 // instead of 25); warps with runs of their own 267; an unmasked path 216; copies that need no barrier
-// 194. More than 8 query rows per kv head are bound by instructions: 16 rows 57 % of the copy rate.
+// 194. More than 8 query rows per kv head are bound by instructions: 16 rows 56 % of the copy rate.
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
