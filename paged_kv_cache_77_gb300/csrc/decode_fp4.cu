@@ -571,7 +571,7 @@ cudaError_t launch_decode_fp4(DecodeArgs a, cudaStream_t stream) {
   for (a.row0 = 0; a.row0 < a.q_total; a.row0 += per) {
     a.q_len = a.q_total - a.row0 < per ? a.q_total - a.row0 : per;
     cudaError_t e = a.n_rep * a.q_len <= 8 ? launch_n<1>(a, stream) : launch_n<2>(a, stream);
-    if (e == cudaSuccess) e = launch_decode_merge(a, stream);
+    if (e == cudaSuccess) e = launch_decode_merge(a, stream, true);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -243,7 +243,14 @@ __global__ void __launch_bounds__(simt::THREADS, 1) decode_simt_kernel(DecodeArg
 // group (q_len * n_rep rows, ordered token then head); lane = 4 consecutive output
 // elements. Segments finished inside one attention CTA are skipped; empty
 // sequences get o = 0, lse = -inf.
+//
+// kFp4: the 4-bit decode's, whose rows may be a part of the call's (row0, q_total) and whose NaN
+// scores make o and lse NaN. Its attention kernel leaves no room on an SM, so registers cost it
+// nothing, and many pieces are loaded eight at a time (one sequence of 8,192 tokens 24.8 -> 16.4 us).
+// The others' must start beside the attention kernel's CTAs: the same there takes 87 registers in
+// place of 62, and four rows per sequence 746 us in place of 738.
 // --------------------------------------------------------------------------
+template <bool kFp4>
 __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   constexpr int D = 128;
   const int seg = blockIdx.x;  // b * Hkv + g
@@ -268,7 +275,8 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   const int n = live_blocks(clamp_len(__ldg(a.seq_lens + b), cap), bs, a.window).n;
   const int64_t base = before * a.Hkv + (int64_t)g * n;
   const int64_t row =
-      ((int64_t)b * a.q_total + a.row0 + h / a.n_rep) * a.H + (int64_t)g * a.n_rep + h % a.n_rep;
+      ((int64_t)b * (kFp4 ? a.q_total : a.q_len) + (kFp4 ? a.row0 : 0) + h / a.n_rep) * a.H +
+      (int64_t)g * a.n_rep + h % a.n_rep;
   auto put = [&](float4 v) {
     if (a.out_f32) {
       reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * D)[lane] = v;
@@ -284,7 +292,9 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   // only), so that after it every piece's loads are issued at once.
   constexpr int kMaxPieces = 8;
   // A CTA without a tile has no piece; with tiles for all of them there is none such to look for.
-  auto without = [&](int64_t i) { return T < G && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G); };
+  auto without = [&](int64_t i) {
+    return (!kFp4 || T < G) && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G);
+  };
   auto slot_of = [&](int64_t i) { return (i == i0) ? (int64_t)seg : (int64_t)a.B * a.Hkv + i; };
   int64_t slots[kMaxPieces];
   int np = 0;
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
       acc.w += w * x[p].w;
       wsum += w;
     }
-  } else {
+  } else if constexpr (kFp4) {
     // More pieces than registers hold (segments far longer than a CTA's share): first the largest
     // log-sum-exp, a piece per lane, then the sums in the pieces' order, kMaxPieces at a time.
     for (int64_t i = i0 + lane; i <= i1; i += 32) {
@@ -357,11 +367,29 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
         wsum += w;
       }
     }
+  } else {
+    // The same, a piece at a time.
+    for (int64_t i = i0; i <= i1; ++i) {
+      if (i > i0 && without(i)) continue;
+      mx = fmaxf(mx, a.ws_lse[slot_of(i) * n_rep + h]);
+    }
+    for (int64_t i = i0; i <= i1; ++i) {
+      if (i > i0 && without(i)) continue;
+      const int64_t slot = slot_of(i);
+      const float l2 = a.ws_lse[slot * n_rep + h];
+      const float w = (l2 == -INFINITY) ? 0.f : exp2f(l2 - mx);
+      const float4 x = reinterpret_cast<const float4*>(a.ws_o + (slot * n_rep + h) * D)[lane];
+      acc.x += w * x.x;
+      acc.y += w * x.y;
+      acc.z += w * x.z;
+      acc.w += w * x.w;
+      wsum += w;
+    }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
   put(make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  // A piece whose log-sum-exp is NaN (the 4-bit decode's, for a NaN score) makes both NaN.
-  if (a.lse && lane == 0) a.lse[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * kLn2;
+  const bool none = kFp4 ? wsum == 0.f : !(wsum > 0.f);  // (NaN: see above)
+  if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (mx + log2f(wsum)) * kLn2;
 }
 
 // H here counts every query row of a sequence (q_len * heads).
@@ -400,11 +428,12 @@ cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream) {
   }
 }
 
-cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream, bool fp4) {
   if (a.B * a.Hkv == 0) return cudaSuccess;
   const int rows = a.n_rep * a.q_len;
   const dim3 grid(a.B * a.Hkv, (rows + 15) / 16);
-  return launch_dependent(decode_merge_kernel, grid, dim3(32 * (rows < 16 ? rows : 16)), 0, stream, a);
+  return launch_dependent(fp4 ? decode_merge_kernel<true> : decode_merge_kernel<false>, grid,
+                          dim3(32 * (rows < 16 ? rows : 16)), 0, stream, a);
 }
 
 }  // namespace pkv

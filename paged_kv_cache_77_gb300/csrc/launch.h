@@ -179,7 +179,7 @@ void decode_workspace_carve(DecodeArgs& a, void* ws);
 
 // CUDA-core split-KV decode (any group size 1..16) followed by the LSE merge.
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream);
-cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream, bool fp4 = false);
 // tcgen05 split-KV decode for head groups (n_rep 1..16), same partials as above.
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t stream);
 // The same kernel for q_len 1..4 query rows per sequence (q_len * n_rep <= 32).
