@@ -180,7 +180,7 @@ int decode_setup(pkv::DecodeArgs& a, bool* empty, const char* what, void* out, i
   a.Hkv = H_kv;
   a.n_rep = n_rep;
   a.max_blocks = max_blocks_per_seq;
-  a.q_len = a.q_total = q_len;
+  a.q_len = q_len;
   a.row_window = window;
   a.window = window > 0 ? window + q_len - 1 : 0;
   a.out_f32 = out_dtype == PKV_F32;
@@ -561,7 +561,7 @@ int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, con
               "%s: max_blocks_per_seq * 128 must fit in int32", what);
   PKV_REQUIRE(B < 0 || H_kv < 0 || B <= INT32_MAX / (H_kv > 0 ? H_kv : 1), PKV_ERR_UNSUPPORTED,
               "%s: B * H_kv must fit in int32", what);
-  DecodeArgs a;
+  DecodeFp4Args a;
   bool empty;
   const int rc0 = decode_setup(a, &empty, what, out, out_dtype, lse, q, k_cache, v_cache,
                                block_table, max_blocks_per_seq, seq_lens, B, H, H_kv, head_dim,
@@ -570,6 +570,7 @@ int pkv_paged_attention_decode_fp4(void* out, int32_t out_dtype, float* lse, con
   if (rc0 != PKV_OK || empty) return rc0;
   PKV_REQUIRE(k_scale && v_scale && aligned16(k_scale) && aligned16(v_scale), PKV_ERR_INVALID_ARG,
               "%s: scale arrays must be set and 16-byte aligned", what);
+  a.q_total = q_len;
   a.k_scale4 = (const uint8_t*)k_scale;
   a.v_scale4 = (const uint8_t*)v_scale;
   clear_error();

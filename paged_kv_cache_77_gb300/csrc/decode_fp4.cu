@@ -163,7 +163,7 @@ __device__ __forceinline__ void take(const Smem<NT>& sm, int warp, int lane, Run
 
 // Writes a segment's rows, or a part of them (slot >= 0) to the workspace.
 template <int NT>
-__device__ __forceinline__ void put(const DecodeArgs& a, const Running<NT>& r, int lane, int b, int kv, int64_t slot) {
+__device__ __forceinline__ void put(const DecodeFp4Args& a, const Running<NT>& r, int lane, int b, int kv, int64_t slot) {
   const int g = lane >> 2, c = lane & 3, R = a.n_rep * a.q_len;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -380,7 +380,7 @@ __device__ __forceinline__ void attend(Running<NT>& r, const uint4 (&qf)[NT][4],
 }
 
 template <int NT>
-__global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(const __grid_constant__ DecodeFp4Args a) {
   constexpr int WARPS = Shape<NT>::WARPS, STAGES = Shape<NT>::STAGES, AT_ONCE = Shape<NT>::AT_ONCE;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<NT>& sm = *reinterpret_cast<Smem<NT>*>(smem_raw);
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
 }
 
 template <int NT>
-cudaError_t launch_n(const DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_n(const DecodeFp4Args& a, cudaStream_t stream) {
   const size_t smem = sizeof(Smem<NT>);
   static_assert(sizeof(Smem<NT>) <= 227 * 1024, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -566,12 +566,12 @@ cudaError_t launch_n(const DecodeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // Query tokens in pieces of at most 16 rows per kv head, each with a pass over the cache of its own.
-cudaError_t launch_decode_fp4(DecodeArgs a, cudaStream_t stream) {
+cudaError_t launch_decode_fp4(DecodeFp4Args a, cudaStream_t stream) {
   const int per = 16 / a.n_rep;
   for (a.row0 = 0; a.row0 < a.q_total; a.row0 += per) {
     a.q_len = a.q_total - a.row0 < per ? a.q_total - a.row0 : per;
     cudaError_t e = a.n_rep * a.q_len <= 8 ? launch_n<1>(a, stream) : launch_n<2>(a, stream);
-    if (e == cudaSuccess) e = launch_decode_merge(a, stream, true);
+    if (e == cudaSuccess) e = launch_decode_merge(a, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -17,6 +17,8 @@
 // Roofline: HBM. Algorithmic bytes per tile = 2 * 128 * 128 * 2 (K and V of one
 // kv head); per call add q and out. This kernel is the CUDA-core path (used for
 // MHA, and as the comparison point for the tensor-core GQA kernel).
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "launch.h"
 
@@ -244,15 +246,16 @@ __global__ void __launch_bounds__(simt::THREADS, 1) decode_simt_kernel(DecodeArg
 // elements. Segments finished inside one attention CTA are skipped; empty
 // sequences get o = 0, lse = -inf.
 //
-// kFp4: the 4-bit decode's, whose rows may be a part of the call's (row0, q_total) and whose NaN
-// scores make o and lse NaN. Its attention kernel leaves no room on an SM, so registers cost it
+// That of the 4-bit decode (DecodeFp4Args), whose rows may be a part of the call's and whose NaN
+// scores make o and lse NaN: its attention kernel leaves no room on an SM, so registers cost it
 // nothing, and many pieces are loaded eight at a time (one sequence of 8,192 tokens 24.8 -> 16.4 us).
 // The others' must start beside the attention kernel's CTAs: the same there takes 87 registers in
 // place of 62, and four rows per sequence 746 us in place of 738.
 // --------------------------------------------------------------------------
-template <bool kFp4>
-__global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
+template <typename Args>
+__global__ void __launch_bounds__(512) decode_merge_kernel(Args a) {
   constexpr int D = 128;
+  constexpr bool kFp4 = std::is_same_v<Args, DecodeFp4Args>;
   const int seg = blockIdx.x;  // b * Hkv + g
   const int b = seg / a.Hkv, g = seg % a.Hkv;
   const int h = blockIdx.y * 16 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -274,9 +277,9 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(DecodeArgs a) {
   const int64_t T = tot * a.Hkv, G = a.num_ctas;
   const int n = live_blocks(clamp_len(__ldg(a.seq_lens + b), cap), bs, a.window).n;
   const int64_t base = before * a.Hkv + (int64_t)g * n;
-  const int64_t row =
-      ((int64_t)b * (kFp4 ? a.q_total : a.q_len) + (kFp4 ? a.row0 : 0) + h / a.n_rep) * a.H +
-      (int64_t)g * a.n_rep + h % a.n_rep;
+  int64_t first = (int64_t)b * a.q_len;  // the sequence's first query row
+  if constexpr (kFp4) first = (int64_t)b * a.q_total + a.row0;
+  const int64_t row = (first + h / a.n_rep) * a.H + (int64_t)g * a.n_rep + h % a.n_rep;
   auto put = [&](float4 v) {
     if (a.out_f32) {
       reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + row * D)[lane] = v;
@@ -428,12 +431,14 @@ cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream) {
   }
 }
 
-cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream, bool fp4) {
+template <typename Args>
+static cudaError_t launch_merge(const Args& a, cudaStream_t stream) {
   if (a.B * a.Hkv == 0) return cudaSuccess;
   const int rows = a.n_rep * a.q_len;
   const dim3 grid(a.B * a.Hkv, (rows + 15) / 16);
-  return launch_dependent(fp4 ? decode_merge_kernel<true> : decode_merge_kernel<false>, grid,
-                          dim3(32 * (rows < 16 ? rows : 16)), 0, stream, a);
+  return launch_dependent(decode_merge_kernel<Args>, grid, dim3(32 * (rows < 16 ? rows : 16)), 0, stream, a);
 }
+cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream) { return launch_merge(a, stream); }
+cudaError_t launch_decode_merge(const DecodeFp4Args& a, cudaStream_t stream) { return launch_merge(a, stream); }
 
 }  // namespace pkv

@@ -159,19 +159,22 @@ struct DecodeArgs {
   int* dev_status;
   int64_t num_blocks;
   int B, H, Hkv, n_rep, max_blocks, out_f32;
-  int q_len;                  // new query rows per sequence (1 = plain decode) of this launch,
-  int q_total, row0;          // which are row0 .. row0 + q_len - 1 of the q_total of q and out
+  int q_len;                  // new query rows per sequence (1 = plain decode)
   int row_window;             // window of one query row (0 = full attention)
   int window;                 // live-block span: row_window + q_len - 1 (0 = all)
   int num_ctas;               // G: CTAs of the attention kernel (one per SM)
   float scale_log2;           // scale * log2(e)
   const float* k_scale;       // FP8 cache only: [nb, Hkv, bs] per-row scales
   const float* v_scale;
-  const uint8_t* k_scale4;    // 4-bit cache only: [nb, Hkv, bs, 8]
-  const uint8_t* v_scale4;
   // Sparse decode only: B counts query rows, rows_per_seq of each sequence.
   const int32_t* block_indices;  // [B, Hkv, num_selected] blocks of the sequence, or null
   int num_selected, rows_per_seq;
+};
+// The 4-bit cache's: codes [nb, Hkv, bs, 64].
+struct DecodeFp4Args : DecodeArgs {
+  const uint8_t* k_scale4;    // [nb, Hkv, bs, 8]
+  const uint8_t* v_scale4;
+  int q_total, row0;          // the launch's q_len rows are row0 .. row0 + q_len - 1 of q and out's q_total
 };
 
 size_t decode_workspace_bytes(int B, int H, int Hkv, int D, int G);
@@ -179,7 +182,8 @@ void decode_workspace_carve(DecodeArgs& a, void* ws);
 
 // CUDA-core split-KV decode (any group size 1..16) followed by the LSE merge.
 cudaError_t launch_decode_simt(const DecodeArgs& a, cudaStream_t stream);
-cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream, bool fp4 = false);
+cudaError_t launch_decode_merge(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_merge(const DecodeFp4Args& a, cudaStream_t stream);
 // tcgen05 split-KV decode for head groups (n_rep 1..16), same partials as above.
 cudaError_t launch_decode_tc(const DecodeArgs& a, cudaStream_t stream);
 // The same kernel for q_len 1..4 query rows per sequence (q_len * n_rep <= 32).
@@ -191,7 +195,7 @@ cudaError_t launch_decode_sparse(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_fp8(const DecodeArgs& a, cudaStream_t stream);
 // Split-KV decode over the 4-bit cache for q_len 1..4 query rows per sequence, same partials as
 // above, and its merge.
-cudaError_t launch_decode_fp4(DecodeArgs a, cudaStream_t stream);
+cudaError_t launch_decode_fp4(DecodeFp4Args a, cudaStream_t stream);
 
 // Absorbed MLA decode (tcgen05) plus its merge, q_len query rows per sequence
 // (1 for plain decode). Workspace: mla_workspace_bytes(B * q_len, num_sms / 2).
