@@ -1,7 +1,8 @@
 // Split-KV decode over the 4-bit cache (fp4.cuh has the format).
 //
 // For each query row, o = softmax(scale q K^T) V over the row's visible positions. A CTA has a
-// share of the (sequence, kv head, block) tiles, equal for all CTAs, and every warp of it an
+// share of the (sequence, kv head, block) tiles, equal for all CTAs (or, where sequences are few and
+// short, all tiles of one sequence and kv head), and every warp of it an
 // equal run of that share in pieces of 32 tokens. A warp works alone: it brings its pieces into a
 // ring of its own in shared memory with asynchronous copies, keeps a running maximum, sum and
 // output in registers, and writes what it finishes. Only the segments that cross from warp to warp are joined, once, when the CTA's share
@@ -388,14 +389,36 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform, and known to be)
   const DenseRows rows = {a.seq_lens, TILE, a.window, a.max_blocks * TILE};
   pdl_wait_then_launch();
-  if (warp == 0) {
-    const int64_t tot = total_live_blocks(rows, a.B, a.dev_status);
-    if (lane == 0) sm.total = tot * a.Hkv;
+  int64_t t0 = 0, t1;  // the CTA's blocks
+  int seg_b = 0, seg_g = 0, seg_len = 0, seg_lo = 0;
+  if (a.whole) {
+    seg_b = blockIdx.x / a.Hkv;
+    seg_g = blockIdx.x % a.Hkv;
+    const int raw = rows.raw(seg_b);
+    seg_len = clamp_len(raw, rows.cap);
+    if (raw != seg_len && seg_g == 0 && tid == 0) flag_status(a.dev_status, PKV_DEV_BAD_LENGTH);
+    const SeqRange range = rows.blocks(seg_len);
+    seg_lo = range.jlo;
+    t1 = range.n;
+    if (range.n == 0) {
+      if (warp == 0) {
+        Running<NT> none;
+        none.clear();
+        put(a, none, lane, seg_b, seg_g, -1);
+      }
+      return;
+    }
+  } else {
+    if (warp == 0) {
+      const int64_t tot = total_live_blocks(rows, a.B, a.dev_status);
+      if (lane == 0) sm.total = tot * a.Hkv;
+    }
+    __syncthreads();
+    const int64_t T = sm.total, G = min((int64_t)gridDim.x, T);
+    if (blockIdx.x >= G) return;
+    t0 = cta_tile_start(blockIdx.x, T, G);
+    t1 = cta_tile_start(blockIdx.x + 1, T, G);
   }
-  __syncthreads();
-  const int64_t T = sm.total, G = gridDim.x;
-  const int64_t t0 = cta_tile_start(blockIdx.x, T, G), t1 = cta_tile_start(blockIdx.x + 1, T, G);
-  if (t0 >= t1) return;
 
   // This warp's run: pieces u0 .. u1 - 1 of the CTA's.
   const int64_t u0 = Walk::run(t1 - t0, warp, WARPS), u1 = Walk::run(t1 - t0, warp + 1, WARPS);
@@ -406,7 +429,12 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
   bool open = false;   // whether it goes on behind the run, and is this warp's to finish
   int left = kNothing;
   if (u0 < u1) {
-    begun = cur.seek(rows, a.B, a.Hkv, t0, t1, u0, u1);
+    if (a.whole) {
+      cur.start(seg_b, seg_g, seg_len, seg_lo, (int)u0, (int)u1);
+      begun = u0 == 0;
+    } else {
+      begun = cur.seek(rows, a.B, a.Hkv, t0, t1, u0, u1);
+    }
     // ---- the ring: the run's it-th visited piece is in stage it % STAGES, one group of
     // asynchronous copies each. A lane copies 16 bytes of every eighth row of the codes, and 16 bytes
     // of the scales of K (lanes 0 to 15) or V.
@@ -560,7 +588,7 @@ cudaError_t launch_n(const DecodeFp4Args& a, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_fp4_kernel<NT>, dim3(a.num_ctas), dim3(32 * Shape<NT>::WARPS), smem, stream, a);
+  return launch_dependent(decode_fp4_kernel<NT>, dim3(a.whole ? a.B * a.Hkv : a.num_ctas), dim3(32 * Shape<NT>::WARPS), smem, stream, a);
 }
 
 }  // namespace
@@ -568,10 +596,15 @@ cudaError_t launch_n(const DecodeFp4Args& a, cudaStream_t stream) {
 // Query tokens in pieces of at most 16 rows per kv head, each with a pass over the cache of its own.
 cudaError_t launch_decode_fp4(DecodeFp4Args a, cudaStream_t stream) {
   const int per = 16 / a.n_rep;
+  // Short sequences, no more (sequence, kv head) pairs than SMs: a CTA each. The second launch and the
+  // joins in memory cost more than the SMs left idle. Measured on GB300 (us shared out, and a CTA each):
+  // 64 pairs of up to 512 tokens 10.3, 7.4, 2,048 11.3, 10.0, 4,096 13.3, 14.4; 128 of 2,048 17.7, 14.1;
+  // 8 of up to 2,048 10.6, 9.7, 4,096 12.5, 13.0; 1 of 2,048 10.5, 12.9; 256 of up to 128 9.5, 12.7.
+  a.whole = a.max_blocks <= 16 && a.B * a.Hkv <= a.num_ctas;
   for (a.row0 = 0; a.row0 < a.q_total; a.row0 += per) {
     a.q_len = a.q_total - a.row0 < per ? a.q_total - a.row0 : per;
     cudaError_t e = a.n_rep * a.q_len <= 8 ? launch_n<1>(a, stream) : launch_n<2>(a, stream);
-    if (e == cudaSuccess) e = launch_decode_merge(a, stream);
+    if (e == cudaSuccess && !a.whole) e = launch_decode_merge(a, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -249,8 +249,10 @@ __global__ void __launch_bounds__(simt::THREADS, 1) decode_simt_kernel(DecodeArg
 // That of the 4-bit decode (DecodeFp4Args), whose rows may be a part of the call's and whose NaN
 // scores make o and lse NaN: its attention kernel leaves no room on an SM, so registers cost it
 // nothing, and many pieces are loaded eight at a time (one sequence of 8,192 tokens 24.8 -> 16.4 us).
-// The others' must start beside the attention kernel's CTAs: the same there takes 87 registers in
-// place of 62, and four rows per sequence 746 us in place of 738.
+// It shares fewer tiles than CTAs out among so many CTAs, so there is none without a tile to look for (one
+// kv head of 2,048 tokens 88 -> 10.5 us). The others' must start beside the attention kernel's CTAs:
+// many pieces at a time there take 87 registers in place of 62, and four rows per sequence 746 us in
+// place of 738.
 // --------------------------------------------------------------------------
 template <typename Args>
 __global__ void __launch_bounds__(512) decode_merge_kernel(Args a) {
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(Args a) {
     tot += __shfl_xor_sync(0xffffffffu, tot, o);
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
-  const int64_t T = tot * a.Hkv, G = a.num_ctas;
+  const int64_t T = tot * a.Hkv, G = kFp4 && T < a.num_ctas ? T : a.num_ctas;
   const int n = live_blocks(clamp_len(__ldg(a.seq_lens + b), cap), bs, a.window).n;
   const int64_t base = before * a.Hkv + (int64_t)g * n;
   int64_t first = (int64_t)b * a.q_len;  // the sequence's first query row
@@ -294,10 +296,8 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(Args a) {
   // The pieces' workspace slots, found before the wait (they depend on the inputs
   // only), so that after it every piece's loads are issued at once.
   constexpr int kMaxPieces = 8;
-  // A CTA without a tile has no piece; with tiles for all of them there is none such to look for.
-  auto without = [&](int64_t i) {
-    return (!kFp4 || T < G) && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G);
-  };
+  // A CTA without a tile has no piece (the 4-bit decode has none such among the G).
+  auto without = [&](int64_t i) { return !kFp4 && cta_tile_start(i + 1, T, G) == cta_tile_start(i, T, G); };
   auto slot_of = [&](int64_t i) { return (i == i0) ? (int64_t)seg : (int64_t)a.B * a.Hkv + i; };
   int64_t slots[kMaxPieces];
   int np = 0;

@@ -175,6 +175,7 @@ struct DecodeFp4Args : DecodeArgs {
   const uint8_t* k_scale4;    // [nb, Hkv, bs, 8]
   const uint8_t* v_scale4;
   int q_total, row0;          // the launch's q_len rows are row0 .. row0 + q_len - 1 of q and out's q_total
+  bool whole;                 // a CTA for every (sequence, kv head), and no merge
 };
 
 size_t decode_workspace_bytes(int B, int H, int Hkv, int D, int G);

@@ -48,6 +48,14 @@ struct Walk {
     enter((t.jlo + t.j) * TILE + (int)(u0 % PER) * SUB);
     return t.j == 0 && u0 % PER == 0;
   }
+  // Enters pieces [u0, u1) of one segment, of kv head kv of sequence seq (len > 0), whose first block is jlo.
+  __device__ __forceinline__ void start(int seq, int kv, int length, int jlo, int u0, int u1) {
+    b = seq;
+    g = kv;
+    len = length;
+    todo = u1 - u0;
+    enter(jlo * TILE + u0 * SUB);
+  }
   // The next segment of the run; false behind its end.
   __device__ __forceinline__ bool next(const DenseRows& rows, int B, int Hkv) {
     todo -= padded;

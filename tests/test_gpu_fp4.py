@@ -430,3 +430,27 @@ def test_two_decodes_at_once():
         outs = [api.paged_attention_decode_fp4(*args, 0.09, stream=s) for args, s in zip(jobs, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, alone))
+
+
+@pytest.mark.parametrize("B,H,hkv,q_len", [(3, 8, 2, 1), (3, 8, 2, 3), (1, 1, 1, 1), (9, 16, 16, 1), (10, 16, 16, 1)])
+@pytest.mark.parametrize("width", [16, 17])
+def test_decode_with_a_cta_for_a_sequence_or_shared_out(B, H, hkv, q_len, width):
+    """Tables on either side of the rule that gives a sequence and kv head a CTA of its own: the
+    same attention, with lengths of zero, of one token, of whole tables, and past the table."""
+    lens = ([2048, 0, 1] + [37 * i for i in range(3, 10)])[:B]
+    b = Batch(80 + B + q_len, lens, H, hkv, q_len)
+    table = np.full((B, width), -3, dtype=np.int32)
+    table[:, :b.table.shape[1]] = b.table[:, :width]
+    args = list(b.args())
+    args[5] = ints(table)
+    st = status()
+    lse = torch.full(args[0].shape[:-1], 7.0, device="cuda")
+    out = api.paged_attention_decode_fp4(*args, 0.09, lse=lse, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    b.check(out, lse, 0.09)
+    args[6] = ints([5000 if n == 2048 else n for n in lens])  # clamped to the table
+    if width == 16:
+        again = api.paged_attention_decode_fp4(*args, 0.09, dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st) == 4 and torch.equal(again, out)
