@@ -574,7 +574,7 @@ def _rope_rows(t, T, d, name):
         raise ValueError(f"{name} has shape {_shape_str(shape)}, expected [{T}, heads, {d}]")
     heads = shape[1]
     st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != d):
+    if T and (st[2] != 1 or (heads > 1 and st[1] != d)):  # (no rows: any strides)
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return heads, st[0] if T > 1 else heads * d
 

@@ -454,3 +454,12 @@ def test_decode_with_a_cta_for_a_sequence_or_shared_out(B, H, hkv, q_len, width)
         again = api.paged_attention_decode_fp4(*args, 0.09, dev_status=st)
         torch.cuda.synchronize()
         assert int(st) == 4 and torch.equal(again, out)
+
+
+def test_a_write_of_no_rows_takes_any_strides():
+    cache = caches(2, 3, BS)
+    before = [t.clone() for t in cache]
+    none = torch.empty(1024, dtype=torch.bfloat16, device="cuda").as_strided((0, 3, D), (1, 1, 1))
+    api.kv_cache_write_fp4(*cache, none, none, ints([]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(cache, before))
