@@ -209,6 +209,58 @@ __device__ __forceinline__ void put(const DecodeFp4Args& a, const Running<NT>& r
     }
 }
 
+// All warps' parts of the CTA's one segment, summed by all threads, two channels of two rows each.
+template <int NT>
+__device__ __forceinline__ void join(const DecodeFp4Args& a, const Smem<NT>& sm, int b, int kv) {
+  constexpr int WARPS = Shape<NT>::WARPS;
+  const int R = a.n_rep * a.q_len;
+  for (int item = threadIdx.x; item < NT * 256; item += 32 * WARPS) {
+    const int n = item >> 8, d = item >> 5 & 7, lane = item & 31, g = lane >> 2, c = lane & 3;
+    float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, sum[2] = {0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+      if (sm.left[w] != kNothing) {
+        const float2 m = *reinterpret_cast<const float2*>(&sm.stat[w][n][0][2 * c]);
+        top[0] = fmaxf(top[0], m.x);
+        top[1] = fmaxf(top[1], m.y);
+      }
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+      if (sm.left[w] != kNothing) {
+        const float2 m = *reinterpret_cast<const float2*>(&sm.stat[w][n][0][2 * c]);
+        const float2 part = *reinterpret_cast<const float2*>(&sm.stat[w][n][1][2 * c]);
+        const float2 exact = *reinterpret_cast<const float2*>(&sm.stat[w][n][2][2 * c]);
+        const float4 v = sm.o[w][n][d][lane];
+        // (A part without a finite score has sums of 0, or NaN, which any factor keeps.)
+        const float by0 = m.x == -INFINITY ? 1.f : exp2_approx(m.x - top[0]);
+        const float by1 = m.y == -INFINITY ? 1.f : exp2_approx(m.y - top[1]);
+        l[0] += part.x * by0;
+        l[1] += part.y * by1;
+        sum[0] += exact.x * by0;
+        sum[1] += exact.y * by1;
+        o[0] += v.x * by0;
+        o[1] += v.y * by1;
+        o[2] += v.z * by0;
+        o[3] += v.w * by1;
+      }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = 8 * n + 2 * c + x;
+      if (row >= R) continue;
+      const bool none = l[x] == 0.f;
+      const float inv = none ? 0.f : 1.f / l[x];
+      const int64_t at = ((int64_t)b * a.q_total + a.row0 + row / a.n_rep) * a.H + (int64_t)kv * a.n_rep + row % a.n_rep;
+      const int64_t to = at * D + 16 * g + 2 * d;
+      if (a.out_f32)
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + to) = make_float2(o[x] * inv, o[x + 2] * inv);
+      else
+        *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<uint16_t*>(a.out) + to) =
+            __floats2bfloat162_rn(o[x] * inv, o[x + 2] * inv);
+      if (a.lse && d == 0 && g == 0) a.lse[at] = none ? -INFINITY : (top[x] + log2f(sum[x]) - kShift) * kLn2;
+    }
+  }
+}
+
 // What the query rows of a launch see of a sequence: row i (of the call's) the positions in
 // (first + i - window, first + i].
 struct Sight {
@@ -553,7 +605,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
         st = (st + 1) % STAGES;
       }
       r.sum_lanes();
-      const bool own = begun || reaches_in;
+      const bool own = !a.whole && (begun || reaches_in);
       if (cur.ends && own) {
         put(a, r, lane, cur.b, cur.g, begun ? (int64_t)-1 : (int64_t)a.B * a.Hkv + blockIdx.x);
       } else if (own) {
@@ -568,6 +620,10 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
   }
   if (lane == 0) sm.left[warp] = left;
   __syncthreads();
+  if (a.whole) {
+    join(a, sm, seg_b, seg_g);
+    return;
+  }
   if (!open) return;
   // The segment that this warp began (or that reaches into the CTA's share from the one before)
   // goes on in the next warps.
@@ -598,9 +654,11 @@ cudaError_t launch_decode_fp4(DecodeFp4Args a, cudaStream_t stream) {
   const int per = 16 / a.n_rep;
   // Short sequences, no more (sequence, kv head) pairs than SMs: a CTA each. The second launch and the
   // joins in memory cost more than the SMs left idle. Measured on GB300 (us shared out, and a CTA each):
-  // 64 pairs of up to 512 tokens 10.3, 7.4, 2,048 11.3, 10.0, 4,096 13.3, 14.4; 128 of 2,048 17.7, 14.1;
-  // 8 of up to 2,048 10.6, 9.7, 4,096 12.5, 13.0; 1 of 2,048 10.5, 12.9; 256 of up to 128 9.5, 12.7.
-  a.whole = a.max_blocks <= 16 && a.B * a.Hkv <= a.num_ctas;
+  // 64 pairs of up to 512 tokens 10.5, 7.1, 2,048 11.4, 9.5, 4,096 13.4, 13.6, all of 4,096 17.2, 19.8; 128 of
+  // 2,048 17.7, 13.2; 8 of up to 2,048 10.6, 8.9; 1 of 2,048 10.9, 12.5; 256 of up to 128 9.5, 12.7. With 16
+  // rows: 64 pairs of up to 1,024 tokens 13.8, 11.2, 2,048 13.9, 16.6.
+  const int most = a.q_total < per ? a.q_total : per;
+  a.whole = a.max_blocks <= (most * a.n_rep <= 8 ? 16 : 8) && a.B * a.Hkv <= a.num_ctas;
   for (a.row0 = 0; a.row0 < a.q_total; a.row0 += per) {
     a.q_len = a.q_total - a.row0 < per ? a.q_total - a.row0 : per;
     cudaError_t e = a.n_rep * a.q_len <= 8 ? launch_n<1>(a, stream) : launch_n<2>(a, stream);

@@ -432,12 +432,15 @@ def test_two_decodes_at_once():
         assert all(torch.equal(a, b) for a, b in zip(outs, alone))
 
 
-@pytest.mark.parametrize("B,H,hkv,q_len", [(3, 8, 2, 1), (3, 8, 2, 3), (1, 1, 1, 1), (9, 16, 16, 1), (10, 16, 16, 1)])
-@pytest.mark.parametrize("width", [16, 17])
+@pytest.mark.parametrize("B,H,hkv,q_len,width", [
+    (3, 8, 2, 1, 16), (3, 8, 2, 1, 17), (3, 8, 4, 3, 16), (3, 8, 4, 3, 17), (1, 1, 1, 1, 16), (1, 1, 1, 1, 17),
+    (9, 16, 16, 1, 16), (10, 16, 16, 1, 16), (3, 8, 2, 3, 8), (3, 8, 2, 3, 9), (3, 16, 2, 4, 8), (3, 16, 2, 4, 9),
+    (3, 16, 1, 1, 8), (3, 16, 1, 1, 9)])
 def test_decode_with_a_cta_for_a_sequence_or_shared_out(B, H, hkv, q_len, width):
     """Tables on either side of the rule that gives a sequence and kv head a CTA of its own: the
     same attention, with lengths of zero, of one token, of whole tables, and past the table."""
-    lens = ([2048, 0, 1] + [37 * i for i in range(3, 10)])[:B]
+    full = 128 * (width // 8 * 8)
+    lens = ([full, 0, 1] + [37 * i for i in range(3, 10)])[:B]
     b = Batch(80 + B + q_len, lens, H, hkv, q_len)
     table = np.full((B, width), -3, dtype=np.int32)
     table[:, :b.table.shape[1]] = b.table[:, :width]
@@ -449,8 +452,8 @@ def test_decode_with_a_cta_for_a_sequence_or_shared_out(B, H, hkv, q_len, width)
     torch.cuda.synchronize()
     assert int(st) == 0
     b.check(out, lse, 0.09)
-    args[6] = ints([5000 if n == 2048 else n for n in lens])  # clamped to the table
-    if width == 16:
+    args[6] = ints([5000 if n == full else n for n in lens])  # clamped to the table
+    if width % 8 == 0:
         again = api.paged_attention_decode_fp4(*args, 0.09, dev_status=st)
         torch.cuda.synchronize()
         assert int(st) == 4 and torch.equal(again, out)
