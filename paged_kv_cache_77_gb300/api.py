@@ -749,49 +749,66 @@ def paged_attention_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     return out
 
 
-def _fp4_cache(k_cache, v_cache, k_scale, v_scale):
-    """(num_blocks, H_kv, block_size, GPU index) of a 4-bit cache after checking its four arrays
-    (v_cache and v_scale None: the two of K)."""
-    if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 and k_cache.shape[3] == 64:
-        nb, hkv, bs, _ = codes = k_cache.shape
-        scales = (nb, hkv, bs, 8)
+def _fp4_cache(k_cache, k_scale, v_cache=None, v_scale=None, only_k=False):
+    """(num_blocks, H_kv, block_size, GPU index) of a 4-bit cache after checking its four arrays, or
+    the two of K."""
+    u8 = torch.uint8
+    try:
+        codes = k_cache.shape
+        nb, hkv, bs, width = codes
         index = k_cache.get_device()
-        u8 = torch.uint8
-        if v_cache is None:
-            if _all_as(index, (k_cache, u8, codes), (k_scale, u8, scales)):
-                return nb, hkv, bs, index
-        elif _all_as(index, (k_cache, u8, codes), (v_cache, u8, codes), (k_scale, u8, scales),
-                     (v_scale, u8, scales)):
+        scales = (nb, hkv, bs, 8)
+        if (index >= 0 and width == 64 and k_cache.dtype is u8 and k_scale.dtype is u8
+                and k_scale.shape == scales and k_scale.get_device() == index
+                and k_cache.is_contiguous() and k_scale.is_contiguous()
+                and (only_k or (
+                    v_cache.dtype is u8 and v_scale.dtype is u8 and v_cache.shape == codes
+                    and v_scale.shape == scales and v_cache.get_device() == index
+                    and v_scale.get_device() == index and v_cache.is_contiguous()
+                    and v_scale.is_contiguous()))):
             return nb, hkv, bs, index
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (k_scale, "k_scale"),
-                 (v_scale, "v_scale")):
-        if t is not None:
-            _fp8_cache(t, n)  # contiguous uint8 on the GPU
+    except (AttributeError, ValueError):  # no tensor, or not of four axes
+        pass
+    # Something is wrong: name it.
+    arrays = {"k_cache": k_cache, "k_scale": k_scale}
+    if not only_k:
+        arrays.update(v_cache=v_cache, v_scale=v_scale)
+    for n, t in arrays.items():
+        _fp8_cache(t, n)  # contiguous uint8 on the GPU
     if k_cache.dim() != 4 or k_cache.shape[3] != 64:
         raise ValueError("k_cache must be [num_blocks, H_kv, block_size, 64] codes of 128 values, "
                          f"got {_shape_str(k_cache.shape)}")
     nb, hkv, bs, _ = k_cache.shape
-    if v_cache is not None:
+    check_shape(k_scale, (nb, hkv, bs, 8), "k_scale")
+    if not only_k:
         check_shape(v_cache, (nb, hkv, bs, 64), "v_cache")
         check_shape(v_scale, (nb, hkv, bs, 8), "v_scale")
-    check_shape(k_scale, (nb, hkv, bs, 8), "k_scale")
     index = k_cache.get_device()
-    _check_gpu(index, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    _check_gpu(index, **arrays)
     return nb, hkv, bs, index
 
 
-def _tables(index, B, block_table, seq_lens, **more):
-    """_table_and_lens, further int32 vectors of B entries, and that all are on GPU `index`."""
+def _tables(index, B, block_table, seq_lens, **more) -> int:
+    """_table_and_lens, further int32 vectors of B entries, and that all are on GPU `index`; the
+    table's width."""
     i32, lens = torch.int32, (B,)
-    width = block_table.shape[-1] if isinstance(block_table, torch.Tensor) and block_table.dim() else 0
-    if _all_as(index, (block_table, i32, (B, width)), (seq_lens, i32, lens),
-               *((t, i32, lens) for t in more.values())):
-        return
+    try:
+        rows, width = block_table.shape
+        if (rows == B and block_table.dtype is i32 and block_table.get_device() == index
+                and block_table.is_contiguous() and seq_lens.dtype is i32
+                and seq_lens.shape == lens and seq_lens.get_device() == index
+                and seq_lens.is_contiguous()
+                and (not more or _all_as(index, *((t, i32, lens) for t in more.values())))):
+            return width
+    except (AttributeError, ValueError):  # no tensor, or not of two axes
+        pass
+    # Something is wrong: name it.
     _table_and_lens(block_table, seq_lens, B)
     for n, t in more.items():
         _dev_i32(t, n)
         check_shape(t, lens, n)
     _check_gpu(index, block_table=block_table, seq_lens=seq_lens, **more)
+    return block_table.shape[1]
 
 
 def kv_cache_write_fp4(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, dev_status=None,
@@ -800,7 +817,7 @@ def kv_cache_write_fp4(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, d
 
     k_cache / v_cache [nb, H_kv, bs, 64] uint8, k_scale / v_scale [nb, H_kv, bs, 8] uint8;
     k / v [T, H_kv, 128] bf16 (slices of one projection's output will do)."""
-    nb, hkv, bs, index = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, bs, index = _fp4_cache(k_cache, k_scale, v_cache, v_scale)
     _dev_i32(slot_mapping, "slot_mapping")
     T = slot_mapping.numel()
     kh, ks = _rope_rows(k, T, 128, "k")
@@ -821,7 +838,7 @@ def kv_cache_read_fp4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=No
                       dev_status=None, stream=None):
     """Rows of a 4-bit cache widened to bf16 (exactly): returns (k, v), [T, H_kv, 128] each
     (`k_out` and `v_out` if given). A negative slot gives a row of zeros."""
-    nb, hkv, bs, index = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, bs, index = _fp4_cache(k_cache, k_scale, v_cache, v_scale)
     _dev_i32(slot_mapping, "slot_mapping")
     T = slot_mapping.numel()
     shape = (T, hkv, 128)
@@ -855,26 +872,32 @@ def paged_attention_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     causal); returns out in q's shape (and fills lse, the shape without its last axis). The
     workspace is decode_spec_workspace_size's."""
     B, Q, H, d = _query_rows(q)
-    nb, hkv, bs, index = _fp4_cache(k_cache, v_cache, k_scale, v_scale)
-    _check_gpu(index, q=q)
-    _tables(index, B, block_table, seq_lens)
+    nb, hkv, bs, index = _fp4_cache(k_cache, k_scale, v_cache, v_scale)
+    if q.get_device() != index:
+        _check_gpu(index, q=q)
+    width = _tables(index, B, block_table, seq_lens)
     raw = _launch_stream(index, stream)
-    shape = q.shape
+    shape, dev = q.shape, q.device
     if out is None or not _all_as(index, (out, torch.bfloat16, shape)):
-        out = out_buffer(out, shape, out_dtype, q.device, stream=stream)
+        out = out_buffer(out, shape, out_dtype, dev, stream=stream)
     if lse is not None and not _all_as(index, (lse, torch.float32, shape[:-1])):
-        lse_buffer(lse, tuple(shape[:-1]), q.device)
+        lse_buffer(lse, tuple(shape[:-1]), dev)
     if dev_status is not None:
-        status_buffer(dev_status, q.device)
-    code = PKV_F32 if out.dtype is torch.float32 else PKV_BF16
+        status_buffer(dev_status, dev)
     lib = load()
+    # (The library compares the size of a workspace that it is given before it launches anything.)
+    given = workspace is not None
     workspace, ws_bytes = workspace_buffer(
-        workspace, lib.pkv_decode_spec_workspace_size(B, Q, H, hkv, d), q.device, stream=stream)
-    check(lib.pkv_paged_attention_decode_fp4(
-        out.data_ptr(), code, _ptr(lse), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), B, Q, H, hkv, d, bs, nb, float(scale), _int32(window, "window"),
-        workspace.data_ptr(), ws_bytes, _ptr(dev_status), raw), "pkv_paged_attention_decode_fp4")
+        workspace, 0 if given else lib.pkv_decode_spec_workspace_size(B, Q, H, hkv, d), dev, stream=stream)
+    code = lib.pkv_paged_attention_decode_fp4(
+        out.data_ptr(), PKV_F32 if out.dtype is torch.float32 else PKV_BF16, _ptr(lse), q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), width, seq_lens.data_ptr(), B, Q, H, hkv, d, bs, nb, float(scale),
+        _int32(window, "window"), workspace.data_ptr(), ws_bytes, _ptr(dev_status), raw)
+    if code < 0:
+        if given:
+            workspace_buffer(workspace, lib.pkv_decode_spec_workspace_size(B, Q, H, hkv, d), dev)
+        check(code, "pkv_paged_attention_decode_fp4")
     return out
 
 
@@ -1099,7 +1122,7 @@ def accumulate_attention_weights(weights, q, lse, k_cache, block_table, seq_lens
         nb, bs, hkv, dk = _cache_dims(k_cache, "k_cache")
         _check_gpu(index, k_cache=k_cache)
     elif isinstance(k_scale, torch.Tensor) and k_scale.dtype == torch.uint8:
-        nb, hkv, bs, at = _fp4_cache(k_cache, None, k_scale, None)
+        nb, hkv, bs, at = _fp4_cache(k_cache, k_scale, only_k=True)
         fmt, dk = KEYS_FP4, 128
         if at != index:
             raise ValueError(f"k_cache is on cuda:{at}, expected cuda:{index}")
@@ -1119,7 +1142,7 @@ def accumulate_attention_weights(weights, q, lse, k_cache, block_table, seq_lens
         check_shape(lse, tuple(rows), "lse")
         check_shape(weights, (nb, hkv, bs), "weights")
         _check_gpu(index, weights=weights, lse=lse)
-    _tables(index, B, block_table, seq_lens, num_fresh=num_fresh)
+    width = _tables(index, B, block_table, seq_lens, num_fresh=num_fresh)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, q.device)
@@ -1127,7 +1150,7 @@ def accumulate_attention_weights(weights, q, lse, k_cache, block_table, seq_lens
         return
     check(load().pkv_accumulate_attention_weights(
         weights.data_ptr(), q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(), _ptr(k_scale), fmt,
-        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), num_fresh.data_ptr(), B, Q,
+        block_table.data_ptr(), width, seq_lens.data_ptr(), num_fresh.data_ptr(), B, Q,
         H, hkv, d, bs, nb, float(scale), float(decay), _ptr(dev_status), raw),
         "pkv_accumulate_attention_weights")
 
@@ -1147,7 +1170,7 @@ def select_rows(weights, block_table, seq_lens, num_keep: int, num_sink: int = 0
     _dev_i32(seq_lens, "seq_lens")
     B = seq_lens.numel()
     index = weights.get_device()
-    _tables(index, B, block_table, seq_lens)
+    width = _tables(index, B, block_table, seq_lens)
     num_keep = _int32(num_keep, "num_keep")
     num_sink, num_recent = _int32(num_sink, "num_sink"), _int32(num_recent, "num_recent")
     if num_keep < 1:
@@ -1163,8 +1186,8 @@ def select_rows(weights, block_table, seq_lens, num_keep: int, num_sink: int = 0
     if dev_status is not None:
         status_buffer(dev_status, weights.device)
     check(load().pkv_select_rows(
-        out.data_ptr(), weights.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-        seq_lens.data_ptr(), B, hkv, bs, nb, num_keep, num_sink, num_recent, _ptr(dev_status), raw),
+        out.data_ptr(), weights.data_ptr(), block_table.data_ptr(), width, seq_lens.data_ptr(), B, hkv,
+        bs, nb, num_keep, num_sink, num_recent, _ptr(dev_status), raw),
         "pkv_select_rows")
     return out
 

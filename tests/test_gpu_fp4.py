@@ -466,3 +466,33 @@ def test_a_write_of_no_rows_takes_any_strides():
     api.kv_cache_write_fp4(*cache, none, none, ints([]))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(cache, before))
+
+
+def test_binding_refuses_wrong_buffers():
+    b = Batch(90, [300, 20], 8, 2, 1)
+    args = b.args()
+    q, kc, vc, ks, vs, table, lens = args
+    need = api.decode_spec_workspace_size(2, 1, 8, 2, D)
+
+    def refused(match, *positional, **kw):
+        with pytest.raises(ValueError, match=match):
+            api.paged_attention_decode_fp4(*(positional or args), 0.09, **kw)
+
+    refused(f"needs {need}", workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    refused("workspace must be contiguous", workspace=torch.empty((need, 2), dtype=torch.uint8, device="cuda")[:, 0])
+    refused("v_cache", q, kc, None, ks, vs, table, lens)
+    refused("v_scale", q, kc, vc, ks, None, table, lens)
+    refused("v_cache", q, kc, vc[:1].contiguous(), ks, vs, table, lens)
+    refused("k_scale", q, kc, vc, ks[..., :4].contiguous(), vs, table, lens)
+    refused("k_cache", q, kc[0], vc, ks, vs, table, lens)
+    refused("block_table", q, kc, vc, ks, vs, table[:1], lens)
+    refused("block_table", q, kc, vc, ks, vs, table[0], lens)
+    refused("seq_lens", q, kc, vc, ks, vs, table, lens.long())
+    refused("seq_lens", q, kc, vc, ks, vs, table, lens[:1])
+    refused("lse", lse=torch.empty((2, 8), dtype=torch.float64, device="cuda"))
+    refused("out", out=torch.empty((2, 8, 64), device="cuda"))
+    for call in (lambda: api.kv_cache_read_fp4(kc, vc, ks, None, ints([0])),
+                 lambda: api.select_rows(torch.zeros((4, 2, BS), device="cuda"), table.long(), lens, 5),
+                 lambda: api.select_rows(torch.zeros((4, 2, BS), device="cuda"), table[:1], lens, 5)):
+        with pytest.raises(ValueError):
+            call()
