@@ -824,7 +824,8 @@ def kv_cache_write_fp4(k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, d
     vh, vs = _rope_rows(v, T, 128, "v")
     if kh != hkv or vh != hkv:
         raise ValueError(f"k and v must have the cache's {hkv} heads")
-    _check_gpu(index, k=k, v=v, slot_mapping=slot_mapping)
+    if not (k.get_device() == index and v.get_device() == index and slot_mapping.get_device() == index):
+        _check_gpu(index, k=k, v=v, slot_mapping=slot_mapping)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, k_cache.device)
@@ -851,7 +852,8 @@ def kv_cache_read_fp4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out=No
             _dev_bf16(t, n)
             check_shape(t, shape, n)
         _check_gpu(index, k_out=k_out, v_out=v_out)
-    _check_gpu(index, slot_mapping=slot_mapping)
+    if slot_mapping.get_device() != index:
+        _check_gpu(index, slot_mapping=slot_mapping)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, k_cache.device)
