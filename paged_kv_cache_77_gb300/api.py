@@ -8,7 +8,6 @@ fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes as C
-import math
 from array import array
 
 import numpy as np
@@ -1212,12 +1211,16 @@ def compact_rows(kept, block_table, row_caches=(), head_caches=(), new_block_tab
     B, hkv, K = kept.shape
     if K < 1:
         raise ValueError("num_keep must be positive")
+    index = kept.get_device()
     nb = bs = None
     data, sizes = [], []
+    by_row_until = len(row_caches)
     for i, t in enumerate(caches):
         if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
             raise ValueError(f"cache {i} must be a contiguous CUDA tensor")
-        by_row = i < len(row_caches)
+        if t.get_device() != index:
+            raise ValueError(f"cache {i} is on {t.device}, expected cuda:{index}")
+        by_row = i < by_row_until
         shape = t.shape
         if len(shape) < 3 or shape[2 if by_row else 1] != hkv:
             order = "[nb, bs, H_kv, ...]" if by_row else "[nb, H_kv, bs, ...]"
@@ -1226,11 +1229,12 @@ def compact_rows(kept, block_table, row_caches=(), head_caches=(), new_block_tab
         here = shape[0], shape[1 if by_row else 2]
         if nb is None:
             nb, bs = here
+            heads = max(1, nb * bs * hkv)
         elif here != (nb, bs):
             raise ValueError(f"cache {i} has {here[0]} blocks of {here[1]}, the first one {nb} of {bs}")
         data.append(t.data_ptr())
         # Bytes of one head's row (strides of axes of length one say nothing).
-        sizes.append(math.prod(shape[3:]) * t.element_size())
+        sizes.append(t.numel() // heads * t.element_size())
     _dev_i32(block_table, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be [B={B}, max_blocks_per_seq], "
@@ -1244,16 +1248,13 @@ def compact_rows(kept, block_table, row_caches=(), head_caches=(), new_block_tab
         width = new_block_table.shape[1]
         if B and K > width * bs:
             raise ValueError(f"{K} rows do not fit in new_block_table's {width} blocks of {bs}")
-    index = kept.get_device()
-    _check_gpu(index, block_table=block_table, new_block_table=new_block_table)
-    for i, t in enumerate(caches):
-        if t.get_device() != index:
-            raise ValueError(f"cache {i} is on {t.device}, expected cuda:{index}")
+    if block_table.get_device() != index or new_block_table is not None:
+        _check_gpu(index, block_table=block_table, new_block_table=new_block_table)
     raw = _launch_stream(index, stream)
     if dev_status is not None:
         status_buffer(dev_status, kept.device)
     ptrs, rows = array("Q", data), array("i", sizes)
-    major = array("i", [0] * len(row_caches) + [1] * len(head_caches))
+    major = array("i", [0] * by_row_until + [1] * (len(caches) - by_row_until))
     check(load().pkv_compact_rows(
         ptrs.buffer_info()[0], rows.buffer_info()[0], major.buffer_info()[0], len(caches),
         kept.data_ptr(), K, block_table.data_ptr(), block_table.shape[1], _ptr(new_block_table), width,
