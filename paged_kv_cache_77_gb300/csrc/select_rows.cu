@@ -37,9 +37,8 @@ namespace cg = cooperative_groups;
 namespace pkv {
 namespace {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32, BS = 128, BINS = 2048;
+constexpr int BS = 128, BINS = 2048, MAX_WARPS = 16;
 constexpr int FLIGHT = 2;        // blocks of a warp in flight while as many are worked on
-constexpr int LIST = 5120;       // rows of a CTA inside the bracket
 constexpr int SHORT = 1024;      // rows of a CTA that need no bracket
 constexpr int MAX_CLUSTER = 8;
 constexpr int MAX_PER_CTA = 4096;  // blocks of a CTA, whose masks take 128 KB
@@ -63,7 +62,7 @@ __device__ __forceinline__ uint4 weight_keys(uint4 w) {
 
 struct Shared {
   int hist[2][BINS];
-  int wsum[WARPS], wabove[WARPS], wequal[WARPS];
+  int wsum[MAX_WARPS], wabove[MAX_WARPS], wequal[MAX_WARPS];
   int bin[2], rest, all, total;          // what a scan found
   int above, inside;                     // of this CTA: rows above the bracket, rows in the list
   int taken, equal;                      // rows taken without ties, rows of the border's weight
@@ -75,8 +74,8 @@ struct Shared {
 struct Lists {
   uint4 *take, *other;
   uint32_t *key, *place;
-  __device__ __forceinline__ Lists(uint4* base, int blocks)
-      : take(base), other(take + blocks), key(reinterpret_cast<uint32_t*>(other + blocks)), place(key + LIST) {}
+  __device__ __forceinline__ Lists(uint4* base, int blocks, int rows)
+      : take(base), other(take + blocks), key(reinterpret_cast<uint32_t*>(other + blocks)), place(key + rows) {}
 };
 
 // Bits 0 to 7 of x as bits 0, 4, .. 28.
@@ -92,7 +91,11 @@ __device__ __forceinline__ uint32_t in_order(uint4 m, int t) {
 }
 __device__ __forceinline__ int size(uint4 m) { return __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w); }
 
-__global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_constant__ SelectRowsArgs a, int cta_blocks) {
+// LIST: rows of a CTA inside the bracket.
+template <int THREADS, int LIST, int RESIDENT>
+__global__ void __launch_bounds__(THREADS, RESIDENT)
+    select_rows_kernel(const __grid_constant__ SelectRowsArgs a, int cta_blocks) {
+  constexpr int WARPS = THREADS / 32;
   __shared__ __align__(16) Shared sh;
   extern __shared__ __align__(16) uint4 dynamic[];
   pdl_wait_then_launch();
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
     else
       cg::this_cluster().sync();
   };
-  const Lists list(dynamic, cta_blocks);
+  const Lists list(dynamic, cta_blocks, LIST);
 
   // This warp's blocks: `count` from `first` on; their masks begin at the own-th of the CTA's.
   const int blocks = (hi + BS - 1) / BS, per = (blocks + C * WARPS - 1) / (C * WARPS);
@@ -524,25 +527,17 @@ __global__ void __launch_bounds__(THREADS, 3) select_rows_kernel(const __grid_co
   if (C > 1) sync();  // no CTA goes while another may read its shared memory
 }
 
-}  // namespace
-
-cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int num_sms) {
-  const int64_t rows = (int64_t)a.B * a.Hkv;
-  // Cluster width: room for the rows inside the bracket (some 13 % of 256 blocks), and CTAs for every
-  // SM where the rows are few, of four blocks a warp or more. Measured on GB300 with wider and narrower
-  // clusters (us for 1, 2, 4, 8 CTAs a row): 8 rows of 256 blocks 15.5, 12.9, 12.6, 15.9; 64 of 64 10.2,
-  // 12.5, 20, 42; 512 of up to 256 31, 44, 83, 258; 128 of up to 1,024 145 (the lists overflow), 46, 46,
-  // 94; 16 of 8,192 535, 535, 285, 68, with 16 CTAs 98.
-  int C = 1;
-  while (C < MAX_CLUSTER && (a.max_blocks > 256 * C || (a.max_blocks > 4 * WARPS * C && rows * 2 * C <= num_sms)))
-    C *= 2;
+template <int THREADS, int LIST, int RESIDENT>
+cudaError_t launch(const SelectRowsArgs& a, int C, cudaStream_t stream) {
+  constexpr int WARPS = THREADS / 32;
+  const auto kernel = select_rows_kernel<THREADS, LIST, RESIDENT>;
   const int cta_blocks = (a.max_blocks + C * WARPS - 1) / (C * WARPS) * WARPS;
   const size_t smem = (size_t)cta_blocks * 2 * sizeof(uint4) + LIST * 8;
-  const cudaError_t e = cudaFuncSetAttribute(select_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              MAX_PER_CTA * 2 * (int)sizeof(uint4) + LIST * 8);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * C));
+  cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * C));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -555,7 +550,28 @@ cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_rows_kernel, a, cta_blocks);
+  return cudaLaunchKernelEx(&cfg, kernel, a, cta_blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int num_sms) {
+  const int64_t rows = (int64_t)a.B * a.Hkv;
+  // Cluster width: room for the rows inside the bracket (some 13 % of 256 blocks), and CTAs for every
+  // SM where the rows are few, of four blocks a warp or more. Measured on GB300 with wider and narrower
+  // clusters (us for 1, 2, 4, 8 CTAs a row): 8 rows of 256 blocks 15.5, 12.9, 12.6, 15.9; 64 of 64 10.2,
+  // 12.5, 20, 42; 512 of up to 256 31, 44, 83, 258; 128 of up to 1,024 145 (the lists overflow), 46, 46,
+  // 94; 16 of 8,192 535, 535, 285, 68, with 16 CTAs 98.
+  int C = 1;
+  while (C < MAX_CLUSTER && (a.max_blocks > 256 * C || (a.max_blocks > 64 * C && rows * 2 * C <= num_sms)))
+    C *= 2;
+  // Much of a CTA's work does not depend on the row's length, so short rows take fewer warps, and more CTAs to
+  // an SM. Measured on GB300 (us with 512 threads, 256, 128): 512 rows of up to 512 weights 11.1, 8.2, 9.2, of
+  // 4,096 14.4, 12.7, 14.3, of 16,384 20.2, 20.4, 26.5; 4,096 rows of up to 512 69, 40, 34, of 4,096 105, 80, 67;
+  // 2,048 rows of up to 8,192 53, 39, 37, of 16,384 97, 89, 131; 160 rows of 4,096 8.6, 9.0, 10.3.
+  if (C == 1 && a.max_blocks <= 32 && rows > 4 * num_sms) return launch<128, 2048, 8>(a, 1, stream);
+  if (C == 1 && a.max_blocks <= 128 && rows > 2 * num_sms) return launch<256, 3584, 4>(a, 1, stream);
+  return launch<512, 5120, 3>(a, C, stream);
 }
 
 }  // namespace pkv

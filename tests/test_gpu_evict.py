@@ -622,3 +622,36 @@ def test_two_evictions_at_once():
         torch.cuda.synchronize()
         for job, want in zip(jobs, alone):
             assert all(torch.equal(a, b) for a, b in zip(job[0], want))
+
+
+@pytest.mark.parametrize("kind", ["spread", "few", "one", "special", "close", "descending", "zeros"])
+@pytest.mark.parametrize("per_sm,longest,keep,sink,recent", [(4, 4096, 500, 4, 100), (4, 4096, 2048, 0, 0), (4, 700, 1, 0, 0),
+                                                             (2, 16384, 900, 1, 32), (2, 5000, 2500, 0, 7)])
+def test_select_rows_of_many_short_sequences(kind, per_sm, longest, keep, sink, recent):
+    """Enough rows for every kernel that takes short ones, against numpy's sort."""
+    hkv = 8
+    B = per_sm * torch.cuda.get_device_properties(0).multi_processor_count // hkv + 4
+    rng = np.random.default_rng(longest + keep)
+    lens = [longest, 0, keep, keep + 1, max(1, longest - 1)] + [int(n) for n in rng.integers(0, longest + 1, B - 5)]
+    table, nb = make_table(rng, lens)
+    w = _weights(rng, kind, nb, hkv)
+    if kind == "descending":
+        w[:] = -np.arange(BS) - BS * rng.permutation(nb)[:, None, None]
+    elif kind == "zeros":
+        w = np.where(rng.random(w.shape) < 0.01, rng.random(w.shape), 0.0).astype(np.float32)
+    st = status()
+    kept = api.select_rows(torch.as_tensor(np.ascontiguousarray(w)).cuda(), ints(table), ints(lens), keep, sink,
+                           recent, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    got = kept.cpu().numpy()
+    for b, m in enumerate(lens):
+        rows = w[table[b, :-(-m // BS)]].transpose(1, 0, 2).reshape(hkv, -1)[:, :m]
+        for g in range(hkv):
+            row = rows[g]
+            rank = np.where(np.isnan(row), 1, 2)
+            rank[:sink] = rank[max(0, m - recent):] = 0
+            weight = np.where(rank == 2, row, 0.0)
+            want = np.sort(np.lexsort((np.arange(m), -weight, rank))[:keep])
+            np.testing.assert_array_equal(got[b, g, :len(want)], want)
+            assert (got[b, g, len(want):] == -1).all()
