@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(Args a) {
     }
   };
   const int64_t i0 = n ? cta_of_tile(base, T, G) : 0, i1 = n ? cta_of_tile(base + n - 1, T, G) : 0;
-  if (n > 0 && i0 == i1) return;  // finished by the attention kernel
+  const bool finished = n > 0 && i0 == i1;  // by the attention kernel
   // The pieces' workspace slots, found before the wait (they depend on the inputs
   // only), so that after it every piece's loads are issued at once.
   constexpr int kMaxPieces = 8;
@@ -306,7 +306,10 @@ __global__ void __launch_bounds__(512) decode_merge_kernel(Args a) {
     if (np < kMaxPieces) slots[np] = slot_of(i);
     ++np;
   }
-  pdl_wait_primary();
+  // The launch behind waits for this grid alone, and the attention kernel let this grid start before its own
+  // end: the first block waits even where there is nothing to merge, so that the grid never ends first.
+  if (!finished || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait_primary();
+  if (finished) return;
   if (n == 0) {
     put(make_float4(0.f, 0.f, 0.f, 0.f));
     if (a.lse && lane == 0) a.lse[row] = -INFINITY;
