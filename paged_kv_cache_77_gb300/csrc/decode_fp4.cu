@@ -510,7 +510,8 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
           const int j = ahead.pos / TILE;
           if ((unsigned)(j - ids_j) >= 32u) {
             ids_j = j;
-            ids = (j + lane) * TILE < ahead.len ? __ldg(a.block_table + (int64_t)ahead.b * a.max_blocks + j + lane) : 0;
+            // (Counted in blocks: the last positions lie just below 2^31.)
+            ids = j + lane <= (ahead.len - 1) / TILE ? __ldg(a.block_table + (int64_t)ahead.b * a.max_blocks + j + lane) : 0;
           }
           const int blk = __shfl_sync(0xffffffffu, ids, j - ids_j);
           const bool ok = blk >= 0 && (int64_t)blk < a.num_blocks;

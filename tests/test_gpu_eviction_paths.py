@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import fp4_ref as f4
 from paged_kv_cache_77_gb300 import api
 from tests.test_gpu_evict import D, ints, keys_of, make_table
 
@@ -48,3 +49,49 @@ def test_weights_behind_a_decode_that_leaves_nothing_to_merge(fmt):
     for _ in range(5):
         for a, b in zip(calm, run(False)):
             assert torch.equal(a.cpu()[live], b.cpu()[live])
+
+
+# ------------------------------------------------------------------ tables as wide as positions are counted
+WIDEST = (2**31 - 1) // 128  # blocks: positions up to 2,147,483,519
+
+
+def test_decode_over_the_widest_table():
+    """2^31 - 128 tokens in a table that names four blocks again and again, the last entries its last
+    ones. Keys are zero, so every weight is equal and the sums are exact in fp32: an output is the mean of
+    the blocks' values as the cache holds them (1 as 33 / 32), the log-sum-exp the length's logarithm."""
+    cache = [torch.zeros((4, 1, 128, w), dtype=torch.uint8, device="cuda") for w in (64, 64, 8, 8)]
+    v = torch.arange(4, dtype=torch.bfloat16, device="cuda").repeat_interleave(128).view(512, 1, 1).expand(512, 1, D)
+    api.kv_cache_write_fp4(*cache, torch.zeros_like(v).contiguous(), v.contiguous(), ints(np.arange(512)))
+    table = torch.arange(WIDEST, dtype=torch.int32, device="cuda").remainder_(4).view(1, WIDEST)
+    q = torch.ones((1, 8, D), dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lse = torch.zeros((1, 8), device="cuda")
+    out = api.paged_attention_decode_fp4(q, *cache, table, ints([WIDEST * 128]), 0.09, lse=lse, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    held = f4.dequantise(*f4.quantise(np.arange(4.0)[:, None].repeat(D, 1)))[:, 0]
+    mean = held @ np.bincount(np.arange(WIDEST) % 4) / WIDEST
+    # A warp's sums are multiples of 2^11 below 2^35 (exact or off by 2^-24 a step of some 27,600, each way);
+    # then 16 warps and 152 CTAs are joined.
+    assert (out.double().cpu() - mean).abs().max() <= 28000 * 2.0 ** -24 * 3
+    assert (lse.double().cpu() - np.log(WIDEST * 128.0)).abs().max() <= 28000 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_weights_over_the_widest_table(fmt):
+    """A sequence of 2^31 - 128 positions of which only the last block exists."""
+    rng = np.random.default_rng(33)
+    cache, k_scale, keys = keys_of(fmt, rng, 2, 1)
+    table = torch.full((1, WIDEST), -1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    q = torch.as_tensor(rng.standard_normal((1, 8, D)), dtype=torch.float32).to(torch.bfloat16).cuda()
+    z = 0.09 * (keys[1, :, 0] @ q[0].double().cpu().numpy().T)  # [128, 8]
+    lse = torch.full((1, 8), 3.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.zeros((2, 1, 128), device="cuda")
+    api.accumulate_attention_weights(w, q, lse, cache, table, ints([WIDEST * 128]), ints([1]), 0.09, k_scale=k_scale,
+                                     dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 2 and not w[0].any()
+    # Relative error: see the module whose helpers these are; |z| and |lse| are below 16 together.
+    np.testing.assert_allclose(w[1, 0].double().cpu().numpy(), np.exp(z - 3.0).sum(-1), rtol=1e-4)
