@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
   using K = Keys<FMT>;
   __shared__ uint4 sq[kWeightsMaxRows / 8][4][32];           // B operands
   __shared__ float sf[kWeightsMaxRows], sl[kWeightsMaxRows];  // score factor, lse (both for log2)
-  __shared__ int si[kWeightsMaxRows];                         // query token of a row
+  __shared__ int si[kWeightsMaxRows];                         // last position that a row sees
   __shared__ int64_t total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const DenseRows rows = {a.seq_lens, BS, 0, a.max_blocks * BS};
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
   fetch(cur, blk, now);
   more = cursor_next(nxt, rows, a.B, a.Hkv);
   if (more) blk1 = block_of(nxt);
-  int seg_b = -1, seg_g = -1, first = 0, fresh = 0;
+  int seg_b = -1, seg_g = -1, fresh = 0;
   for (;;) {
     const TileCursor ahead = nxt;
     const int blk_ahead = blk1;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
       __syncthreads();  // nobody reads the last segment's rows any more
       seg_b = cur.b;
       seg_g = cur.g;
-      first = cur.len - a.q_len + a.row0;  // position of the launch's first query token
+      const int first = cur.len - a.q_len + a.row0;  // position of the launch's first query token
       const int n = __ldg(a.num_fresh + cur.b);
       fresh = cur.len - (n < 0 ? 0 : n > cur.len ? cur.len : n);
       for (int n8 = warp; n8 < tiles; n8 += WARPS) {
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
         if (c == 0) {
           sf[r] = factor;
           sl[r] = r < R ? __ldg(a.lse + row) * kLog2e : 0.f;
-          si[r] = r < R ? r / a.n_rep : -(1 << 30);  // no position is that early
+          si[r] = r < R ? first + r / a.n_rep : INT32_MIN;  // (a column without a row sees none)
         }
       }
       __syncthreads();
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
           float f = sf[r];
           if constexpr (FMT == kKeysFp8) f *= __uint_as_float(now.scale[i >> 1]);
           const float p = exp2f(fmaf(s[i], f, -sl[r]));
-          const bool seen = (i < 2 ? pa : pb) <= first + si[r];
+          const bool seen = (i < 2 ? pa : pb) <= si[r];
           if (i < 2)
             wa += seen ? p : 0.f;
           else

@@ -95,3 +95,21 @@ def test_weights_over_the_widest_table(fmt):
     assert int(st) == 2 and not w[0].any()
     # Relative error: see the module whose helpers these are; |z| and |lse| are below 16 together.
     np.testing.assert_allclose(w[1, 0].double().cpu().numpy(), np.exp(z - 3.0).sum(-1), rtol=1e-4)
+
+
+@pytest.mark.parametrize("fmt,H,Q", [("bf16", 1, 1), ("bf16", 3, 4), ("fp8", 5, 4), ("fp4", 5, 4)])
+def test_first_weights_of_the_widest_table(fmt, H, Q):
+    """The same with the first block alone, for query rows that do not fill the products' 8 columns: what
+    fills them counts for nothing, however far the last position is."""
+    rng = np.random.default_rng(34)
+    cache, k_scale, keys = keys_of(fmt, rng, 2, 1)
+    table = torch.full((1, WIDEST), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = 1
+    q = torch.as_tensor(rng.standard_normal((1, Q, H, D)), dtype=torch.float32).to(torch.bfloat16).cuda()
+    z = 0.09 * (keys[1, :, 0] @ q.double().cpu().numpy().reshape(Q * H, D).T)
+    lse = torch.full((1, Q, H), 3.0, device="cuda")
+    w = torch.zeros((2, 1, 128), device="cuda")
+    api.accumulate_attention_weights(w, q, lse, cache, table, ints([WIDEST * 128]), ints([1]), 0.09, k_scale=k_scale)
+    torch.cuda.synchronize()
+    assert not w[0].any()
+    np.testing.assert_allclose(w[1, 0].double().cpu().numpy(), np.exp(z - 3.0).sum(-1), rtol=1e-4)
