@@ -5,7 +5,7 @@ import torch
 
 from oracle import fp4_ref as f4
 from paged_kv_cache_77_gb300 import api
-from tests.test_gpu_evict import D, ints, keys_of, make_table
+from tests.test_gpu_evict import D, check_weights, ints, keys_of, make_table
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,84 @@ def test_first_weights_of_the_widest_table(fmt, H, Q):
     torch.cuda.synchronize()
     assert not w[0].any()
     np.testing.assert_allclose(w[1, 0].double().cpu().numpy(), np.exp(z - 3.0).sum(-1), rtol=1e-4)
+
+
+# ------------------------------------------------------------------ runs of many pieces
+def reference(w0, q, lse, keys, table, lens, fresh, scale, decay):
+    """Sums after a step and the reach of their scores (see test_gpu_evict.py), a sequence at a time in
+    float64. q [B, Q, H, d], lse [B, Q, H], keys [nb, 128, H_kv, d]; entries outside the cache are skipped."""
+    out, reach = w0.astype(np.float64), np.zeros(w0.shape)
+    nb, hkv = w0.shape[:2]
+    B, Q, H, _ = q.shape
+    for b, n in enumerate(lens):
+        p = np.arange(n)
+        blk = table[b, p // 128]
+        p, blk = p[(blk >= 0) & (blk < nb)], blk[(blk >= 0) & (blk < nb)]
+        rows = keys[blk, p % 128]                                           # [n, H_kv, d]
+        qq = q[b].reshape(Q, hkv, H // hkv, D)
+        z = scale * np.einsum("qghd,ngd->ngqh", qq, rows)
+        mag = scale * np.einsum("qghd,ngd->ngqh", np.abs(qq), np.abs(rows)).max(axis=(2, 3))
+        seen = p[:, None] <= n - Q + np.arange(Q)                            # [n, Q]
+        e = np.exp(z - lse[b].reshape(Q, hkv, H // hkv).swapaxes(0, 1)) * seen[:, None, :, None]
+        old = np.where(p >= n - min(max(int(fresh[b]), 0), n), 0.0, decay)
+        at = blk[:, None], np.arange(hkv)[None], (p % 128)[:, None]
+        out[at] = old[:, None] * out[at] + e.sum(axis=(2, 3))
+        reach[at] = mag
+    return out, reach
+
+
+def check_step(fmt, rng, lens, H, hkv, Q, table, nb, decay=0.75, code=0):
+    cache, k_scale, keys = keys_of(fmt, rng, nb, hkv)
+    q = torch.as_tensor(rng.standard_normal((len(lens), Q, H, D)), dtype=torch.float32).to(torch.bfloat16).cuda()
+    lse = torch.as_tensor(3 + rng.random((len(lens), Q, H)), dtype=torch.float32).cuda()
+    w0 = rng.random((nb, hkv, 128)).astype(np.float32)
+    fresh = [n if b % 5 == 0 else b % 5 + Q for b, n in enumerate(lens)]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = []
+    for _ in range(2):
+        w = torch.as_tensor(w0).cuda()
+        api.accumulate_attention_weights(w, q, lse, cache, ints(table), ints(lens), ints(fresh), 0.09,
+                                         k_scale=k_scale, decay=decay, dev_status=st)
+        torch.cuda.synchronize()
+        got.append(w)
+    assert int(st) == code and torch.equal(*got)
+    l64 = lse.double().cpu().numpy()
+    want, reach = reference(w0, q.double().cpu().numpy(), l64, keys, table, lens, fresh, 0.09, decay)
+    check_weights(got[0], want, reach, l64, Q * H // hkv)
+    behind = want == w0
+    assert np.array_equal(got[0].cpu().numpy()[behind], w0[behind])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("H,Q", [(8, 1), (16, 2), (64, 1), (64, 2)])
+def test_weights_of_many_sequences(fmt, H, Q):
+    """Some fifteen blocks for every CTA: rings that are refilled, runs that pass from sequence to
+    sequence and from kv head to kv head."""
+    rng = np.random.default_rng(35)
+    lens = [int(n) for n in rng.integers(0, 1500, 90)] + [9000]
+    table, nb = make_table(rng, lens)
+    check_step(fmt, rng, lens, H, 4, Q, table, nb)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("hkv", [1, 4])
+def test_weights_of_runs_that_pass_many_blocks(fmt, hkv):
+    """A sequence of ten million positions of which 300 blocks exist: a warp's run is longer than the 32
+    table entries that it holds at a time."""
+    rng = np.random.default_rng(36)
+    width, exist = 84_000 // hkv, 300
+    at = np.sort(np.r_[rng.choice(width - 1, exist - 1, replace=False), width - 1])
+    table = np.full((1, width), -1, dtype=np.int32)
+    table[0, at] = rng.permutation(exist + 2)[:exist]
+    check_step(fmt, rng, [width * 128 - 5], 8 * hkv, hkv, 1, table, exist + 2, code=2)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("H,hkv,Q", [(16, 1, 9), (32, 2, 17), (20, 2, 14), (3, 3, 129)])
+def test_weights_of_more_rows_than_one_launch_takes(fmt, H, hkv, Q):
+    """The second launch adds to what the first one left, with no decay and no fresh start of its own,
+    whichever kernel its rows fall to."""
+    rng = np.random.default_rng(37)
+    lens = [300, 7, 0, 900, 128, 1]
+    table, nb = make_table(rng, lens)
+    check_step(fmt, rng, lens, H, hkv, Q, table, nb)
