@@ -91,7 +91,7 @@ __device__ __forceinline__ uint32_t in_order(uint4 m, int t) {
 }
 __device__ __forceinline__ int size(uint4 m) { return __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w); }
 
-// LIST: rows of a CTA inside the bracket.
+// LIST: rows of a CTA inside the bracket; RESIDENT: CTAs that an SM holds.
 template <int THREADS, int LIST, int RESIDENT>
 __global__ void __launch_bounds__(THREADS, RESIDENT)
     select_rows_kernel(const __grid_constant__ SelectRowsArgs a, int cta_blocks) {
@@ -530,6 +530,8 @@ __global__ void __launch_bounds__(THREADS, RESIDENT)
 template <int THREADS, int LIST, int RESIDENT>
 cudaError_t launch(const SelectRowsArgs& a, int C, cudaStream_t stream) {
   constexpr int WARPS = THREADS / 32;
+  static_assert(RESIDENT * (sizeof(Shared) + LIST * 8 + WARPS * 2 * sizeof(uint4) + 1024) <= 228 * 1024,
+                "RESIDENT CTAs fit an SM's shared memory, 1 KB of it reserved for each");
   const auto kernel = select_rows_kernel<THREADS, LIST, RESIDENT>;
   const int cta_blocks = (a.max_blocks + C * WARPS - 1) / (C * WARPS) * WARPS;
   const size_t smem = (size_t)cta_blocks * 2 * sizeof(uint4) + LIST * 8;
@@ -569,7 +571,7 @@ cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int
   // an SM. Measured on GB300 (us with 512 threads, 256, 128): 512 rows of up to 512 weights 11.1, 8.2, 9.2, of
   // 4,096 14.4, 12.7, 14.3, of 16,384 20.2, 20.4, 26.5; 4,096 rows of up to 512 69, 40, 34, of 4,096 105, 80, 67;
   // 2,048 rows of up to 8,192 53, 39, 37, of 16,384 97, 89, 131; 160 rows of 4,096 8.6, 9.0, 10.3.
-  if (C == 1 && a.max_blocks <= 32 && rows > 4 * num_sms) return launch<128, 2048, 8>(a, 1, stream);
+  if (C == 1 && a.max_blocks <= 32 && rows > 4 * num_sms) return launch<128, 2048, 6>(a, 1, stream);
   if (C == 1 && a.max_blocks <= 128 && rows > 2 * num_sms) return launch<256, 3584, 4>(a, 1, stream);
   return launch<512, 5120, 3>(a, C, stream);
 }
