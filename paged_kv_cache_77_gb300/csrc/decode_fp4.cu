@@ -56,7 +56,6 @@ template <int NT>
 struct Shape {
   static constexpr int WARPS = NT == 1 ? 16 : 8;
   static constexpr int STAGES = NT == 1 ? 2 : 4;
-  static constexpr int AT_ONCE = 2;  // 16-token products side by side
 };
 
 enum : int { kNothing = 0, kGoesOn = 1, kEnds = 2 };  // what a warp left of its first segment
@@ -434,7 +433,7 @@ __device__ __forceinline__ void attend(Running<NT>& r, const uint4 (&qf)[NT][4],
 
 template <int NT>
 __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(const __grid_constant__ DecodeFp4Args a) {
-  constexpr int WARPS = Shape<NT>::WARPS, STAGES = Shape<NT>::STAGES, AT_ONCE = Shape<NT>::AT_ONCE;
+  constexpr int WARPS = Shape<NT>::WARPS, STAGES = Shape<NT>::STAGES;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem<NT>& sm = *reinterpret_cast<Smem<NT>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -590,10 +589,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::WARPS, 1) decode_fp4_kernel(co
           const uint8_t *k = tile, *v = tile + CODES, *ks = tile + 2 * CODES, *vs = ks + SCALES;
           constexpr int C16 = 16 * fp4::kCodeBytes, S16 = 16 * fp4::kScaleBytes;
           if (sight.all(cur.pos, cur.pos + SUB - 1)) {
-            attend<NT, AT_ONCE, false>(r, qf, f, limit, shift, row_i, k, v, ks, vs, cur.pos, sight, g, c);
-            if (AT_ONCE == 1)
-              attend<NT, AT_ONCE, false>(r, qf, f, limit, shift, row_i, k + C16, v + C16, ks + S16, vs + S16,
-                                         cur.pos + 16, sight, g, c);
+            attend<NT, 2, false>(r, qf, f, limit, shift, row_i, k, v, ks, vs, cur.pos, sight, g, c);
           } else {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h)
