@@ -681,8 +681,8 @@ int pkv_accumulate_attention_weights(float* weights, const void* q, const float*
  * weight of it is read. Rows of a table entry outside [0, num_blocks) rank below all
  * (PKV_DEV_BAD_BLOCK); lengths past the table are clamped (PKV_DEV_BAD_LENGTH).
  *   kept [B, H_kv, num_keep] int32 (written), which may not overlap anything the call reads
- * Supported: block_size 128, num_sink + num_recent <= num_keep, max_blocks_per_seq <= 32768
- * (4,194,304 tokens). No workspace. */
+ * Supported: block_size 128, num_sink + num_recent <= num_keep <= 2^30, max_blocks_per_seq
+ * <= 32768 (4,194,304 tokens). No workspace. */
 int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_table,
                     int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t B, int32_t H_kv,
                     int32_t block_size, int64_t num_blocks, int32_t num_keep, int32_t num_sink,
@@ -701,8 +701,8 @@ int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_ta
  *     that other requests share); the new one's blocks for the kept rows must be none of those
  *     that the call reads. No block that one sequence writes may be read or written by another.
  * Entries past block_table set PKV_DEV_BAD_LENGTH, rows of a block outside [0, num_blocks)
- * PKV_DEV_BAD_BLOCK; neither is moved. Supported: row_bytes a multiple of 4 up to 65536, up to 16 caches
- * (PKV_ERR_UNSUPPORTED otherwise). Caches 16-byte aligned. No workspace. */
+ * PKV_DEV_BAD_BLOCK; neither is moved. Supported: row_bytes a multiple of 4 up to 65536, up to 16 caches,
+ * num_keep <= 2^30 (PKV_ERR_UNSUPPORTED otherwise). Caches 16-byte aligned. No workspace. */
 int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_t* head_major,
                      int32_t num_caches, const int32_t* kept, int32_t num_keep,
                      const int32_t* block_table, int32_t max_blocks_per_seq,

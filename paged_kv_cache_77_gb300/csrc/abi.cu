@@ -731,6 +731,7 @@ int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_ta
   PKV_REQUIRE(block_size == 128, PKV_ERR_UNSUPPORTED, "%s: only block_size 128 is implemented", what);
   PKV_REQUIRE((int64_t)num_sink + num_recent <= num_keep, PKV_ERR_INVALID_ARG,
               "%s: num_sink + num_recent exceeds num_keep", what);
+  PKV_REQUIRE(num_keep <= kMaxKept, PKV_ERR_UNSUPPORTED, "%s: num_keep exceeds %d", what, kMaxKept);
   PKV_REQUIRE(max_blocks_per_seq <= kSelectRowsMaxBlocks, PKV_ERR_UNSUPPORTED,
               "%s: max_blocks_per_seq exceeds %d", what, kSelectRowsMaxBlocks);
   PKV_REQUIRE(num_blocks * block_size <= INT32_MAX && B <= INT32_MAX / 8 / H_kv, PKV_ERR_UNSUPPORTED,
@@ -762,6 +763,7 @@ int pkv_compact_rows(void* const* caches, const int32_t* row_bytes, const int32_
               PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
   PKV_REQUIRE(num_caches <= kCompactMaxCaches, PKV_ERR_UNSUPPORTED, "%s: more than %d caches", what,
               kCompactMaxCaches);
+  PKV_REQUIRE(num_keep <= kMaxKept, PKV_ERR_UNSUPPORTED, "%s: num_keep exceeds %d", what, kMaxKept);
   PKV_REQUIRE(num_blocks * block_size <= INT32_MAX && B <= INT32_MAX / H_kv, PKV_ERR_UNSUPPORTED,
               "%s: num_blocks * block_size and B * H_kv must fit in int32", what);
   PKV_REQUIRE(!new_block_table || (new_max_blocks_per_seq > 0 &&

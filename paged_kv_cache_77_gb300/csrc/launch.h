@@ -116,6 +116,7 @@ struct WeightsArgs {
 cudaError_t launch_attn_weights(WeightsArgs a, int format, cudaStream_t stream, int num_sms);
 
 // Eviction (select_rows.cu, compact_rows.cu).
+constexpr int kMaxKept = 1 << 30;  // entries of a list: the kernels' strides past its end stay below 2^31
 constexpr int kSelectRowsMaxBlocks = 32768;  // widest table of a choice of rows: four million tokens
 struct SelectRowsArgs {
   const float* weights;       // [nb, Hkv, bs]
