@@ -3,8 +3,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import evict_ref as ev
 from oracle import fp4_ref as f4
 from paged_kv_cache_77_gb300 import api
+from paged_kv_cache_77_gb300._lib import PagedKVError
 from tests.test_gpu_evict import D, check_weights, ints, keys_of, make_table
 
 pytestmark = pytest.mark.gpu
@@ -194,3 +196,75 @@ def test_weights_of_more_rows_than_one_launch_takes(fmt, H, hkv, Q):
     lens = [300, 7, 0, 900, 128, 1]
     table, nb = make_table(rng, lens)
     check_step(fmt, rng, lens, H, hkv, Q, table, nb)
+
+
+# ------------------------------------------------------------------ selections and moves at their limits
+@pytest.mark.parametrize("kind", ["spread", "narrow", "levels"])
+@pytest.mark.parametrize("n,keep,sink,recent", [(4_194_304, 300_000, 4, 100), (4_194_303, 4_194_300, 0, 2),
+                                                (3_999_000, 1, 0, 0)])
+def test_selection_from_the_longest_sequence(kind, n, keep, sink, recent):
+    """The widest table of a selection, against numpy's stable sort."""
+    rng = np.random.default_rng(keep)
+    nb = 32768
+    table = rng.permutation(nb).astype(np.int32)[None]
+    if kind == "spread":
+        w = np.exp(2.5 * rng.standard_normal((nb, 1, 128)) - 8).astype(np.float32)
+    elif kind == "narrow":  # all in one bin of the selection's first digit
+        w = (1.0 + 0.1 * rng.random((nb, 1, 128))).astype(np.float32)
+    else:
+        w = rng.integers(0, 5, (nb, 1, 128)).astype(np.float32)
+    kept = api.select_rows(torch.as_tensor(w).cuda(), ints(table), ints([n]), keep, sink, recent)
+    torch.cuda.synchronize()
+    row = w[table[0], 0].reshape(-1)[:n]
+    always = np.r_[0:sink, n - recent:n]
+    ranked = np.arange(sink, n - recent)
+    best = ranked[np.argsort(-row[ranked], kind="stable")[:keep - sink - recent]]
+    np.testing.assert_array_equal(kept.cpu().numpy()[0, 0], np.sort(np.r_[always, best]))
+
+
+@pytest.mark.parametrize("kind", ["narrow", "uniform"])
+@pytest.mark.parametrize("B,width", [(3, 2048), (70, 300)])
+def test_selection_behind_a_table_wider_than_its_rows(kind, B, width):
+    """Clusters by the table's width, rows of a few blocks: most of a cluster's CTAs have none."""
+    rng = np.random.default_rng(B)
+    lens = [0, 128, 1] + [int(n) for n in rng.integers(1, 3000, B - 3)]
+    table, nb = make_table(rng, lens, width=width)
+    w = (rng.random((nb, 2, 128)) * (0.01 if kind == "narrow" else 1.0) + 1.0 * (kind == "narrow")).astype(np.float32)
+    kept = api.select_rows(torch.as_tensor(w).cuda(), ints(table), ints(lens), 100, 1, 5).cpu().numpy()
+    for b, n in enumerate(lens):
+        for g in range(2):
+            row = w[table[b, :-(-n // 128)], g].reshape(-1)[:n]
+            want = np.arange(n)
+            if n > 100:
+                mid = np.arange(1, n - 5)
+                want = np.sort(np.r_[0, n - 5:n, mid[np.argsort(-row[mid], kind="stable")[:94]]])
+            np.testing.assert_array_equal(kept[b, g, :len(want)], want)
+            assert (kept[b, g, len(want):] == -1).all()
+
+
+@pytest.mark.parametrize("own_blocks", [False, True])
+def test_moves_of_sixteen_caches_and_of_the_longest_rows(own_blocks):
+    rng = np.random.default_rng(41)
+    lens, hkv, keep = [400, 129], 2, 150
+    table, nb = make_table(rng, lens, nb_more=5)
+    new = None
+    if own_blocks:
+        new = rng.permutation(np.setdiff1d(np.arange(nb), table))[:4].reshape(2, 2).astype(np.int32)
+    kept = np.full((2, hkv, keep), -1, dtype=np.int32)
+    for b, n in enumerate(lens):
+        for g in range(hkv):
+            m = min(n, keep)
+            kept[b, g, :m] = np.sort(rng.choice(n, m, replace=False))
+    widths = [16384, 16383, 1026, 257, 1, 2, 3, 5]  # of 4 bytes
+    row = [torch.as_tensor(rng.integers(0, 2**31, (nb, 128, hkv, x), dtype=np.int32)).cuda() for x in widths]
+    head = [torch.as_tensor(rng.integers(0, 2**31, (nb, hkv, 128, x), dtype=np.int32)).cuda() for x in widths]
+    before = [t.cpu().numpy() for t in row + head]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.compact_rows(ints(kept), ints(table), row, head, None if new is None else ints(new), dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    for i, t in enumerate(row + head):
+        want = ev.compact(before[i], kept, table, table if new is None else new, i >= len(row))
+        assert np.array_equal(t.cpu().numpy(), want), i
+    with pytest.raises(PagedKVError, match="16 caches"):
+        api.compact_rows(ints(kept), ints(table), row, [*head, torch.zeros((nb, hkv, 128), device="cuda")])
