@@ -680,7 +680,10 @@ int pkv_accumulate_attention_weights(float* weights, const void* q, const float*
  * ranks above all. A sequence with no more than num_keep positions keeps every one, and no
  * weight of it is read. Rows of a table entry outside [0, num_blocks) rank below all
  * (PKV_DEV_BAD_BLOCK); lengths past the table are clamped (PKV_DEV_BAD_LENGTH).
- *   kept [B, H_kv, num_keep] int32 (written), which may not overlap anything the call reads
+ *   kept [B, H_kv, num_keep] int32 (written, 16-byte aligned), which may not overlap anything the
+ *     call reads
+ * max_blocks_per_seq chooses how many CTAs share a row, so the same sequences take longer behind a
+ * wider table: give it the width that the longest sequence needs.
  * Supported: block_size 128, num_sink + num_recent <= num_keep <= 2^30, max_blocks_per_seq
  * <= 32768 (4,194,304 tokens). No workspace. */
 int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_table,
@@ -691,7 +694,8 @@ int pkv_select_rows(int32_t* kept, const float* weights, const int32_t* block_ta
 /* pkv_compact_rows: in each of num_caches caches, row i of sequence b and kv head g becomes
  * what row kept[b][g][i] was, for i up to the first negative entry; afterwards the sequence has
  * that many rows and its blocks behind them can go back to the pool. Rows behind stay as they
- * were. kept[b][g] must ascend (pkv_select_rows' does).
+ * were. kept[b][g] must ascend, every entry above the one before, the negative ones behind the last
+ * (pkv_select_rows' does).
  *   caches, row_bytes, head_major: HOST arrays. A cache is [num_blocks, block_size, H_kv] rows
  *     of row_bytes (head_major 0: the bf16 and FP8 caches), or [num_blocks, H_kv, block_size]
  *     (head_major 1: the 4-bit cache, scales, weights). Caches may not overlap one another,

@@ -1163,7 +1163,8 @@ def select_rows(weights, block_table, seq_lens, num_keep: int, num_sink: int = 0
     weights [nb, H_kv, bs] fp32 (accumulate_attention_weights); returns int32
     [B, H_kv, num_keep] (`out` if given): positions, ascending, -1 behind the last of a sequence
     with fewer rows. The first num_sink and the last num_recent positions are always among
-    them."""
+    them. The table's width decides how many CTAs share a row: the same sequences take longer
+    behind a table wider than the longest of them needs."""
     _f32_dev(weights, "weights")
     if weights.dim() != 3:
         raise ValueError("weights must be [num_blocks, H_kv, block_size]")
@@ -1197,8 +1198,8 @@ def compact_rows(kept, block_table, row_caches=(), head_caches=(), new_block_tab
                  dev_status=None, stream=None) -> None:
     """Move the kept rows of each sequence and kv head to the front of the sequence, in order.
 
-    kept [B, H_kv, K] int32, ascending, negative entries behind the last (select_rows). The
-    caches are contiguous CUDA tensors of any type, row_caches [nb, bs, H_kv, ...] and
+    kept [B, H_kv, K] int32, every entry above the one before, negative entries behind the last
+    (select_rows). The caches are contiguous CUDA tensors of any type, row_caches [nb, bs, H_kv, ...] and
     head_caches [nb, H_kv, bs, ...]; row i becomes what row kept[i] was, in place or, with
     new_block_table [B, blocks], in that table's blocks. The sequence then has as many rows as
     were kept; rows behind them stay as they were."""

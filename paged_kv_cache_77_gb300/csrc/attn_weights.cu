@@ -11,13 +11,15 @@
 //     head, block) tiles; each of its 8 warps takes 16 tokens of a tile straight from global memory
 //     into the registers of the A operand (the next tile's while it works on this one), 8 query rows
 //     at a time are the columns of B, from shared memory. bf16 keys of one decode step run at the
-//     memory's rate (64 sequences of up to 32,768 tokens, 64 / 8 heads: 325 us, 97 % of the copy rate),
-//     those of an observation window at the matrix instructions' (4 x 8,192 tokens, 32 rows of 8
-//     heads: 71 us);
+//     memory's rate (64 sequences of up to 32,768 tokens, 64 / 8 heads: 324 to 332 us, 95 to 98 % of the
+//     copy rate). Those of an observation window are bound by latency: 4 x 8,192 tokens, 32 rows of 8
+//     heads, two launches of 128 rows each, 69 us where the keys' bytes take 10; 16 warps an SM wait for
+//     their products, for B operands (shared memory 59 % busy) and for exponentials in turn (tensor pipe
+//     34 %, issue slots 34 %, exponential unit 9 %);
 //   - FP8 and 4-bit keys with up to 16 rows, which are bound by instructions: every warp has a run
 //     of its own, in pieces of 32 tokens through a ring in shared memory, the queries in registers
-//     (the same batch over FP8 keys 239 us with the first kernel and 203 with this one, 83 % of the copy
-//     rate; over 4-bit keys 253 and 108 us, 89 %).
+//     (the same batch over FP8 keys 239 us with the first kernel and 187 to 206 with this one, 82 to 89 %
+//     of the copy rate; over 4-bit keys 253 and 108 us, 89 %).
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"

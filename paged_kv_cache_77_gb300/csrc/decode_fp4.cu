@@ -26,7 +26,7 @@
 //
 // Roofline: HBM; 144 bytes per token and kv head. Measured on GB300: 64 sequences of up to 32,768
 // tokens, 64 / 8 heads (1.16 GB) 192 us, 89 % of the copy rate, 301 warp instructions per 16 tokens and
-// kv head, issue slots 65 % busy. Before: the warps of a CTA on one tile, joined at each segment's end
+// kv head, issue slots 68 % busy. Before: the warps of a CTA on one tile, joined at each segment's end
 // through shared memory, 368 us (a segment's end cost 6 us, and 64 sequences of up to 2,048 tokens 78 us
 // instead of 25); warps with runs of their own 267; an unmasked path 216; copies that need no barrier
 // 194. More than 8 query rows per kv head are bound by instructions: 16 rows 56 % of the copy rate.
@@ -653,7 +653,8 @@ cudaError_t launch_decode_fp4(DecodeFp4Args a, cudaStream_t stream) {
   // joins in memory cost more than the SMs left idle. Measured on GB300 (us shared out, and a CTA each):
   // 64 pairs of up to 512 tokens 10.5, 7.1, 2,048 11.4, 9.5, 4,096 13.4, 13.6, all of 4,096 17.2, 19.8; 128 of
   // 2,048 17.7, 13.2; 8 of up to 2,048 10.6, 8.9; 1 of 2,048 10.9, 12.5; 256 of up to 128 9.5, 12.7. With 16
-  // rows: 64 pairs of up to 1,024 tokens 13.8, 11.2, 2,048 13.9, 16.6.
+  // rows: 64 pairs of up to 1,024 tokens 13.8, 11.2, 2,048 13.9, 16.6. The host knows the table's width, not the
+  // lengths: behind a wider table short sequences are shared out.
   const int most = a.q_total < per ? a.q_total : per;
   a.whole = a.max_blocks <= (most * a.n_rep <= 8 ? 16 : 8) && a.B * a.Hkv <= a.num_ctas;
   for (a.row0 = 0; a.row0 < a.q_total; a.row0 += per) {

@@ -12,8 +12,12 @@
 //   - the border is found in the list digit by digit, a histogram and a scan from the top each;
 //   - the list's rows above it enter the first mask, those that equal it a mask of their own, of
 //     which the lowest positions are taken; every lane writes the positions of words of the masks.
-// Where the bracket misses, or the list overflows (weights of few different values), all of it is
-// done again with every digit over all weights, read from L2 each time.
+// Where the bracket misses, or the list overflows, all of it is done again with every digit over all
+// weights, read from L2 each time. The bracket is a digit wide at least, a quarter of an octave, so the list
+// overflows where many weights lie that close together: few different values, but sums of a narrow
+// spread too. Measured on GB300, 512 rows of up to 32,768 weights, 4,096 kept: lognormal weights with a
+// spread of 2.5 30 us, of 0.3 81, uniform ones 89, sums of 128 steps and 8 heads of independent normal
+// scores 89; 16 rows of a million 62, 228, 229, 228; 512 rows of up to 8,192 17, 16, 16, 29.
 //
 // A row (sequence, kv head) is the work of a cluster of 1 to 8 CTAs, each with its own run of
 // blocks, list and histograms; every CTA sums the histograms of the cluster for itself through
@@ -563,7 +567,9 @@ cudaError_t launch_select_rows(const SelectRowsArgs& a, cudaStream_t stream, int
   // SM where the rows are few, of four blocks a warp or more. Measured on GB300 with wider and narrower
   // clusters (us for 1, 2, 4, 8 CTAs a row): 8 rows of 256 blocks 15.5, 12.9, 12.6, 15.9; 64 of 64 10.2,
   // 12.5, 20, 42; 512 of up to 256 31, 44, 83, 258; 128 of up to 1,024 145 (the lists overflow), 46, 46,
-  // 94; 16 of 8,192 535, 535, 285, 68, with 16 CTAs 98.
+  // 94; 16 of 8,192 535, 535, 285, 68, with 16 CTAs 98. The host knows the table's width, not the lengths: the 512
+  // rows of up to 256 blocks take 30 us behind a table of 256, 43 behind 512, 80 behind 1,024, 249 behind 2,048,
+  // 270 behind 8,192 and 448 behind 32,768; 512 rows of up to 32 blocks 13, 30, 64, 220, 240 and 389.
   int C = 1;
   while (C < MAX_CLUSTER && (a.max_blocks > 256 * C || (a.max_blocks > 64 * C && rows * 2 * C <= num_sms)))
     C *= 2;
